@@ -313,6 +313,173 @@ fa_status fa_backward_varlen(const void *Q, const void *K, const void *V, const 
 /* Workspace bytes fa_backward_varlen needs (0 for invalid sizes). */
 size_t fa_backward_varlen_workspace_bytes(int64_t B, int64_t H, int64_t total_q);
 
+/*
+ * ---- Queries and keys on their way to attention: per-head norm, rotary positions,
+ * and the paged K/V cache of a serving loop.
+ *
+ * The calls below take descriptors, plain structs that the caller fills once and
+ * keeps; the library reads them during the call only.
+ */
+
+/* A (batch, head, token, d) tensor: `data` is the element (0, 0, 0, 0) and the three
+ * strides count elements; d is contiguous. Device memory, 16-byte aligned, every
+ * stride a multiple of 8 elements and >= 0. data = NULL: the tensor is not there. */
+typedef struct {
+    void *data;
+    int64_t batch, head, token;
+} fa_rows;
+
+typedef enum {
+    FA_ROPE_HALF = 0,       /* pairs (j, j + rotary_dim / 2) */
+    FA_ROPE_INTERLEAVED = 1 /* pairs (2 j, 2 j + 1) */
+} fa_rope_layout;
+
+/*
+ * What happens to a row x of d elements (one head of one token) at position p, the
+ * norm first and the rotation second, all in float32 with one rounding at the end:
+ *     n_i = x_i * w_i / sqrt( (x_0^2 + .. + x_{d-1}^2) / d + eps )   (n = x without a weight)
+ *     (y_a, y_b) = magnitude * (n_a cos(p f_j) - n_b sin(p f_j),
+ *                               n_b cos(p f_j) + n_a sin(p f_j))     for pair j = (a, b)
+ *     y_i = n_i                                                      for i >= rotary_dim
+ * steps: device memory, rotary_dim / 2 entries, the frequencies f_j as fa_rope_steps
+ * writes them; 16-byte aligned. rotary_dim: even, 0 .. d (0: no rotation, steps unused).
+ * layout: see fa_rope_layout. magnitude: finite (scalings for long contexts use one; else 1).
+ * q_weight, k_weight: device memory, d elements of the call's dtype, 16-byte aligned;
+ * NULL: queries (keys) are not normalised. eps: >= 0, finite.
+ */
+typedef struct {
+    const uint64_t *steps;
+    int64_t rotary_dim;
+    fa_rope_layout layout;
+    float magnitude;
+    const void *q_weight, *k_weight;
+    float eps;
+} fa_norm_rope;
+
+/*
+ * fa_rope_steps -- the frequencies of n rotary pairs (radians per position) as
+ * fractions of a turn in 64-bit fixed point, steps[j] = f_j / (2 pi) * 2^64 mod 2^64,
+ * rounded to nearest. Both arrays are host memory. A position times such a step, modulo
+ * 2^64, is the exact phase of that position, so far positions lose nothing: the error
+ * of an angle stays below 2^-52 f_j p + 2^-22 radians. Scalings of the frequencies for
+ * long contexts are applied to f_j by the caller. FA_ERR_INVALID_ARG for NULL, n < 1
+ * or a frequency that is not finite or of magnitude 2^20 or more.
+ */
+fa_status fa_rope_steps(const double *frequencies, int64_t n, uint64_t *steps);
+
+/*
+ * fa_qk_norm_rope -- norms of queries and keys per head, and their rotary positions,
+ * in one pass: q_out, k_out from q, k as fa_norm_rope says. Queries are B x H x N x d,
+ * keys B x H_kv x N x d, by the strides of their descriptors: slices of a fused
+ * projection go straight to the layout an attention call takes. Either pair may be
+ * absent (data = NULL in both q and q_out, or in both k and k_out).
+ * positions: device memory, B x N int32, the position of each token (any value), or
+ * NULL: token n of every batch entry stands at n. d: 32, 64, 128 or 256.
+ * An output may be its own input (the same data and strides: in place); other
+ * overlaps of the buffers are refused when their extents cross, unless they are
+ * interleaved slices of one fused buffer with equal token (and batch) strides.
+ * One kernel launch, asynchronous on `stream`. Errors as fa_forward.
+ */
+fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_out,
+                          const fa_rows *k_out, const fa_norm_rope *rope, const int32_t *positions,
+                          int64_t B, int64_t H, int64_t H_kv, int64_t N, int64_t d, fa_dtype dtype,
+                          void *stream);
+
+/*
+ * fa_qk_norm_rope_backward -- gradients of fa_qk_norm_rope: from its inputs q, k and
+ * the gradients dq_out, dk_out of its outputs, dq and dk, and dq_weight, dk_weight (d
+ * float32 each), the gradients of the weights summed over every token and head. With
+ * u the rotation's transpose applied to dy, r = 1 / sqrt(mean(x^2) + eps), z = x r:
+ *     dx = r (u w - z mean(u w z)),   dw = sum u z      (dx = u without a weight).
+ * q (k) is read only where its weight is given, and dq_weight (dk_weight) is written
+ * exactly there; it must be NULL without. dq may be dq_out (in place), likewise dk.
+ * workspace: caller-owned device memory of at least
+ * fa_qk_norm_rope_backward_workspace_bytes(d) bytes, 16-byte aligned, scratch; needed
+ * only with a weight (else it may be NULL). Deterministic: no atomics, fixed order.
+ * One kernel launch, two with a weight. Everything else as fa_qk_norm_rope.
+ */
+fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_rows *dq_out,
+                                   const fa_rows *dk_out, const fa_rows *dq, const fa_rows *dk,
+                                   float *dq_weight, float *dk_weight, const fa_norm_rope *rope,
+                                   const int32_t *positions, int64_t B, int64_t H, int64_t H_kv,
+                                   int64_t N, int64_t d, fa_dtype dtype, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* Workspace bytes fa_qk_norm_rope_backward needs on the current device (0: invalid d). */
+size_t fa_qk_norm_rope_backward_workspace_bytes(int64_t d);
+
+/*
+ * A paged K/V cache: num_pages pages of page_size tokens of H_kv heads of d elements,
+ * K and V alike, element (page, token, head, i) at data + page * page_stride + token *
+ * token_stride + head * head_stride + i. The strides are multiples of 8 elements, > 0,
+ * and place every element somewhere else: token-major pages, head-major pages and
+ * K and V interleaved in one buffer are all fine. k, v: device memory, 16-byte aligned.
+ * page_size: a power of two, 8 .. 2^20. d: 32, 64, 128 or 256. num_pages < 2^31.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t num_pages, page_size, H_kv, d;
+    fa_dtype dtype;
+} fa_paged_cache;
+
+/*
+ * The batch of a serving step, as fa_paged_append and fa_forward_paged take it: B
+ * sequences with total_q new tokens, packed token-major; sequence b owns tokens
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 (none, one, or a chunk of a prompt), and
+ * seqlens_k[b] keys, its new tokens included: they stand at its last positions. Key
+ * position j of sequence b lives in page block_table[b * max_pages + j / page_size], at
+ * token j mod page_size. The three arrays are int32 on the device, read by the kernels
+ * and not checked on the host: offsets are clamped to the tensors, lengths to max_pages
+ * pages, and page numbers outside the cache are not followed (they read as zeros and
+ * are not written), so inconsistent arrays give wrong results but no access outside
+ * the buffers. Tokens past cu_seqlens_q[B] (a padded batch) belong to no sequence.
+ *
+ * fa_paged_append -- write the new tokens' keys and values into their pages, the keys
+ * (and, when q is given, the queries) normalised and rotated on the way as
+ * fa_norm_rope says; a token's rotary position is its key position. rope = NULL: keys
+ * are stored, and queries copied, as they are. q, q_out: total_q x H x d, or both with
+ * data = NULL (H is then ignored); k, v: total_q x H_kv x d; of all four the descriptor's
+ * `head` and `token` strides are used. q_out may be q. Rows of q_out of tokens that belong
+ * to no sequence are left as they are. Two sequences that write the same slot of a page
+ * leave either's row there. A sequence whose first new tokens would stand before position
+ * 0 (more new tokens than keys) stores only the others. One kernel launch.
+ */
+fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *q_out,
+                          const fa_paged_cache *cache, const int32_t *block_table, int64_t max_pages,
+                          const int32_t *cu_seqlens_q, const int32_t *seqlens_k, int64_t B, int64_t H,
+                          int64_t total_q, const fa_norm_rope *rope, void *stream);
+
+/*
+ * fa_forward_paged -- attention of the new tokens over their sequences' keys in the
+ * cache (fa_paged_append first: a token sees its own key). Q, O: total_q x H x d,
+ * contiguous, of the cache's dtype; LSE: total_q x H float32; H is a multiple of the
+ * cache's H_kv, query head h reads K/V head h / (H / H_kv). Token i of a sequence
+ * with L_q new tokens and L_k keys stands at i + L_k - L_q, which is what the masks
+ * refer to. A token that sees no key (L_k = 0, or a position before 0 under a mask)
+ * gets O = 0 and LSE = -infinity. Rows of O and LSE of tokens that belong to no
+ * sequence are left as they are. What pages hold past a sequence's end, or before the
+ * window of every query that is processed with it, is not looked at (NaN included); a
+ * NaN or infinity in a value row that one query of a sequence sees may reach the
+ * outputs of its other new tokens processed in the same tile.
+ *
+ * workspace: caller-owned device memory of at least
+ * fa_forward_paged_workspace_bytes(d) bytes, 32-byte aligned, scratch: its contents on
+ * entry do not matter. It does not depend on the batch. Calls that may overlap on the
+ * GPU need a workspace each. Two kernel launches. The results are the same every time
+ * on one device. Alignment of Q, O, LSE and errors as fa_forward; the arrays of the
+ * batch are 4-byte aligned. total_q = 0 returns FA_OK with nothing enqueued.
+ */
+fa_status fa_forward_paged(const void *Q, void *O, float *LSE, const fa_paged_cache *cache,
+                           const int32_t *block_table, int64_t max_pages,
+                           const int32_t *cu_seqlens_q, const int32_t *seqlens_k, int64_t B,
+                           int64_t H, int64_t total_q, float scale, fa_mask_mode mask_mode,
+                           int64_t window_left, int64_t window_right, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Workspace bytes fa_forward_paged needs on the current device (0: invalid d). */
+size_t fa_forward_paged_workspace_bytes(int64_t d);
+
 /* Static, NUL-terminated description of a status code. Never NULL. */
 const char *fa_status_string(fa_status status);
 

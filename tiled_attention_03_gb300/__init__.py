@@ -13,3 +13,8 @@ from .binding import backward, fa_backward, fa_backward_workspace_bytes  # noqa:
 from .binding import fa_forward_varlen  # noqa: F401
 from .binding import fa_forward_host, fa_forward_host_workspace_bytes  # noqa: F401
 from .binding import fa_backward_varlen, fa_backward_varlen_workspace_bytes  # noqa: F401
+from .binding import (NormRope, PagedCache, fa_forward_paged,  # noqa: F401
+                      fa_forward_paged_workspace_bytes, fa_paged_append, fa_qk_norm_rope,
+                      fa_qk_norm_rope_backward, fa_qk_norm_rope_backward_workspace_bytes,
+                      fa_rope_steps, forward_paged, qk_norm_rope, qk_norm_rope_backward,
+                      rope_frequencies, rope_steps)

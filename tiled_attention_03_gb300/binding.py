@@ -9,6 +9,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -30,6 +31,28 @@ class FaError(RuntimeError):
     def __init__(self, status: int, what: str = "fa_forward"):
         self.status = status
         super().__init__(f"{what}: {fa_status_string(status)}")
+
+
+class FaRows(ctypes.Structure):
+    """fa_rows of include/fa.h: a (batch, head, token, d) tensor by its strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("token", ctypes.c_int64)]
+
+
+class FaNormRope(ctypes.Structure):
+    """fa_norm_rope of include/fa.h."""
+    _fields_ = [("steps", ctypes.c_void_p), ("rotary_dim", ctypes.c_int64),
+                ("layout", ctypes.c_int), ("magnitude", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class FaPagedCache(ctypes.Structure):
+    """fa_paged_cache of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("H_kv", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -97,6 +120,28 @@ def load_library_at(path: str) -> ctypes.CDLL:
         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.fa_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_backward_workspace_bytes.argtypes = [ctypes.c_int64] * 4
+    rows, rope, cache = (ctypes.POINTER(t) for t in (FaRows, FaNormRope, FaPagedCache))
+    lib.fa_rope_steps.restype = ctypes.c_int
+    lib.fa_rope_steps.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.fa_qk_norm_rope.restype = ctypes.c_int
+    lib.fa_qk_norm_rope.argtypes = [rows] * 4 + [rope, ctypes.c_void_p] + [ctypes.c_int64] * 5 + [
+        ctypes.c_int, ctypes.c_void_p]
+    lib.fa_qk_norm_rope_backward.restype = ctypes.c_int
+    lib.fa_qk_norm_rope_backward.argtypes = [rows] * 6 + [ctypes.c_void_p] * 2 + [
+        rope, ctypes.c_void_p] + [ctypes.c_int64] * 5 + [
+        ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.fa_qk_norm_rope_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_qk_norm_rope_backward_workspace_bytes.argtypes = [ctypes.c_int64]
+    lib.fa_paged_append.restype = ctypes.c_int
+    lib.fa_paged_append.argtypes = [rows] * 4 + [cache, ctypes.c_void_p, ctypes.c_int64] + [
+        ctypes.c_void_p] * 2 + [ctypes.c_int64] * 3 + [rope, ctypes.c_void_p]
+    lib.fa_forward_paged.restype = ctypes.c_int
+    lib.fa_forward_paged.argtypes = [ctypes.c_void_p] * 3 + [
+        cache, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p] + [
+        ctypes.c_int64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                               ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.fa_forward_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_forward_paged_workspace_bytes.argtypes = [ctypes.c_int64]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_status_string.argtypes = [ctypes.c_int]
     lib.fa_sync_status.restype = ctypes.c_int
@@ -451,3 +496,327 @@ def fa_backward_varlen(q, k, v, o, do, lse, cu_seqlens_q, cu_seqlens_k, dq, dk, 
                                 _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, "fa_backward_varlen")
+
+
+# ---- queries and keys on their way to attention, and the paged cache of a serving loop
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, context: float = 0, slow: float = 1.0,
+                     fast: float = 32.0) -> list[float]:
+    """Radians per position of the rotary_dim / 2 pairs: base^(-2 j / rotary_dim), scaled
+    for contexts longer than the trained one by `factor`:
+      "none"    as they are;
+      "linear"  f / factor (positions interpolated);
+      "base"    base * factor^(rotary_dim / (rotary_dim - 2)) in place of base, so that the
+                slowest pair is slowed by `factor` and the fastest not at all;
+      "band"    by the turns t = context * f / (2 pi) of a pair over the trained
+                `context`: f where t >= fast, f / factor where t <= slow, and
+                f (g + (1 - g) / factor), g = (t - slow) / (fast - slow), between."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise FaError(FA_ERR_INVALID_ARG, "rope_frequencies")
+    if scaling == "base":
+        if rotary_dim == 2:
+            raise FaError(FA_ERR_INVALID_ARG, "rope_frequencies")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = [base ** (-2.0 * j / rotary_dim) for j in range(rotary_dim // 2)]
+    if scaling in ("none", "base"):
+        return f
+    if scaling == "linear":
+        return [x / factor for x in f]
+    if scaling != "band" or not fast > slow:
+        raise FaError(FA_ERR_INVALID_ARG, "rope_frequencies")
+    ramp = [min(1.0, max(0.0, (context * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
+    return [x * (g + (1 - g) / factor) for x, g in zip(f, ramp)]
+
+
+def fa_rope_steps(frequencies) -> list[int]:
+    """fa_rope_steps on a sequence of floats: each frequency as a fraction of a turn per
+    position, in 64-bit fixed point."""
+    n = len(frequencies)
+    f = (ctypes.c_double * max(n, 1))(*frequencies)
+    out = (ctypes.c_uint64 * max(n, 1))()
+    rc = load_library().fa_rope_steps(f, n, out)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rope_steps")
+    return list(out[:n])
+
+
+def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               context: float = 0, slow: float = 1.0, fast: float = 32.0,
+               device="cuda") -> torch.Tensor:
+    """The steps of rope_frequencies(...) as the device tensor NormRope takes (64-bit
+    patterns in int64)."""
+    steps = fa_rope_steps(rope_frequencies(rotary_dim, base, scaling, factor, context, slow, fast))
+    return torch.tensor([x - (1 << 64) if x >= 1 << 63 else x for x in steps],
+                        dtype=torch.int64).to(device)
+
+
+class NormRope:
+    """fa_norm_rope with the tensors it points to: the rotary steps (int64, None: no
+    rotation), "half" or "interleaved" pairs, the magnitude that some scalings apply, and
+    the weights of the per-head norms of queries and keys (None: not normalised)."""
+
+    def __init__(self, steps: torch.Tensor | None = None, layout: str = "half",
+                 magnitude: float = 1.0, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6):
+        if layout not in _LAYOUTS:
+            raise FaError(FA_ERR_INVALID_ARG, "NormRope")
+        for t in (steps, q_weight, k_weight):
+            if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dim() != 1):
+                raise FaError(FA_ERR_INVALID_ARG, "NormRope")
+        if steps is not None and steps.dtype != torch.int64:
+            raise FaError(FA_ERR_INVALID_ARG, "NormRope")
+        if any(w is not None and w.dtype not in _DTYPES for w in (q_weight, k_weight)):
+            raise FaError(FA_ERR_INVALID_ARG, "NormRope")
+        self.steps, self.q_weight, self.k_weight = steps, q_weight, k_weight
+        self._weights = [(w.dtype, w.numel()) for w in (q_weight, k_weight) if w is not None]
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = FaNormRope(ptr(steps), 0 if steps is None else 2 * steps.numel(),
+                            _LAYOUTS[layout], float(magnitude), ptr(q_weight), ptr(k_weight),
+                            float(eps))
+
+    def check(self, dtype, d: int, what: str) -> None:
+        for w in self._weights:
+            if w != (dtype, d):
+                raise FaError(FA_ERR_INVALID_ARG, what)
+
+
+class PagedCache:
+    """fa_paged_cache over two tensors (num_pages, page_size, H_kv, d) of equal strides;
+    views are fine (head-major pages, K and V interleaved in one buffer) as long as d is
+    contiguous."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if not k.is_cuda or k.dim() != 4 or k.dtype not in _DTYPES or v.dtype != k.dtype or \
+                v.device != k.device or v.shape != k.shape or v.stride() != k.stride() or \
+                k.stride(3) != 1:
+            raise FaError(FA_ERR_INVALID_ARG, "PagedCache")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.num_pages, self.page_size, self.H_kv, self.d = k.shape
+        ps, ts, hs = k.stride()[:3]
+        self.c = FaPagedCache(k.data_ptr(), v.data_ptr(), ps, ts, hs, *k.shape, _DTYPES[k.dtype])
+
+
+_NO_ROWS = FaRows(None, 0, 0, 0)
+
+
+def _rows(t: torch.Tensor | None, dtype, what: str) -> FaRows:
+    """The descriptor of a (B, H, N, d) or token-major (tokens, H, d) tensor."""
+    if t is None:
+        return _NO_ROWS
+    s = t.stride()
+    if not t.is_cuda or t.dtype != dtype or s[-1] != 1:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    if len(s) == 4:
+        return FaRows(t.data_ptr(), s[0], s[1], s[2])
+    return FaRows(t.data_ptr(), 0, s[1], s[0])
+
+
+def _qk_sizes(q, k, what: str):
+    """B, H, H_kv, N, d of queries and keys that may each be None."""
+    some = q if q is not None else k
+    if some is None or some.dim() not in (3, 4) or some.dtype not in _DTYPES:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    shape = some.shape
+    B, N, d = (shape[0], shape[2], shape[3]) if len(shape) == 4 else (1, shape[0], shape[2])
+    H, H_kv = (0 if t is None else t.shape[1] for t in (q, k))
+    if q is not None and k is not None:
+        other = k.shape
+        if len(other) != len(shape) or other[0] != shape[0] or other[2:] != shape[2:]:
+            raise FaError(FA_ERR_INVALID_ARG, what)
+    return B, H, H_kv, N, d
+
+
+def _same_shape(a, b, what: str) -> None:
+    if (a is None) != (b is None) or (a is not None and a.shape != b.shape):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+
+
+def _int32(t: torch.Tensor | None, numel: int, what: str):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    return t.data_ptr()
+
+
+def _workspace(workspace, need: int, like: torch.Tensor, stream, what: str):
+    """(pointer, bytes) of a caller's workspace, or of one from PyTorch's caching
+    allocator, marked as used on `stream`."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 32), dtype=torch.uint8, device=like.device)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)
+        elif stream is not None:
+            workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=like.device))
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def fa_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
+                    k_out: torch.Tensor | None, rope: NormRope,
+                    positions: torch.Tensor | None = None, stream=None) -> None:
+    """Enqueue fa_qk_norm_rope: q, q_out (B, H, N, d) and k, k_out (B, H_kv, N, d), or token-major
+    (tokens, heads, d), any strides with d contiguous (slices of a fused projection);
+    either pair may be None. positions: int32, one per token (B x N), None: 0 .. N-1."""
+    what = "fa_qk_norm_rope"
+    B, H, H_kv, N, d = _qk_sizes(q, k, what)
+    dtype = (q if q is not None else k).dtype
+    _same_shape(q, q_out, what)
+    _same_shape(k, k_out, what)
+    rope.check(dtype, d, what)
+    rc = load_library().fa_qk_norm_rope(
+        _rows(q, dtype, what), _rows(k, dtype, what), _rows(q_out, dtype, what),
+        _rows(k_out, dtype, what), rope.c, _int32(positions, B * N, what), B, H, H_kv, N, d,
+        _DTYPES[dtype], _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope: NormRope,
+                 positions: torch.Tensor | None = None, stream=None):
+    """Queries and keys normalised and rotated, as new contiguous tensors."""
+    q_out, k_out = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                    for t in (q, k))
+    fa_qk_norm_rope(q, k, q_out, k_out, rope, positions, stream)
+    return q_out, k_out
+
+
+def fa_qk_norm_rope_backward_workspace_bytes(d: int) -> int:
+    return load_library().fa_qk_norm_rope_backward_workspace_bytes(d)
+
+
+def fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, rope: NormRope,
+                             positions: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Enqueue fa_qk_norm_rope_backward: dq_out, dq (B, H, N, d) and dk_out, dk
+    (B, H_kv, N, d) (or token-major), either pair may be None; q, k as in the forward, and
+    dq_weight, dk_weight (d,) float32, each given exactly where `rope` has the weight.
+    Without a workspace tensor one is taken from PyTorch's caching allocator."""
+    what = "fa_qk_norm_rope_backward"
+    lib = load_library()
+    B, H, H_kv, N, d = _qk_sizes(dq, dk, what)
+    like = dq if dq is not None else dk
+    dtype = like.dtype
+    for x, dy, dx, w, dw in ((q, dq_out, dq, rope.q_weight, dq_weight),
+                             (k, dk_out, dk, rope.k_weight, dk_weight)):
+        _same_shape(dy, dx, what)
+        if dx is not None and w is not None:
+            _same_shape(x, dx, what)
+        if dw is not None and (not dw.is_cuda or dw.dtype != torch.float32 or dw.numel() != d
+                               or not dw.is_contiguous()):
+            raise FaError(FA_ERR_INVALID_ARG, what)
+    rope.check(dtype, d, what)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    ws, n, keep = None, 0, None
+    if dq_weight is not None or dk_weight is not None:
+        ws, n, keep = _workspace(
+            workspace, lib.fa_qk_norm_rope_backward_workspace_bytes(d) if workspace is None else 0,
+            like, stream, what)
+    rc = lib.fa_qk_norm_rope_backward(
+        _rows(q, dtype, what), _rows(k, dtype, what), _rows(dq_out, dtype, what),
+        _rows(dk_out, dtype, what), _rows(dq, dtype, what), _rows(dk, dtype, what), ptr(dq_weight),
+        ptr(dk_weight), rope.c, _int32(positions, B * N, what), B, H, H_kv, N, d, _DTYPES[dtype],
+        ws, n, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, rope: NormRope,
+                          positions: torch.Tensor | None = None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of qk_norm_rope for the upstream gradients of its
+    outputs; a weight's gradient is None where `rope` has no such weight."""
+    dq, dk = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+              for t in (dq_out, dk_out))
+    dw = [None if g is None or w is None else
+          torch.empty(w.shape, dtype=torch.float32, device=w.device)
+          for g, w in ((dq, rope.q_weight), (dk, rope.k_weight))]
+    fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dw[0], dw[1], rope, positions, None, stream)
+    return dq, dk, dw[0], dw[1]
+
+
+def _batch(block_table, cu_seqlens_q, seqlens_k, what: str):
+    """(table pointer, max_pages, cu pointer, seqlens pointer, B) of a serving batch."""
+    B = seqlens_k.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or B < 1:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    pages = block_table.shape[1]
+    return (_int32(block_table, B * pages, what), pages, _int32(cu_seqlens_q, B + 1, what),
+            _int32(seqlens_k, B, what), B)
+
+
+def fa_paged_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                    q_out: torch.Tensor | None, cache: PagedCache, block_table: torch.Tensor,
+                    cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor,
+                    rope: NormRope | None = None, stream=None) -> None:
+    """Enqueue fa_paged_append: k, v (total_q, H_kv, d) go to the pages of block_table
+    (B, max_pages) int32 at each sequence's last positions, k normalised and rotated
+    by `rope` on the way, and so does q (total_q, H, d) to q_out (both may be None).
+    cu_seqlens_q (B + 1,) and seqlens_k (B,) int32; seqlens_k counts the new tokens."""
+    what = "fa_paged_append"
+    dtype, d = cache.dtype, cache.d
+    total = k.shape[0]
+    if k.dim() != 3 or k.shape[1] != cache.H_kv or k.shape[2] != d or v.shape != k.shape:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    _same_shape(q, q_out, what)
+    if q is not None and (q.dim() != 3 or q.shape[0] != total or q.shape[2] != d):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    if rope is not None:
+        rope.check(dtype, d, what)
+    table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
+    rc = load_library().fa_paged_append(
+        _rows(q, dtype, what), _rows(k, dtype, what), _rows(v, dtype, what),
+        _rows(q_out, dtype, what), cache.c, table, pages, cu, lens, B,
+        0 if q is None else q.shape[1], total, None if rope is None else rope.c,
+        _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def fa_forward_paged_workspace_bytes(d: int) -> int:
+    return load_library().fa_forward_paged_workspace_bytes(d)
+
+
+def fa_forward_paged(q: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, cache: PagedCache,
+                     block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                     seqlens_k: torch.Tensor, scale: float, mask_mode=FA_MASK_CAUSAL,
+                     window_left: int = 0, window_right: int = 0,
+                     workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Enqueue fa_forward_paged: q, o (total_q, H, d) and lse (total_q, H) float32,
+    contiguous; block_table (B, max_pages), cu_seqlens_q (B + 1,), seqlens_k (B,) int32.
+    Without a workspace tensor one is taken from PyTorch's caching allocator."""
+    what = "fa_forward_paged"
+    lib = load_library()
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.d or o.shape != shape or lse.shape != shape[:2] or \
+            q.dtype != cache.dtype or o.dtype != q.dtype or lse.dtype != torch.float32:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    for t in (q, o, lse):
+        if not t.is_cuda or not t.is_contiguous():
+            raise FaError(FA_ERR_INVALID_ARG, what)
+    table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
+    ws, n, keep = _workspace(
+        workspace, lib.fa_forward_paged_workspace_bytes(cache.d) if workspace is None else 0, q,
+        stream, what)
+    rc = lib.fa_forward_paged(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache.c, table, pages, cu,
+                              lens, B, shape[1], shape[0], float(scale), _MASKS[mask_mode],
+                              int(window_left), int(window_right), ws, n, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def forward_paged(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
+                  cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor, scale: float | None = None,
+                  mask="causal", window=(0, 0), stream=None):
+    """Attention of the new tokens q (total_q, H, d) over a paged cache: returns (O, LSE)."""
+    q = q.contiguous()
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    fa_forward_paged(q, o, lse, cache, block_table, cu_seqlens_q, seqlens_k,
+                     q.shape[-1] ** -0.5 if scale is None else scale, mask, window[0], window[1], None,
+                     stream)
+    return o, lse

@@ -1,0 +1,259 @@
+// fa_paged_api.cu -- fa_forward_paged: argument checks, tensor maps and launches of the
+// paged attention kernel and its merge (fa_paged_kernel.cuh).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_paged_host.h"
+#include "fa_paged_kernel.cuh"
+
+namespace {
+
+using fa_host::align256;
+
+constexpr int kMaxDevices = 64;
+
+// K/V tiles per CTA at least: shares of one tile (a merge of as many pieces) measured
+// no slower than longer ones at small sizes.
+constexpr int kMinTiles = 1;
+
+struct Configured {
+    std::once_flag once;
+    cudaError_t err = cudaSuccess;
+};
+Configured g_configured[kMaxDevices];
+
+template <int D, bool BF16>
+cudaError_t opt_in() {
+    return cudaFuncSetAttribute(fa::paged::fa_paged_kernel<D, BF16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                fa::paged::Smem<D>::kAlloc);
+}
+
+bool configured(int dev) {
+    Configured &c = g_configured[dev];
+    std::call_once(c.once, [&c] {
+        cudaError_t e = opt_in<32, false>();
+        if (e == cudaSuccess) e = opt_in<32, true>();
+        if (e == cudaSuccess) e = opt_in<64, false>();
+        if (e == cudaSuccess) e = opt_in<64, true>();
+        if (e == cudaSuccess) e = opt_in<128, false>();
+        if (e == cudaSuccess) e = opt_in<128, true>();
+        if (e == cudaSuccess) e = opt_in<256, false>();
+        if (e == cudaSuccess) e = opt_in<256, true>();
+        c.err = e;
+    });
+    return c.err == cudaSuccess;
+}
+
+// Two partial results of 128 rows per CTA, and what the merge needs to know of each CTA.
+struct Layout {
+    size_t lse, o, bytes;  // info at 0
+};
+Layout layout_of(int64_t d, int64_t ctas) {
+    Layout l;
+    l.lse = align256(static_cast<size_t>(ctas) * sizeof(fa::paged::MergeInfo));
+    l.o = l.lse + align256(static_cast<size_t>(2 * ctas) * fa::paged::kBM * sizeof(float));
+    l.bytes = l.o + static_cast<size_t>(2 * ctas) * fa::paged::kBM * static_cast<size_t>(d) * sizeof(float);
+    return l;
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                   const fa::paged::Params &p, const fa::paged::MergeParams &m, unsigned ctas,
+                   unsigned row_blocks, cudaStream_t st) {
+    fa::paged::fa_paged_kernel<D, BF16>
+        <<<ctas, fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st>>>(q, k, v, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    fa::paged::fa_paged_merge_kernel<D, BF16>
+        <<<dim3(ctas, row_blocks), fa::paged::kMergeWarps * 32, 0, st>>>(m);
+    return cudaGetLastError();
+}
+
+int sm_count_or_default() {
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    else
+        cudaGetLastError();
+    return sms;
+}
+
+fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, const int32_t *table,
+              int64_t max_pages, const int32_t *cu_q, const int32_t *seq_k, int64_t B, int64_t H,
+              int64_t total_q, float scale, fa_mask_mode mask_mode, int64_t window_left,
+              int64_t window_right, void *workspace, size_t workspace_bytes, void *stream) {
+    // ---- host-side checks: nothing is enqueued on failure
+    if (cache == nullptr || B < 1 || H < 1 || total_q < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
+    size_t cache_bytes = 0;
+    const fa_status cs = fa_host::check_cache(*cache, &cache_bytes);
+    if (cs != FA_OK) return cs;
+    const int64_t d = cache->d, H_kv = cache->H_kv;
+    if (H % H_kv != 0) return FA_ERR_INVALID_ARG;
+    if (mask_mode != FA_MASK_NONE && mask_mode != FA_MASK_CAUSAL && mask_mode != FA_MASK_WINDOW)
+        return FA_ERR_INVALID_ARG;
+    if (mask_mode == FA_MASK_WINDOW && (window_left < 0 || window_right < 0)) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (total_q == 0) return FA_OK;  // no query rows: nothing to do
+    if (!Q || !O || !LSE || !cu_q || !seq_k || (!table && max_pages > 0)) return FA_ERR_INVALID_ARG;
+    if (!fa_host::aligned16(Q) || !fa_host::aligned32(O) || !fa_host::aligned4(LSE) ||
+        !fa_host::aligned4(cu_q) || !fa_host::aligned4(seq_k) || !fa_host::aligned4(table))
+        return FA_ERR_INVALID_ARG;
+    // Heads of a unit: all query heads of one K/V head, or a divisor of them.
+    const int64_t group = H / H_kv;
+    int64_t pf = group;
+    if (pf > fa::paged::kBM)
+        for (pf = fa::paged::kBM; group % pf != 0;) --pf;
+    const int64_t tpt = fa::paged::kBM / pf, spaces = H / pf;
+    const int64_t max_keys = max_pages * cache->page_size;
+    // Size limits of this implementation: 32-bit token and key indices, and a line of
+    // work below 2^31 tiles.
+    const int64_t kLimit = int64_t{1} << 29;
+    if (total_q > kLimit || max_pages > kLimit || max_keys > kLimit || B > kLimit || H > kLimit ||
+        total_q * H > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    const double tiles = static_cast<double>(max_keys / fa::paged::bn(static_cast<int>(d)) + 2);
+    if (static_cast<double>(spaces) * static_cast<double>(total_q / tpt + B) * tiles > 2147483647.0)
+        return FA_ERR_UNSUPPORTED;
+    const int ctas_needed = sm_count_or_default();
+    const Layout lay = layout_of(d, ctas_needed);
+    if (workspace == nullptr || !fa_host::aligned32(workspace) || workspace_bytes < lay.bytes)
+        return FA_ERR_INVALID_ARG;
+    const size_t tbytes = static_cast<size_t>(total_q) * H * d * 2;
+    const size_t lbytes = static_cast<size_t>(total_q) * H * sizeof(float);
+    const size_t cubytes = static_cast<size_t>(B + 1) * 4, skbytes = static_cast<size_t>(B) * 4;
+    const size_t tabytes = static_cast<size_t>(B) * max_pages * 4;
+    struct Buf {
+        const void *p;
+        size_t n;
+    };
+    const Buf in[] = {{Q, tbytes}, {cache->k, cache_bytes}, {cache->v, cache_bytes},
+                      {cu_q, cubytes}, {seq_k, skbytes}, {table, tabytes}};
+    const Buf out[] = {{O, tbytes}, {LSE, lbytes}, {workspace, lay.bytes}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Buf &b : in)
+            if (b.n > 0 && fa_host::overlaps(out[i].p, out[i].n, b.p, b.n)) return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (fa_host::overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return FA_ERR_INVALID_ARG;
+    }
+
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    const fa_host::DeviceInfo di = fa_host::device_info(dev);
+    if (di.err == cudaErrorInvalidDevice || dev >= kMaxDevices) return FA_ERR_UNSUPPORTED;
+    if (di.err != cudaSuccess) return FA_ERR_CUDA;
+    if (!(di.cc_major == 10 && di.cc_minor == 3)) return FA_ERR_UNSUPPORTED;
+    const void *all[] = {Q, O, LSE, cu_q, seq_k, cache->k, cache->v, workspace};
+    for (const void *x : all)
+        if (!fa_host::on_device(x, dev)) return FA_ERR_INVALID_ARG;
+    if (max_pages > 0 && !fa_host::on_device(table, dev)) return FA_ERR_INVALID_ARG;
+    if (!configured(dev)) return FA_ERR_CUDA;
+
+    const bool bf16 = cache->dtype == FA_DTYPE_BF16;
+    const int kbn = fa::paged::bn(static_cast<int>(d));
+    const int64_t chunk = cache->page_size < kbn ? cache->page_size : kbn;
+    CUtensorMap mq, mk, mv;
+    if (!fa_host::make_map_rows(&mq, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf),
+                                static_cast<uint32_t>(tpt)) ||
+        !fa_host::make_map_pages(&mk, cache->k, *cache, static_cast<uint32_t>(chunk)) ||
+        !fa_host::make_map_pages(&mv, cache->v, *cache, static_cast<uint32_t>(chunk)))
+        return FA_ERR_CUDA;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    fa::paged::Params p{};
+    p.O = O;
+    p.LSE = LSE;
+    p.info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
+    p.part_LSE = reinterpret_cast<float *>(ws + lay.lse);
+    p.part_O = reinterpret_cast<float *>(ws + lay.o);
+    p.cu_q = cu_q;
+    p.seq_k = seq_k;
+    p.table = table;
+    p.B = static_cast<int>(B);
+    p.H = static_cast<int>(H);
+    p.kv_group = static_cast<int>(group);
+    p.pf = static_cast<int>(pf);
+    p.spaces = static_cast<int>(spaces);
+    p.tpt = static_cast<int>(tpt);
+    p.total_q = static_cast<int>(total_q);
+    p.max_pages = static_cast<int>(max_pages);
+    p.page_log2 = 0;
+    while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
+    p.num_pages = static_cast<int>(cache->num_pages);
+    p.max_keys = static_cast<int>(max_keys);
+    p.chunk = static_cast<int>(chunk);
+    // "all keys" is a window wider than any offset
+    const int64_t every = total_q + max_keys;
+    int64_t wl = every, wr = every;
+    if (mask_mode == FA_MASK_CAUSAL) wr = 0;
+    if (mask_mode == FA_MASK_WINDOW) {
+        wl = window_left < every ? window_left : every;
+        wr = window_right < every ? window_right : every;
+    }
+    p.wl = static_cast<int>(wl);
+    p.wr = static_cast<int>(wr);
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.min_tiles = kMinTiles;
+    p.wait_budget_ns = fa_host::wait_budget();
+    p.status = di.status;
+    p.fault_skip_k = fa_host::take_fault_position();
+    fa::paged::MergeParams m{};
+    m.info = p.info;
+    m.part_O = p.part_O;
+    m.part_LSE = p.part_LSE;
+    m.O = O;
+    m.LSE = LSE;
+    m.H = p.H;
+    m.pf = p.pf;
+    const unsigned ctas = static_cast<unsigned>(di.sm_count);
+    const int64_t max_rows = tpt * pf < total_q * pf ? tpt * pf : total_q * pf;
+    const unsigned row_blocks =
+        static_cast<unsigned>((max_rows + fa::paged::kMergeWarps - 1) / fa::paged::kMergeWarps);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (d == 32)
+        e = bf16 ? launch<32, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
+                 : launch<32, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+    else if (d == 64)
+        e = bf16 ? launch<64, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
+                 : launch<64, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+    else if (d == 128)
+        e = bf16 ? launch<128, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
+                 : launch<128, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+    else
+        e = bf16 ? launch<256, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
+                 : launch<256, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    fa_host::count_launches(2);
+    return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_forward_paged_workspace_bytes(int64_t d) {
+    if (d != 32 && d != 64 && d != 128 && d != 256) return 0;
+    return layout_of(d, sm_count_or_default()).bytes;
+}
+
+fa_status fa_forward_paged(const void *Q, void *O, float *LSE, const fa_paged_cache *cache,
+                           const int32_t *block_table, int64_t max_pages,
+                           const int32_t *cu_seqlens_q, const int32_t *seqlens_k, int64_t B,
+                           int64_t H, int64_t total_q, float scale, fa_mask_mode mask_mode,
+                           int64_t window_left, int64_t window_right, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    return run(Q, O, LSE, cache, block_table, max_pages, cu_seqlens_q, seqlens_k, B, H, total_q, scale,
+               mask_mode, window_left, window_right, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

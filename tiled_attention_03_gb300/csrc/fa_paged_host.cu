@@ -1,0 +1,111 @@
+// fa_paged_host.cu -- checks and tensor maps shared by the paged-cache calls.
+#include "fa_paged_host.h"
+
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "fa_host.h"
+
+namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// Swizzle and promotion as in the library's other maps: rows of 128 bytes (64 at d = 32).
+bool encode(CUtensorMap *map, const void *base, bool bf16, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box, int64_t d) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               d < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+namespace fa_host {
+
+fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
+    if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return FA_ERR_INVALID_ARG;
+    if (c.dtype != FA_DTYPE_FP16 && c.dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+    if (c.num_pages < 1 || c.H_kv < 1 || c.page_size < 1 || c.d < 1) return FA_ERR_INVALID_ARG;
+    const int64_t st[3] = {c.page_stride, c.token_stride, c.head_stride};
+    for (int64_t s : st)
+        if (s < 1 || s % 8 != 0) return FA_ERR_INVALID_ARG;
+    if (c.d != 32 && c.d != 64 && c.d != 128 && c.d != 256) return FA_ERR_UNSUPPORTED;
+    if (c.page_size < 8 || c.page_size > (int64_t{1} << 20) || (c.page_size & (c.page_size - 1)) != 0)
+        return FA_ERR_UNSUPPORTED;
+    // what a tensor map and 64-bit extents hold
+    if (c.num_pages >= (int64_t{1} << 31) || c.H_kv > (int64_t{1} << 20)) return FA_ERR_UNSUPPORTED;
+    for (int64_t s : st)
+        if (s >= (int64_t{1} << 39)) return FA_ERR_UNSUPPORTED;
+    const double extent = static_cast<double>(c.num_pages - 1) * static_cast<double>(c.page_stride) +
+                          static_cast<double>(c.page_size - 1) * static_cast<double>(c.token_stride) +
+                          static_cast<double>(c.H_kv - 1) * static_cast<double>(c.head_stride);
+    if (extent > 1e18) return FA_ERR_UNSUPPORTED;
+    // every element at a place of its own: with the (extent > 1) dimensions sorted by
+    // stride, each steps over all that the smaller ones span
+    struct Dim {
+        int64_t n, s;
+    } dim[3] = {{c.num_pages, st[0]}, {c.page_size, st[1]}, {c.H_kv, st[2]}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (dim[j].s > dim[j + 1].s) {
+                const Dim t = dim[j];
+                dim[j] = dim[j + 1];
+                dim[j + 1] = t;
+            }
+    int64_t span = c.d;
+    for (const Dim &x : dim)
+        if (x.n > 1) {
+            if (x.s < span) return FA_ERR_INVALID_ARG;
+            span += (x.n - 1) * x.s;
+        }
+    *bytes = static_cast<size_t>(span) * 2;
+    return FA_OK;
+}
+
+bool make_map_rows(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t heads,
+                   int64_t d, uint32_t box_heads, uint32_t box_tokens) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d * 2),
+                                   static_cast<cuuint64_t>(heads * d * 2)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(d < 64 ? d : 64), box_heads, box_tokens};
+    return encode(map, base, bf16, 3, dims, strides, box, d);
+}
+
+bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c,
+                    uint32_t box_tokens) {
+    const cuuint64_t dims[4] = {
+        static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page_size),
+        static_cast<cuuint64_t>(c.H_kv), static_cast<cuuint64_t>(c.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride * 2),
+                                   static_cast<cuuint64_t>(c.head_stride * 2),
+                                   static_cast<cuuint64_t>(c.page_stride * 2)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.d < 64 ? c.d : 64), box_tokens, 1, 1};
+    return encode(map, base, c.dtype == FA_DTYPE_BF16, 4, dims, strides, box, c.d);
+}
+
+}  // namespace fa_host

@@ -1,0 +1,25 @@
+// fa_paged_host.h -- host-side helpers of the paged-cache calls (internal).
+#pragma once
+
+#include <cuda.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fa.h"
+
+namespace fa_host {
+
+// Checks a cache descriptor (not its device); bytes: the extent of k (and of v) from
+// its first to its last element.
+fa_status check_cache(const fa_paged_cache &c, size_t *bytes);
+// 3-D TMA map over a contiguous tokens x heads x d 16-bit tensor, ordered (d, heads,
+// tokens): box of min(d, 64) columns x box_heads x box_tokens.
+bool make_map_rows(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t heads,
+                   int64_t d, uint32_t box_heads, uint32_t box_tokens);
+// 4-D TMA map over one tensor of a paged cache, ordered (d, token in page, head, page):
+// box of min(d, 64) columns x box_tokens tokens of one head of one page.
+bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c,
+                    uint32_t box_tokens);
+
+}  // namespace fa_host

@@ -1,0 +1,1004 @@
+// fa_paged_kernel.cuh -- attention of a batch's new tokens over a paged K/V cache, for
+// head dimensions 32, 64, 128 and 256 on sm_103a.
+//
+// The method is that of fa_fwd1t_kernel.cuh (128-row Q tile, K/V blocks of bn(D) keys,
+// S in two or three TMEM buffers, online softmax with a lazily moved reference max, P
+// in tensor memory, O divided by l once). What differs:
+//   * K and V tiles are gathered from pages: the tile's keys are cut into chunks of
+//     min(page size, bn) tokens, lane c of the producer warp reads chunk c's page number
+//     and issues its TMA boxes; chunks that hold no key of the unit are not read.
+//   * Rows of a unit are (token, head) pairs: the pf query heads of one K/V head (or
+//     a divisor of them when there are more than 128) for 128 / pf tokens, token-major
+//     in the tile, so that every K/V tile is read once for all of them, at one token
+//     per sequence as well as in a chunk of a prompt.
+//   * The work is cut by K/V tiles, not by units: all units (sequence, head group,
+//     tile of tokens) with all their visible K/V tiles form one line of W tiles, and
+//     CTA c takes tiles c T .. c T + T - 1 of it (T = ceil(W / CTAs), at least
+//     min_tiles). Every CTA gets the same share whatever the lengths are, without counters.
+//     A unit cut by a share's end leaves one partial (O / l and LSE, fp32) per piece,
+//     which fa_paged_merge_kernel joins in the order of the pieces: at most two pieces
+//     per CTA are partial, so the workspace depends on the SM count and D alone. The
+//     lengths are read on the device, so a captured call follows them.
+//   * Keys that no row of the unit sees (past the sequence's end in its last page, or
+//     before a window) may hold anything, NaN included: their scores are replaced
+//     before the maximum, and their V rows are zeroed in shared memory before the product.
+//   * A row that sees no key (a sequence without keys, or more queries than keys under
+//     a mask) gets O = 0 and LSE = -inf.
+//
+// Warps (256 threads): 0-3 softmax, 4 Q and K producer, 5 MMA issuer, 6 V producer,
+// 7 scheduler (walks the CTA's share and publishes its pieces). A softmax warp none of
+// whose rows exists (decode: pf rows of 128) passes its blocks on without touching them.
+// Every wait is bounded; on expiry the CTA records the failure, drains its copies and
+// MMAs, frees its tensor memory and returns.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "fa_mask.cuh"
+#include "fa_tmem_max.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace paged {
+
+constexpr int kBM = 128;  // rows per unit (TMEM lanes)
+__host__ __device__ constexpr int bn(int D) { return D == 256 ? 64 : 128; }  // keys per tile
+constexpr int kThreads = 256;
+constexpr int kQKWarp = 4;
+constexpr int kMmaWarp = 5;
+constexpr int kVWarp = 6;
+constexpr int kSchedWarp = 7;
+// K and V ring depths: what shared memory holds next to the Q tile
+__host__ __device__ constexpr int k_stages(int D) { return D <= 64 ? 6 : 3; }
+__host__ __device__ constexpr int v_stages(int D) { return D <= 64 ? 6 : D == 128 ? 3 : 2; }
+constexpr int kMaxStages = 6;
+constexpr int kSBufs = 3;
+__host__ __device__ constexpr int s_bufs(int D) { return D == 256 ? 2 : 3; }
+// Q read by S = Q K^T from TMEM at d = 256: with 64-key tiles the shared-memory form
+// would need more than the SM's shared-memory bandwidth (see fa_fwd1t_kernel.cuh)
+__host__ __device__ constexpr bool q_in_tmem(int D) { return D == 256; }
+constexpr uint32_t kTmemCols = 512;
+__host__ __device__ constexpr uint32_t tmem_o(int D) { return D == 256 ? 256u : 384u; }
+constexpr uint32_t kTmemS = 0;
+constexpr uint32_t kTmemQ = 128;  // d = 256 only
+constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in fa_fwd_kernel.cuh
+constexpr unsigned kStatusTimeout = 4;
+constexpr int kUnitSlots = 2;
+constexpr int kUnitConsumers = 7;  // warps 0-6 arrive once each per piece
+constexpr int kMinPage = 8;        // tokens per page at least: a swizzle atom of a tile
+enum : int { kRoleSoftmax = 1, kRoleTma = 2, kRoleMma = 3 };
+
+// Written by every CTA for the merge: the unit whose first piece is this CTA's last
+// one and which later CTAs continue (last_cta < 0: none).
+struct MergeInfo {
+    int last_cta;   // the CTA of the unit's last piece
+    int slot;       // partial slot of the first piece (the others: 2 * cta)
+    int rows;       // rows of the unit
+    int tok0, head0;  // its first token (of all tokens) and head
+    int pad[3];
+};
+
+struct Params {
+    void *O;
+    float *LSE;
+    float *part_O;     // [2 * CTAs][128][D]: O / l of the pieces of cut units
+    float *part_LSE;   // [2 * CTAs][128]
+    MergeInfo *info;   // [CTAs]
+    const int *cu_q;   // B + 1: sequence b owns tokens cu_q[b] .. cu_q[b+1] - 1
+    const int *seq_k;  // B: keys of each sequence, its new tokens included
+    const int *table;  // B x max_pages page numbers
+    int B, H, kv_group, pf, spaces, tpt;  // heads per unit; H / pf; tokens per unit
+    int total_q, max_pages, page_log2, num_pages;
+    int max_keys;      // max_pages pages of keys (a length above it counts as this)
+    int chunk;         // tokens per TMA box: min(page size, bn(D))
+    int wl, wr;        // key j visible to the query at position i iff i - wl <= j <= i + wr
+    float scale_log2;
+    int min_tiles;     // K/V tiles per CTA at least
+    unsigned long long wait_budget_ns;
+    unsigned int *status;
+    int fault_skip_k;  // test hook: every CTA skips the K load at this ring position (-1: none)
+};
+
+// Tiles are stored as regions of min(D, 64) columns with the swizzle of that row width.
+template <int D>
+struct Smem {
+    static constexpr int kCols = D < 64 ? D : 64;
+    static constexpr int kRowBytes = kCols * 2;
+    static constexpr int kRegions = D / kCols;
+    static constexpr int kQRegion = kBM * kRowBytes;
+    static constexpr int kKVRegion = bn(D) * kRowBytes;
+    static constexpr int kQBytes = kRegions * kQRegion;
+    static constexpr int kKVBytes = kRegions * kKVRegion;
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + kQBytes;
+    static constexpr int kV = kK + k_stages(D) * kKVBytes;
+    static constexpr int kBar = kV + v_stages(D) * kKVBytes;
+    static constexpr int kNumBars = 48;
+    static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag
+    static constexpr int kScan = kMisc + 16;           // 8 warp sums, start sequence and offset
+    static constexpr int kUnitRing = kScan + 48;       // kUnitSlots pieces
+    static constexpr int kBytes = kUnitRing + kUnitSlots * 64;
+    // more than half of the SM's shared memory: one CTA (and one holder of all 512
+    // TMEM columns) per SM
+    static constexpr int kAlloc = kBytes + 1024 > 120 * 1024 ? kBytes + 1024 : 120 * 1024;
+    static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+enum : int {
+    kBarQFull = 0,
+    kBarQEmpty = 1,
+    kBarKFull = 2,                         // + stage
+    kBarKEmpty = kBarKFull + kMaxStages,   // + stage
+    kBarVFull = kBarKEmpty + kMaxStages,   // + stage
+    kBarVEmpty = kBarVFull + kMaxStages,   // + stage
+    kBarSFull = kBarVEmpty + kMaxStages,   // + buffer (3)
+    kBarPFull = kBarSFull + kSBufs,        // + buffer (3)
+    kBarPVDone = kBarPFull + kSBufs,       // + parity of the block (2)
+    kBarODone = kBarPVDone + 2,
+    kBarOFree = kBarODone + 1,
+    kBarUnitFull = kBarOFree + 1,               // + slot (2)
+    kBarUnitEmpty = kBarUnitFull + kUnitSlots,  // + slot (2)
+    kBarDrain = kBarUnitEmpty + kUnitSlots,
+    kBarQReady = kBarDrain + 1,            // Q copied into TMEM (d = 256)
+    kNumBarsUsed = kBarQReady + 1,
+};
+static_assert(kNumBarsUsed <= Smem<256>::kNumBars, "barrier slots");
+
+// One piece of a unit: K/V tiles j0 .. j1 (none when j1 < j0: no row sees a key) of the
+// unit with tokens t0 .. t0 + ceil(rows / pf) - 1 of sequence b.
+struct Piece {
+    int b, sp, t0, rows;
+    int j0, j1;
+    int lo_key, hi_key;  // the first and last key that any row of the unit sees
+    int q_off, nk;       // token i of the sequence stands at key position i + q_off
+    int tok0;            // the unit's first token of all tokens
+    int slot;            // partial slot, or -1: the whole unit, written to O and LSE
+};
+static_assert(sizeof(Piece) <= 64, "ring slot");
+
+struct Seq {
+    int q0, nq, nk;
+};
+__device__ __forceinline__ Seq load_seq(int b, const Params &p) {
+    Seq s;
+    s.q0 = min(max(p.cu_q[b], 0), p.total_q);
+    s.nq = min(max(p.cu_q[b + 1], s.q0), p.total_q) - s.q0;
+    s.nk = min(max(p.seq_k[b], 0), p.max_keys);
+    return s;
+}
+
+// K/V tiles j0 .. j1 that the rows of token tile qb see, and the keys lo .. hi.
+template <int kBN>
+__device__ __forceinline__ void unit_range(const Seq &s, int qb, const Params &p, int &lo, int &hi,
+                                           int &j0, int &j1) {
+    const int t0 = qb * p.tpt, tl = min(t0 + p.tpt, s.nq) - 1;
+    const int q_off = s.nk - s.nq;
+    lo = max(0, t0 + q_off - p.wl);
+    hi = min(s.nk - 1, tl + q_off + p.wr);
+    j0 = lo / kBN;
+    j1 = hi < lo ? j0 - 1 : hi / kBN;
+}
+// A unit's share of the line of work: its tiles, and 1 when it has none (its rows are
+// written all the same).
+template <int kBN>
+__device__ __forceinline__ int unit_work(const Seq &s, int qb, const Params &p) {
+    int lo, hi, j0, j1;
+    unit_range<kBN>(s, qb, p, lo, hi, j0, j1);
+    return max(j1 - j0 + 1, 1);
+}
+
+__device__ __forceinline__ void record_timeout(const Params &p, volatile int *abort_flag, int role,
+                                               int unit) {
+    *abort_flag = 1;
+    if (atomicCAS(p.status, 0u, kStatusTimeout) == 0u) {
+        p.status[1] = static_cast<unsigned>(role);
+        p.status[2] = static_cast<unsigned>(unit);
+        p.status[3] = blockIdx.x;
+        __threadfence();
+    }
+}
+
+// 4-D tiled copy global -> shared, completion counted on mbarrier `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ unsigned warp_sum(unsigned v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Work of one head group of sequence b (every thread of the warp calls it with its own
+// b; b >= B gives 0). Long sequences, with many token tiles, are summed by the whole
+// warp one after the other.
+template <int kBN>
+__device__ __forceinline__ unsigned seq_work(int b, const Params &p) {
+    Seq s{0, 0, 0};
+    if (b < p.B) s = load_seq(b, p);
+    const int nqb = (s.nq + p.tpt - 1) / p.tpt;
+    unsigned w = 0;
+    constexpr int kOwn = 4;
+    if (nqb <= kOwn)
+        for (int qb = 0; qb < nqb; ++qb) w += unit_work<kBN>(s, qb, p);
+    unsigned todo = __ballot_sync(0xffffffffu, nqb > kOwn);
+    const int lane = threadIdx.x & 31;
+    while (todo != 0) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.nk, src)};
+        const int n = __shfl_sync(0xffffffffu, nqb, src);
+        unsigned part = 0;
+        for (int qb = lane; qb < n; qb += 32) part += unit_work<kBN>(o, qb, p);
+        part = warp_sum(part);
+        if (lane == src) w = part;
+    }
+    return w;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const Params p) {
+    using L = Smem<D>;
+    constexpr int kBN = bn(D);
+    constexpr uint32_t kTmemO = tmem_o(D);
+    constexpr int kSB = s_bufs(D);
+    constexpr bool kQT = q_in_tmem(D);
+    constexpr int kKStages = k_stages(D);
+    constexpr int kVStages = v_stages(D);
+    static_assert(kQT ? (kSB * kBN <= static_cast<int>(kTmemQ) && kTmemQ + D / 2 <= kTmemO)
+                      : kSB * kBN <= static_cast<int>(kTmemO),
+                  "TMEM columns");
+    static_assert(kTmemO + D <= kTmemCols, "TMEM columns");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sQ = sbase + L::kQ;
+    const uint32_t bar0 = sbase + L::kBar;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+    volatile unsigned *scan = reinterpret_cast<volatile unsigned *>(smem + L::kScan);
+    auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    auto sK = [sbase](int t) { return sbase + L::kK + (t % kKStages) * L::kKVBytes; };
+    auto sV = [sbase](int t) { return sbase + L::kV + (t % kVStages) * L::kKVBytes; };
+    auto slot_of = [smem](int k) {
+        return reinterpret_cast<Piece *>(smem + L::kUnitRing + (k % kUnitSlots) * 64);
+    };
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint64_t budget = p.wait_budget_ns;
+
+    // ---- this CTA's share of the line of work: tiles w0 .. w1 - 1 of W. B sequences are
+    // summed, and then searched for w0, 256 at a time.
+    auto block_sum = [&](unsigned v) -> unsigned {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) scan[warp] = v;
+        __syncthreads();
+        unsigned s = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) s += scan[i];
+        return s;
+    };
+    unsigned mine = 0, first = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const unsigned w = seq_work<kBN>(b0 + static_cast<int>(threadIdx.x), p) * p.spaces;
+        if (b0 == 0) first = w;
+        mine += w;
+    }
+    const unsigned W = block_sum(mine);
+    const unsigned T = max((W + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(p.min_tiles));
+    const unsigned w0 = min(blockIdx.x * T, W), w1 = min(w0 + T, W);
+    if (w0 >= w1) {  // nothing left for this CTA
+        if (threadIdx.x == 0) p.info[blockIdx.x].last_cta = -1;
+        return;
+    }
+    unsigned carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        const unsigned w = b0 == 0 ? first : seq_work<kBN>(b, p) * p.spaces;
+        unsigned incl = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        unsigned before = carry, all = carry;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += scan[i];
+            all += scan[i];
+        }
+        const unsigned lo = before + incl - w;
+        if (lo <= w0 && w0 < lo + w) {
+            scan[8] = static_cast<unsigned>(b);
+            scan[9] = w0 - lo;
+        }
+        carry = all;
+        if (w0 < carry) break;
+    }
+
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == kQKWarp * 32) {
+        mbar_init(bar(kBarQFull), 1);
+        // Q's shared-memory copy is released by the MMA warp's commit, or at d = 256
+        // by the softmax threads once they have copied it into TMEM
+        mbar_init(bar(kBarQEmpty), kQT ? 128 : 1);
+        mbar_init(bar(kBarQReady), 128);
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(bar(kBarKFull + s), 1);
+            mbar_init(bar(kBarKEmpty + s), 1);
+        }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(bar(kBarVFull + s), 1);
+            mbar_init(bar(kBarVEmpty + s), 1);
+        }
+        for (int b = 0; b < kSB; ++b) {
+            mbar_init(bar(kBarSFull + b), 1);
+            mbar_init(bar(kBarPFull + b), 128);
+        }
+        mbar_init(bar(kBarPVDone + 0), 1);
+        mbar_init(bar(kBarPVDone + 1), 1);
+        mbar_init(bar(kBarODone), 1);
+        mbar_init(bar(kBarOFree), 128);
+        for (int k = 0; k < kUnitSlots; ++k) {
+            mbar_init(bar(kBarUnitFull + k), 1);
+            mbar_init(bar(kBarUnitEmpty + k), kUnitConsumers);
+        }
+        mbar_init(bar(kBarDrain), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // The k-th piece of this CTA (every role walks the same pieces). b < 0: no more.
+    auto take = [&](int k, bool &ok) -> Piece {
+        Piece P{};
+        P.b = -1;
+        const int slot = k % kUnitSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarUnitFull + slot), (k / kUnitSlots) & 1,
+                                                       abort_flag, budget));
+        if (!ok) return P;
+        P = *slot_of(k);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarUnitEmpty + slot));
+        return P;
+    };
+
+    // Chunks of K/V tile j that hold a key of the piece's unit; chunk `lane`'s page and
+    // first token in it. Returns the ballot of the chunks to load.
+    auto chunk_of = [&](const Piece &P, int j, int &page, int &tok) -> uint32_t {
+        const int k0 = j * kBN + lane * p.chunk;
+        const bool need = lane * p.chunk < kBN && k0 + p.chunk > P.lo_key && k0 <= P.hi_key;
+        page = 0;
+        tok = k0 & ((1 << p.page_log2) - 1);
+        if (need) {
+            page = p.table[static_cast<size_t>(P.b) * p.max_pages + (k0 >> p.page_log2)];
+            // a page number outside the cache reads as zeros
+            if (page < 0 || page >= p.num_pages) page = p.num_pages;
+        }
+        return __ballot_sync(0xffffffffu, need);
+    };
+    auto load_chunks = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, uint32_t need, int page,
+                           int tok, int hkv) {
+        if (lane == 0)
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(need)) * p.chunk * L::kRowBytes *
+                                            L::kRegions);
+        __syncwarp();
+        if ((need >> lane) & 1u)
+            for (int g = 0; g < L::kRegions; ++g)
+                tma_load_4d(dst + g * L::kKVRegion + lane * p.chunk * L::kRowBytes, map, full,
+                            L::kCols * g, tok, hkv, page);
+        __syncwarp();
+    };
+
+    if (warp == kSchedWarp) {
+        // ================================================================ scheduler
+        if (lane == 0) {
+            int b = static_cast<int>(scan[8]), sp, qb = 0, rem;
+            Seq s = load_seq(b, p);
+            int nqb = (s.nq + p.tpt - 1) / p.tpt;
+            {
+                int per = 0;
+                for (int x = 0; x < nqb; ++x) per += unit_work<kBN>(s, x, p);
+                sp = static_cast<int>(scan[9]) / per;
+                rem = static_cast<int>(scan[9]) - sp * per;
+                for (; qb < nqb - 1; ++qb) {
+                    const int n = unit_work<kBN>(s, qb, p);
+                    if (rem < n) break;
+                    rem -= n;
+                }
+            }
+            unsigned w = w0;
+            bool ok = true;
+            MergeInfo info{};
+            info.last_cta = -1;
+            int k = 0;
+            for (; ok; ++k) {
+                const int slot = k % kUnitSlots;
+                ok = mbar_wait_bounded(bar(kBarUnitEmpty + slot), ((k / kUnitSlots) & 1) ^ 1, abort_flag,
+                                       budget);
+                if (!ok) break;
+                Piece P{};
+                P.b = -1;
+                if (w < w1) {
+                    int lo, hi, j0, j1;
+                    unit_range<kBN>(s, qb, p, lo, hi, j0, j1);
+                    const int n = max(j1 - j0 + 1, 1);
+                    const int len = min(n - rem, static_cast<int>(w1 - w));
+                    P.b = b;
+                    P.sp = sp;
+                    P.t0 = qb * p.tpt;
+                    P.rows = (min(P.t0 + p.tpt, s.nq) - P.t0) * p.pf;
+                    P.lo_key = lo;
+                    P.hi_key = hi;
+                    P.q_off = s.nk - s.nq;
+                    P.nk = s.nk;
+                    P.tok0 = s.q0 + P.t0;
+                    P.j0 = j0 + rem;
+                    P.j1 = j1 < j0 ? P.j0 - 1 : P.j0 + len - 1;
+                    const bool starts = rem == 0, ends = rem + len == n;
+                    P.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (k > 0);
+                    if (starts && !ends) {
+                        info.last_cta = static_cast<int>((w + n - 1) / T);
+                        info.slot = P.slot;
+                        info.rows = P.rows;
+                        info.tok0 = P.tok0;
+                        info.head0 = sp * p.pf;
+                    }
+                    w += len;
+                    rem = 0;
+                    if (++qb == nqb) {
+                        qb = 0;
+                        if (++sp == p.spaces) {
+                            sp = 0;
+                            while (w < w1 && ++b < p.B) {
+                                s = load_seq(b, p);
+                                nqb = (s.nq + p.tpt - 1) / p.tpt;
+                                if (nqb > 0) break;
+                            }
+                            if (b >= p.B) w = w1;
+                        }
+                    }
+                }
+                *slot_of(k) = P;
+                mbar_arrive(bar(kBarUnitFull + slot));
+                if (P.b < 0) break;
+            }
+            if (!ok) record_timeout(p, abort_flag, kRoleTma, k);
+            p.info[blockIdx.x] = info;
+        }
+    } else if (warp == kQKWarp) {
+        // ================================================================ Q and K
+        int t = 0, q_loads = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Piece P = take(k, ok);
+            if (!ok || P.b < 0) break;
+            if (P.j1 < P.j0) continue;
+            const int hkv = P.sp * p.pf / p.kv_group;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty), (q_loads & 1) ^ 1, abort_flag,
+                                                           budget));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(kBarQFull), static_cast<uint32_t>(p.pf * p.tpt) * L::kRowBytes *
+                                                          L::kRegions);
+                for (int g = 0; g < L::kRegions; ++g)
+                    tma_load_3d(sQ + g * L::kQRegion, &tmQ, bar(kBarQFull), L::kCols * g, P.sp * p.pf,
+                                P.tok0);
+            }
+            ++q_loads;
+            int page, tok;
+            uint32_t need = chunk_of(P, P.j0, page, tok);
+            for (int j = P.j0; j <= P.j1; ++j, ++t) {
+                const int st = t % kKStages;
+                // the next tile's page numbers are on their way while this one waits
+                int page_n = 0, tok_n = 0;
+                uint32_t need_n = 0;
+                if (j < P.j1) need_n = chunk_of(P, j + 1, page_n, tok_n);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarKEmpty + st), ((t / kKStages) & 1) ^ 1,
+                                                               abort_flag, budget));
+                if (!ok) break;
+                if (t != p.fault_skip_k) load_chunks(&tmK, sK(t), bar(kBarKFull + st), need, page, tok, hkv);
+                page = page_n;
+                tok = tok_n;
+                need = need_n;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) record_timeout(p, abort_flag, kRoleTma, -1);
+            if (q_loads > 0) mbar_wait_bounded(bar(kBarQFull), (q_loads - 1) & 1, nullptr, budget);
+            for (int s = 0; s < kKStages; ++s)
+                if (t > s) {
+                    const int last = t - 1 - ((t - 1 - s) % kKStages);
+                    mbar_wait_bounded(bar(kBarKFull + s), (last / kKStages) & 1, nullptr, budget);
+                }
+        }
+    } else if (warp == kVWarp) {
+        // ================================================================ V
+        int t = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Piece P = take(k, ok);
+            if (!ok || P.b < 0) break;
+            const int hkv = P.sp * p.pf / p.kv_group;
+            int page, tok;
+            uint32_t need = chunk_of(P, P.j0, page, tok);
+            for (int j = P.j0; j <= P.j1; ++j, ++t) {
+                const int st = t % kVStages;
+                int page_n = 0, tok_n = 0;
+                uint32_t need_n = 0;
+                if (j < P.j1) need_n = chunk_of(P, j + 1, page_n, tok_n);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarVEmpty + st), ((t / kVStages) & 1) ^ 1,
+                                                               abort_flag, budget));
+                if (!ok) break;
+                load_chunks(&tmV, sV(t), bar(kBarVFull + st), need, page, tok, hkv);
+                page = page_n;
+                tok = tok_n;
+                need = need_n;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) record_timeout(p, abort_flag, kRoleTma, -1);
+            for (int s = 0; s < kVStages; ++s)
+                if (t > s) {
+                    const int last = t - 1 - ((t - 1 - s) % kVStages);
+                    mbar_wait_bounded(bar(kBarVFull + s), (last / kVStages) & 1, nullptr, budget);
+                }
+        }
+    } else if (warp == kMmaWarp) {
+        // ================================================================ MMA issuer
+        constexpr uint32_t idesc_s = idesc_f16_ab(BF16, kBM, kBN, false, false);
+        constexpr uint32_t idesc_o = idesc_f16_ab(BF16, kBM, D, false, true);
+        constexpr int kSteps = L::kCols / 16;  // K-steps of 16 columns per region
+        auto wait = [&](int b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag, budget));
+        };
+        auto commit = [&](int b) {
+            if (elect_one()) umma_commit(bar(b));
+            __syncwarp();
+        };
+        // S(t) = Q K_t^T into S buffer t mod kSB; Q from shared memory, or from TMEM.
+        auto issue_s = [&](int t) {
+            tc_fence_after();
+            const uint64_t dq = swz_desc<L::kRowBytes>(sQ, 16);
+            const uint64_t dk = swz_desc<L::kRowBytes>(sK(t), 16);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t offq = (k / kSteps) * (L::kQRegion >> 4) + (k % kSteps) * 2;
+                    const uint32_t offk = (k / kSteps) * (L::kKVRegion >> 4) + (k % kSteps) * 2;
+                    if constexpr (kQT)
+                        umma_f16_ts(tmem + kTmemS + (t % kSB) * kBN, tmem + kTmemQ + k * 8, dk + offk,
+                                    idesc_s, k > 0 ? 1u : 0u);
+                    else
+                        umma_f16_ss(tmem + kTmemS + (t % kSB) * kBN, dq + offq, dk + offk, idesc_s,
+                                    k > 0 ? 1u : 0u);
+                }
+                umma_commit(bar(kBarSFull + t % kSB));
+            }
+            __syncwarp();
+        };
+        // O (+)= P(t) V_t, P read from the first kBN / 2 columns of S buffer t mod kSB.
+        auto issue_pv = [&](int t, bool first_tile) {
+            tc_fence_after();
+            const uint64_t dv = swz_desc<L::kRowBytes>(sV(t), L::kKVRegion);
+            const uint32_t acc0 = first_tile ? 0u : 1u;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kBN / 16; ++k)
+                    umma_f16_ts(tmem + kTmemO, tmem + kTmemS + (t % kSB) * kBN + k * 8,
+                                dv + k * ((16 * L::kRowBytes) >> 4), idesc_o, k > 0 ? 1u : acc0);
+                umma_commit(bar(kBarPVDone + (t & 1)));
+            }
+            __syncwarp();
+        };
+        // Rows of V tile t (keys kv0 ..) outside keys lo .. hi: 0 times whatever the page
+        // holds there must be 0.
+        auto zero_rows = [&](int t, int kv0, int lo, int hi) {
+            const int head = min(max(lo - kv0, 0), kBN), tail = min(max(hi + 1 - kv0, 0), kBN);
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            for (int g = 0; g < L::kRegions; ++g) {
+                uint8_t *base = smem + L::kV + (t % kVStages) * L::kKVBytes + g * L::kKVRegion;
+                for (int c = lane; c < head * (L::kRowBytes / 16); c += 32)
+                    *reinterpret_cast<uint4 *>(base + c * 16) = z;
+                for (int c = tail * (L::kRowBytes / 16) + lane; c < kBN * (L::kRowBytes / 16); c += 32)
+                    *reinterpret_cast<uint4 *>(base + c * 16) = z;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        int t = 0, live = 0;  // K/V tiles, and pieces with tiles, so far
+        bool ok = true;
+        int k = 0;
+        for (; ok; ++k) {
+            const Piece P = take(k, ok);
+            if (!ok || P.b < 0) break;
+            const int n = P.j1 - P.j0 + 1;
+            if (n <= 0) continue;
+            ok = wait(kQT ? kBarQReady : kBarQFull, live & 1);
+            for (int x = 0; ok && x < n && x < kSB; ++x) {
+                ok = wait(kBarKFull + (t + x) % kKStages, ((t + x) / kKStages) & 1);
+                if (ok) {
+                    issue_s(t + x);
+                    commit(kBarKEmpty + (t + x) % kKStages);  // K is read by S only
+                }
+            }
+            for (int x = 0; ok && x < n; ++x, ++t) {
+                ok = wait(kBarPFull + t % kSB, (t / kSB) & 1) &&
+                     wait(kBarVFull + t % kVStages, (t / kVStages) & 1);
+                if (ok && x == 0 && live > 0) ok = wait(kBarOFree, (live - 1) & 1);
+                if (!ok) break;
+                const int kv0 = (P.j0 + x) * kBN;
+                if (kv0 < P.lo_key || kv0 + kBN - 1 > P.hi_key) zero_rows(t, kv0, P.lo_key, P.hi_key);
+                issue_pv(t, x == 0);
+                commit(kBarVEmpty + t % kVStages);
+                if (x + kSB < n) {
+                    ok = wait(kBarKFull + (t + kSB) % kKStages, ((t + kSB) / kKStages) & 1);
+                    if (!ok) break;
+                    issue_s(t + kSB);  // reuses buffer t mod kSB after O += P(t) V_t
+                    commit(kBarKEmpty + (t + kSB) % kKStages);
+                }
+            }
+            if (!ok) break;
+            if constexpr (!kQT) commit(kBarQEmpty);
+            commit(kBarODone);
+            ++live;
+        }
+        if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleMma, k);
+        if (elect_one()) umma_commit(bar(kBarDrain));
+        __syncwarp();
+        if (lane == 0) mbar_wait_bounded(bar(kBarDrain), 0, nullptr, budget);
+        __syncwarp();
+    } else {
+        // ================================================================ softmax warpgroup
+        const int row = threadIdx.x & 127;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const float sl2 = p.scale_log2;
+        const int row_tok = row / p.pf, row_head = row - row_tok * p.pf;
+        // d = 256: copy the k-th live piece's Q tile from shared memory into TMEM, this
+        // thread's row into its lane (128-byte swizzle: 16-byte chunk c of row r sits
+        // at chunk c ^ (r mod 8) of the row), then release both copies' barriers.
+        auto copy_q = [&](int k) -> bool {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQFull), k & 1, abort_flag, budget)))
+                return false;
+#pragma unroll
+            for (int g = 0; g < L::kRegions; ++g) {
+                uint32_t w[32];
+                const uint8_t *src = smem + L::kQ + g * L::kQRegion + row * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) << 4));
+                    w[4 * c] = v.x;
+                    w[4 * c + 1] = v.y;
+                    w[4 * c + 2] = v.z;
+                    w[4 * c + 3] = v.w;
+                }
+                tmem_st32(tl + kTmemQ + g * 32, w);
+            }
+            tmem_st_wait();
+            mbar_arrive(bar(kBarQEmpty));
+            tc_fence_before();
+            mbar_arrive(bar(kBarQReady));
+            return true;
+        };
+        int k = 0;  // pieces taken
+        bool ok = true;
+        auto out_row = [&](const Piece &P) {
+            return (static_cast<size_t>(P.tok0) + row_tok) * p.H + P.sp * p.pf + row_head;
+        };
+        // The next piece with tiles (b < 0: none); pieces without get O = 0, LSE = -inf.
+        auto next_live = [&]() -> Piece {
+            while (true) {
+                const Piece P = take(k, ok);
+                ++k;
+                if (!ok || P.b < 0 || P.j0 <= P.j1) return P;
+                if (row < P.rows) {
+                    const size_t g = out_row(P);
+                    const uint32_t z[8] = {};
+                    uint8_t *orow = reinterpret_cast<uint8_t *>(p.O) + g * (D * 2);
+                    for (int c = 0; c < D / 16; ++c) st_global_v8(orow + c * 32, z);
+                    p.LSE[g] = -INFINITY;
+                }
+            }
+        };
+        int t = 0, live = 0;
+        Piece P = next_live();
+        if (ok && kQT && P.b >= 0) ok = copy_q(0);
+        while (ok && P.b >= 0) {
+            const int i = P.t0 + row_tok;
+            const bool active = row < P.rows;
+            const bool warp_active = warp * 32 < P.rows;
+            const int lo_i = max(0, i + P.q_off - p.wl);
+            const int hi_i = min(P.nk - 1, i + P.q_off + p.wr);
+            // a tile with keys in [lo_last, hi_first] only is visible to every row
+            const int tl_i = P.t0 + (P.rows - 1) / p.pf;
+            const int lo_last = max(0, tl_i + P.q_off - p.wl);
+            const int hi_first = min(P.nk - 1, P.t0 + P.q_off + p.wr);
+            float m = -INFINITY, l = 0.f;
+            for (int j = P.j0; j <= P.j1; ++j, ++t) {
+                const uint32_t tS = tl + kTmemS + (t % kSB) * kBN;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarSFull + t % kSB), (t / kSB) & 1,
+                                                               abort_flag, budget));
+                if (!ok) break;
+                if (!warp_active) {
+                    // no row here: S is passed on as it is (an MMA row depends on its own
+                    // A row alone, and these rows are not stored)
+                    mbar_arrive(bar(kBarPFull + t % kSB));
+                    continue;
+                }
+                tc_fence_after();
+                float x[kBN];
+                const int kv0 = j * kBN;
+                float m_tile;
+                if (kv0 >= lo_last && kv0 + kBN - 1 <= hi_first) {
+                    // every key visible: the TMEM loads reduce each 32-column run to
+                    // its maximum
+                    float mr[kBN / 32];
+#pragma unroll
+                    for (int h = 0; h < kBN; h += 64) {
+                        uint32_t a[32], b[32];
+                        tmem_ld32_max(tS + h, a, mr[h / 32]);
+                        tmem_ld32_max(tS + h + 32, b, mr[h / 32 + 1]);
+                        tmem_ld_max_wait(a, mr[h / 32]);
+                        tmem_ld_max_wait(b, mr[h / 32 + 1]);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            x[h + c] = __uint_as_float(a[c]);
+                            x[h + c + 32] = __uint_as_float(b[c]);
+                        }
+                    }
+                    float mm = mr[0];
+#pragma unroll
+                    for (int c = 1; c < kBN / 32; ++c) mm = fmaxf(mm, mr[c]);
+                    m_tile = mm * sl2;
+                } else {
+#pragma unroll
+                    for (int h = 0; h < kBN; h += 64) {
+                        uint32_t a[32], b[32];
+                        tmem_ld32(tS + h, a);
+                        tmem_ld32(tS + h + 32, b);
+                        tmem_ld_wait(a);
+                        tmem_ld_wait(b);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            x[h + c] = __uint_as_float(a[c]);
+                            x[h + c + 32] = __uint_as_float(b[c]);
+                        }
+                    }
+                    mask_outside_run(x, lo_i - kv0, hi_i - kv0, -INFINITY);
+                    float ma = fmaxf(x[0], x[1]), mb = fmaxf(x[2], x[3]);
+#pragma unroll
+                    for (int c = 4; c < kBN; c += 4) {
+                        ma = max3f(ma, x[c], x[c + 1]);
+                        mb = max3f(mb, x[c + 2], x[c + 3]);
+                    }
+                    m_tile = fmaxf(ma, mb) * sl2;
+                }
+                if (!active) m_tile = -INFINITY;  // a row that is not there moves no reference
+                const float m_old = m;
+                if (m_tile > m + kRescaleThreshold) m = m_tile;
+                const float corr = m != m_old ? ex2_approx(m_old - m) : 1.f;
+                const float nm = m == -INFINITY ? 0.f : -m;
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                for (int c = 0; c < kBN; c += 2) {
+                    ffma2(x[c], x[c + 1], sl2, sl2, nm, nm);
+                    x[c] = ex2_approx(x[c]);
+                    x[c + 1] = ex2_approx(x[c + 1]);
+                }
+#pragma unroll
+                for (int c = 0; c < kBN; c += 4) {
+                    fadd2(s0, s1, x[c], x[c + 1]);
+                    fadd2(s2, s3, x[c + 2], x[c + 3]);
+                }
+                // P(j) as 16-bit pairs over the first kBN / 2 columns of the buffer (the
+                // operand type of the product; l keeps the fp32 values)
+#pragma unroll
+                for (int h = 0; h < kBN; h += 64) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) pk[e] = pack2<BF16>(x[h + 2 * e], x[h + 2 * e + 1]);
+                    tmem_st16(tS + h / 2, pk);
+                    tmem_st16(tS + h / 2 + 16, pk + 16);
+                }
+                l = l * corr + ((s0 + s1) + (s2 + s3));
+                // The reference max moved: O holds the sum through block j-1 once that
+                // product completes; rescale this row's O before P(j) is released.
+                if (j > P.j0 && __any_sync(0xffffffffu, corr != 1.f)) {
+                    const int tp = t - 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarPVDone + (tp & 1)), (tp >> 1) & 1,
+                                                                   abort_flag, budget));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tl + kTmemO + c * 32, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[e + 1]);
+                            fmul2(a0, a1, corr, corr);
+                            o[e] = __float_as_uint(a0);
+                            o[e + 1] = __float_as_uint(a1);
+                        }
+                        tmem_st32(tl + kTmemO + c * 32, o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bar(kBarPFull + t % kSB));
+            }
+            if (!ok) break;
+            Piece N{};
+            if constexpr (kQT) {
+                // every S of this piece has completed (its last S buffer was read), so
+                // the next piece's Q can replace this one's in TMEM during the epilogue
+                N = next_live();
+                if (ok && N.b >= 0) ok = copy_q(live + 1);
+                if (!ok) break;
+            }
+            // ---- epilogue: O / l rounded to 16 bit, LSE = ln 2 (m + log2 l); a piece of
+            // a cut unit keeps both in fp32 for the merge
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarODone), live & 1, abort_flag, budget));
+            if (!ok) break;
+            if (warp_active) {
+                tc_fence_after();
+                const float inv_l = l == 0.f ? 0.f : 1.f / l;
+                const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+                if (P.slot < 0) {
+                    const size_t grow = out_row(P);
+                    uint8_t *orow = reinterpret_cast<uint8_t *>(p.O) + grow * (D * 2);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tl + kTmemO + c * 32, o);
+                        tmem_ld_wait(o);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = pack2<BF16>(__uint_as_float(o[2 * e]) * inv_l,
+                                                __uint_as_float(o[2 * e + 1]) * inv_l);
+                        if (l == 0.f)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = 0;
+                        if (active) {
+                            st_global_v8(orow + c * 64, pk);
+                            st_global_v8(orow + c * 64 + 32, pk + 8);
+                        }
+                    }
+                    if (active) p.LSE[grow] = lse;
+                } else {
+                    const size_t prow = static_cast<size_t>(P.slot) * kBM + row;
+                    float *orow = p.part_O + prow * D;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tl + kTmemO + c * 32, o);
+                        tmem_ld_wait(o);
+                        if (active) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv_l);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) st_global_v8(orow + c * 32 + q * 8, o + q * 8);
+                        }
+                    }
+                    if (active) p.part_LSE[prow] = lse;
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(kBarOFree));
+            ++live;
+            if constexpr (!kQT) N = next_live();
+            P = N;
+        }
+        if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleSoftmax, k);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the pieces of the cut units: block (c, y) the unit whose first piece is the last
+// one of CTA c, one warp per row. With O_s, LSE_s of piece s:
+//     LSE = ln sum_s exp(LSE_s)          O = sum_s exp(LSE_s - LSE) O_s
+// around the largest LSE_s, in the order of the pieces (the same result every time).
+struct MergeParams {
+    const MergeInfo *info;
+    const float *part_O, *part_LSE;
+    void *O;
+    float *LSE;
+    int H, pf;
+};
+
+constexpr int kMergeWarps = 8;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const MergeParams p) {
+    const int c = blockIdx.x;
+    const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const MergeInfo u = p.info[c];
+    if (u.last_cta < 0 || row >= u.rows) return;
+    constexpr int kV = D / 32;  // consecutive columns per lane
+    const int n = u.last_cta - c + 1;
+    auto prow = [&](int s) { return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * kBM + row; };
+    float m = -INFINITY;
+    bool bad = false;
+    for (int s = lane; s < n; s += 32) {
+        const float x = p.part_LSE[prow(s)];
+        bad |= x != x;
+        m = fmaxf(m, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    bad = __any_sync(0xffffffffu, bad);
+    float acc[kV];
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+    float wsum = 0.f, lse = -INFINITY;
+    if (m != -INFINITY || bad) {
+        for (int s0 = 0; s0 < n; s0 += 32) {
+            // every lane the weight of one piece; an empty piece (LSE = -inf) weighs 0
+            float w = 0.f;
+            if (s0 + lane < n) {
+                const float x = p.part_LSE[prow(s0 + lane)];
+                w = x == -INFINITY ? 0.f : expf(x - m);
+            }
+            const int ns = min(32, n - s0);
+#pragma unroll 4
+            for (int s = 0; s < ns; ++s) {
+                const float ws = __shfl_sync(0xffffffffu, w, s);
+                const float *o = p.part_O + prow(s0 + s) * D + lane * kV;
+                wsum += ws;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] = fmaf(ws, o[e], acc[e]);
+            }
+        }
+        const float inv = 1.f / wsum;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] *= inv;
+        lse = m + logf(wsum);
+    }
+    const int i = row / p.pf;
+    const size_t g = (static_cast<size_t>(u.tok0) + i) * p.H + u.head0 + (row - i * p.pf);
+    uint16_t *orow = reinterpret_cast<uint16_t *>(p.O) + g * D + lane * kV;
+    if constexpr (kV == 1) {
+        orow[0] = static_cast<uint16_t>(pack2<BF16>(acc[0], 0.f) & 0xffffu);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kV; e += 2)
+            *reinterpret_cast<uint32_t *>(orow + e) = pack2<BF16>(acc[e], acc[e + 1]);
+    }
+    if (lane == 0) p.LSE[g] = lse;
+}
+
+}  // namespace paged
+}  // namespace fa
