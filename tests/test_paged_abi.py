@@ -10,8 +10,18 @@ import pytest
 import torch
 
 import tiled_attention_03_gb300 as fa
-from tiled_attention_03_gb300.binding import FaNormRope, FaPagedCache, FaRows, load_library
+from tiled_attention_03_gb300.binding import FaNormRope, FaPagedCache, load_library
 from tiled_attention_03_gb300.build import build_library
+
+
+class FaRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("token", ctypes.c_int64)]
+
+
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
 
 INVALID, UNSUPPORTED = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
 AT = 0x10000000
@@ -47,7 +57,7 @@ def forward(lib, B=2, H=4, Hk=2, N=16, d=64, dtype=1, positions=0x93000000, r=No
     k = t.get("k", rows(1, Hk, N, d))
     y = t.get("y", rows(2, H, N, d))
     z = t.get("z", rows(3, Hk, N, d))
-    return lib.fa_qk_norm_rope(q, k, y, z, rope() if r is None else r, positions, B, H, Hk, N, d, dtype, None)
+    return lib.fa_qk_norm_rope(ref(q), ref(k), ref(y), ref(z), ref(rope() if r is None else r), positions, B, H, Hk, N, d, dtype, None)
 
 
 def test_a_good_forward_passes_the_checks(lib):
@@ -97,8 +107,8 @@ def backward(lib, B=2, H=4, Hk=2, N=16, d=64, dwq=0x94000000, dwk=0x95000000, r=
     x = [t.get(n, rows(i, Hk if n in ("k", "dz", "dk") else H, N, d)) for i, n in enumerate(names)]
     if ws_bytes is None:
         ws_bytes = lib.fa_qk_norm_rope_backward_workspace_bytes(d)
-    return lib.fa_qk_norm_rope_backward(*x, dwq, dwk, rope() if r is None else r, None, B, H, Hk, N, d, 1, ws, ws_bytes,
-                                        None)
+    return lib.fa_qk_norm_rope_backward(*map(ref, x), dwq, dwk, ref(rope() if r is None else r), None, B, H, Hk, N, d, 1,
+                                        ws, ws_bytes, None)
 
 
 def test_a_good_backward_passes_the_checks(lib):
@@ -132,7 +142,7 @@ def cache(**kw):
 
 def attend(lib, q=AT, o=AT + FAR, lse=AT + 2 * FAR, c=None, table=AT + 3 * FAR, pages=8, cu=AT + 4 * FAR,
            lens=AT + 5 * FAR, B=3, H=4, total=20, scale=0.125, mask=1, wl=0, wr=0, ws=AT + 6 * FAR, ws_bytes=1 << 26):
-    return lib.fa_forward_paged(q, o, lse, cache() if c is None else c, table, pages, cu, lens, B, H, total, scale, mask,
+    return lib.fa_forward_paged(q, o, lse, ref(cache() if c is None else c), table, pages, cu, lens, B, H, total, scale, mask,
                                 wl, wr, ws, ws_bytes, None)
 
 
@@ -141,7 +151,8 @@ def append(lib, H=4, B=3, total=20, table=AT + 5 * FAR, pages=8, cu=AT + 6 * FAR
     d = 64
     token = lambda i, h: FaRows(AT + i * FAR, 0, d, h * d)  # noqa: E731
     q, k, v, y = (t.get(n, token(i, h)) for i, (n, h) in enumerate((("q", H), ("k", 2), ("v", 2), ("y", H))))
-    return lib.fa_paged_append(q, k, v, y, cache() if c is None else c, table, pages, cu, lens, B, H, total, r, None)
+    return lib.fa_paged_append(ref(q), ref(k), ref(v), ref(y), ref(cache() if c is None else c), table, pages, cu, lens, B,
+                               H, total, ref(r), None)
 
 
 def test_good_paged_calls_pass_the_checks(lib):
@@ -215,7 +226,7 @@ def test_null_descriptors(lib):
     assert lib.fa_forward_paged(AT, AT, AT, None, None, 0, None, None, 1, 1, 1, 1.0, 0, 0, 0, None, 0, None) == INVALID
     assert lib.fa_paged_append(None, None, None, None, None, None, 0, None, None, 1, 1, 1, None, None) == INVALID
     assert lib.fa_qk_norm_rope(None, None, None, None, None, None, 1, 1, 1, 1, 64, 0, None) == INVALID
-    assert lib.fa_qk_norm_rope(None, None, None, None, rope(), None, 1, 1, 1, 1, 64, 0, None) == INVALID
+    assert lib.fa_qk_norm_rope(None, None, None, None, ref(rope()), None, 1, 1, 1, 1, 64, 0, None) == INVALID
 
 
 def test_binding_refuses_cpu_tensors():

@@ -12,6 +12,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 
 import torch
 
@@ -31,12 +32,6 @@ class FaError(RuntimeError):
     def __init__(self, status: int, what: str = "fa_forward"):
         self.status = status
         super().__init__(f"{what}: {fa_status_string(status)}")
-
-
-class FaRows(ctypes.Structure):
-    """fa_rows of include/fa.h: a (batch, head, token, d) tensor by its strides."""
-    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
-                ("token", ctypes.c_int64)]
 
 
 class FaNormRope(ctypes.Structure):
@@ -120,7 +115,9 @@ def load_library_at(path: str) -> ctypes.CDLL:
         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.fa_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_backward_workspace_bytes.argtypes = [ctypes.c_int64] * 4
-    rows, rope, cache = (ctypes.POINTER(t) for t in (FaRows, FaNormRope, FaPagedCache))
+    # descriptors are passed as addresses (a NormRope or PagedCache keeps its own; rows are
+    # packed bytes, see _rows): cheaper to make than a ctypes structure per call
+    rows = rope = cache = ctypes.c_void_p
     lib.fa_rope_steps.restype = ctypes.c_int
     lib.fa_rope_steps.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
     lib.fa_qk_norm_rope.restype = ctypes.c_int
@@ -193,7 +190,9 @@ def fa_test_arm_fault(kv_position: int) -> None:
 
 def _stream_handle(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -572,16 +571,19 @@ class NormRope:
         if any(w is not None and w.dtype not in _DTYPES for w in (q_weight, k_weight)):
             raise FaError(FA_ERR_INVALID_ARG, "NormRope")
         self.steps, self.q_weight, self.k_weight = steps, q_weight, k_weight
-        self._weights = [(w.dtype, w.numel()) for w in (q_weight, k_weight) if w is not None]
+        kinds = {(w.dtype, w.numel()) for w in (q_weight, k_weight) if w is not None}
+        if len(kinds) > 1:
+            raise FaError(FA_ERR_INVALID_ARG, "NormRope")
+        self._kind = kinds.pop() if kinds else None  # dtype and d of the weights
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self.c = FaNormRope(ptr(steps), 0 if steps is None else 2 * steps.numel(),
                             _LAYOUTS[layout], float(magnitude), ptr(q_weight), ptr(k_weight),
                             float(eps))
+        self.address = ctypes.addressof(self.c)
 
     def check(self, dtype, d: int, what: str) -> None:
-        for w in self._weights:
-            if w != (dtype, d):
-                raise FaError(FA_ERR_INVALID_ARG, what)
+        if self._kind is not None and self._kind != (dtype, d):
+            raise FaError(FA_ERR_INVALID_ARG, what)
 
 
 class PagedCache:
@@ -598,21 +600,25 @@ class PagedCache:
         self.num_pages, self.page_size, self.H_kv, self.d = k.shape
         ps, ts, hs = k.stride()[:3]
         self.c = FaPagedCache(k.data_ptr(), v.data_ptr(), ps, ts, hs, *k.shape, _DTYPES[k.dtype])
+        self.address = ctypes.addressof(self.c)
 
 
-_NO_ROWS = FaRows(None, 0, 0, 0)
+_FA_ROWS = struct.Struct("@Pqqq")  # fa_rows of include/fa.h: data and three strides
+_pack_rows = _FA_ROWS.pack
+_NO_ROWS = _pack_rows(0, 0, 0, 0)
 
 
-def _rows(t: torch.Tensor | None, dtype, what: str) -> FaRows:
-    """The descriptor of a (B, H, N, d) or token-major (tokens, H, d) tensor."""
+def _rows(t: torch.Tensor | None, dtype, what: str) -> bytes:
+    """The descriptor (fa_rows) of a (B, H, N, d) or token-major (tokens, H, d) tensor; the
+    library checks where its memory is."""
     if t is None:
         return _NO_ROWS
     s = t.stride()
-    if not t.is_cuda or t.dtype != dtype or s[-1] != 1:
+    if t.dtype is not dtype or s[-1] != 1:
         raise FaError(FA_ERR_INVALID_ARG, what)
     if len(s) == 4:
-        return FaRows(t.data_ptr(), s[0], s[1], s[2])
-    return FaRows(t.data_ptr(), 0, s[1], s[0])
+        return _pack_rows(t.data_ptr(), s[0], s[1], s[2])
+    return _pack_rows(t.data_ptr(), 0, s[1], s[0])
 
 
 def _qk_sizes(q, k, what: str):
@@ -638,7 +644,7 @@ def _same_shape(a, b, what: str) -> None:
 def _int32(t: torch.Tensor | None, numel: int, what: str):
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.numel() != numel or not t.is_contiguous():
         raise FaError(FA_ERR_INVALID_ARG, what)
     return t.data_ptr()
 
@@ -671,7 +677,7 @@ def fa_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch
     rope.check(dtype, d, what)
     rc = load_library().fa_qk_norm_rope(
         _rows(q, dtype, what), _rows(k, dtype, what), _rows(q_out, dtype, what),
-        _rows(k_out, dtype, what), rope.c, _int32(positions, B * N, what), B, H, H_kv, N, d,
+        _rows(k_out, dtype, what), rope.address, _int32(positions, B * N, what), B, H, H_kv, N, d,
         _DTYPES[dtype], _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, what)
@@ -720,7 +726,7 @@ def fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
     rc = lib.fa_qk_norm_rope_backward(
         _rows(q, dtype, what), _rows(k, dtype, what), _rows(dq_out, dtype, what),
         _rows(dk_out, dtype, what), _rows(dq, dtype, what), _rows(dk, dtype, what), ptr(dq_weight),
-        ptr(dk_weight), rope.c, _int32(positions, B * N, what), B, H, H_kv, N, d, _DTYPES[dtype],
+        ptr(dk_weight), rope.address, _int32(positions, B * N, what), B, H, H_kv, N, d, _DTYPES[dtype],
         ws, n, _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, what)
@@ -770,8 +776,8 @@ def fa_paged_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
     rc = load_library().fa_paged_append(
         _rows(q, dtype, what), _rows(k, dtype, what), _rows(v, dtype, what),
-        _rows(q_out, dtype, what), cache.c, table, pages, cu, lens, B,
-        0 if q is None else q.shape[1], total, None if rope is None else rope.c,
+        _rows(q_out, dtype, what), cache.address, table, pages, cu, lens, B,
+        0 if q is None else q.shape[1], total, None if rope is None else rope.address,
         _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, what)
@@ -802,7 +808,7 @@ def fa_forward_paged(q: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, cache:
     ws, n, keep = _workspace(
         workspace, lib.fa_forward_paged_workspace_bytes(cache.d) if workspace is None else 0, q,
         stream, what)
-    rc = lib.fa_forward_paged(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache.c, table, pages, cu,
+    rc = lib.fa_forward_paged(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache.address, table, pages, cu,
                               lens, B, shape[1], shape[0], float(scale), _MASKS[mask_mode],
                               int(window_left), int(window_right), ws, n, _stream_handle(stream))
     if rc != FA_OK:

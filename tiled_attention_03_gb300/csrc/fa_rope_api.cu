@@ -155,27 +155,29 @@ int mode_of(const fa_norm_rope &r) {
     return r.rotary_dim % 16 == 0 ? fa::rope::kLane : fa::rope::kAnywhere;
 }
 
-// Tokens and heads per block. Few rows: one row per group and a token per block, so that
-// they spread over the SMs; many: about eight rows per group, so that the cosines and
-// coefficients of a token serve several heads.
-void set_blocks(Params &p, int64_t d, int heads, int sms) {
-    const int groups = fa::rope::kThreads / static_cast<int>(d / 8);
-    if (p.tokens * heads <= static_cast<int64_t>(groups) * sms * 4) {
-        p.T = 1;
-        p.chunk = groups < heads ? groups : heads;
-    } else {
-        int T = 1;
-        while (T < fa::rope::kMaxTokens && T < groups && T * heads < 8 * groups) T *= 2;
-        p.T = T;
-        p.chunk = heads;
-    }
-    p.chunks = (heads + p.chunk - 1) / p.chunk;
-    p.tiles = (p.tokens + p.T - 1) / p.T * p.chunks;
+// Stages of a token and items (see the kernels): a whole token per warp, which computes its
+// angles once, or parts of it when the tokens alone would leave warps of the launch idle.
+void set_items(Params &p, int64_t d, int rows, int most_blocks) {
+    const int heads = static_cast<int>(256 / d) * rows;  // of a stage
+    auto stages = [heads](int h) { return (h + heads - 1) / heads; };
+    p.s_q = stages(p.H);
+    p.s_k = stages(p.H_kv);
+    p.s_v = stages(p.H_v);
+    const int all = p.s_q + p.s_k + p.s_v;
+    const int64_t warps = static_cast<int64_t>(most_blocks) * fa::rope::kWarps;
+    int64_t chunks = warps / p.tokens;
+    chunks = chunks < 1 ? 1 : chunks > all ? all : chunks;
+    p.per_item = static_cast<int>((all + chunks - 1) / chunks);
+    p.chunks = (all + p.per_item - 1) / p.per_item;
+    p.items = static_cast<int64_t>(p.tokens) * p.chunks;
+}
+unsigned blocks_of(const Params &p, int most_blocks) {
+    const int64_t b = (p.items + fa::rope::kWarps - 1) / fa::rope::kWarps;
+    return static_cast<unsigned>(b < most_blocks ? b : most_blocks);
 }
 
 template <int D, bool BF16, bool PAGED>
-void forward_mode(const Params &p, int mode, cudaStream_t st) {
-    const unsigned g = static_cast<unsigned>(p.tiles);
+void forward_mode(const Params &p, int mode, unsigned g, cudaStream_t st) {
     if (mode == fa::rope::kBeside)
         fa::rope::fa_norm_rope_kernel<D, BF16, fa::rope::kBeside, PAGED><<<g, fa::rope::kThreads, 0, st>>>(p);
     else if (mode == fa::rope::kLane)
@@ -193,15 +195,15 @@ void backward_mode(const Params &p, int mode, unsigned g, cudaStream_t st) {
         fa::rope::fa_norm_rope_bwd_kernel<D, BF16, fa::rope::kAnywhere><<<g, fa::rope::kThreads, 0, st>>>(p);
 }
 template <bool PAGED>
-cudaError_t forward(const Params &p, int64_t d, bool bf16, int mode, cudaStream_t st) {
+cudaError_t forward(const Params &p, int64_t d, bool bf16, int mode, unsigned g, cudaStream_t st) {
     if (d == 32)
-        bf16 ? forward_mode<32, true, PAGED>(p, mode, st) : forward_mode<32, false, PAGED>(p, mode, st);
+        bf16 ? forward_mode<32, true, PAGED>(p, mode, g, st) : forward_mode<32, false, PAGED>(p, mode, g, st);
     else if (d == 64)
-        bf16 ? forward_mode<64, true, PAGED>(p, mode, st) : forward_mode<64, false, PAGED>(p, mode, st);
+        bf16 ? forward_mode<64, true, PAGED>(p, mode, g, st) : forward_mode<64, false, PAGED>(p, mode, g, st);
     else if (d == 128)
-        bf16 ? forward_mode<128, true, PAGED>(p, mode, st) : forward_mode<128, false, PAGED>(p, mode, st);
+        bf16 ? forward_mode<128, true, PAGED>(p, mode, g, st) : forward_mode<128, false, PAGED>(p, mode, g, st);
     else
-        bf16 ? forward_mode<256, true, PAGED>(p, mode, st) : forward_mode<256, false, PAGED>(p, mode, st);
+        bf16 ? forward_mode<256, true, PAGED>(p, mode, g, st) : forward_mode<256, false, PAGED>(p, mode, g, st);
     return cudaGetLastError();
 }
 cudaError_t backward(const Params &p, int64_t d, bool bf16, int mode, unsigned g, cudaStream_t st) {
@@ -216,8 +218,9 @@ cudaError_t backward(const Params &p, int64_t d, bool bf16, int mode, unsigned g
     return cudaGetLastError();
 }
 
-// Blocks of a backward launch at most: what fills the SMs. Each leaves 2 d partial sums.
-constexpr int kBlocksPerSm = 4;
+// Resident blocks per SM (the kernels' launch bounds): the blocks of a launch at most.
+constexpr int kBlocksPerSm = 3;
+constexpr int kBackwardBlocksPerSm = 2;  // each leaves 2 d partial sums
 
 int sm_count_or_default() {
     int dev = 0, sms = 152;
@@ -298,13 +301,13 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
     p.H = static_cast<int>(H);
     p.H_kv = static_cast<int>(H_kv);
     p.N = static_cast<int>(N);
-    p.tokens = B * N;
+    p.tokens = static_cast<int>(B * N);
     p.positions = positions;
     set_rope(p, *rope);
-    set_blocks(p, d, p.H + p.H_kv, di.sm_count);
-    if (p.tiles > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    if (forward<false>(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), static_cast<cudaStream_t>(stream)) !=
-        cudaSuccess)
+    const int most = di.sm_count * kBlocksPerSm;
+    set_items(p, d, fa::rope::kRows, most);
+    if (forward<false>(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks_of(p, most),
+                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
     fa_host::count_launches(1);
     return FA_OK;
@@ -312,7 +315,7 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
 
 size_t fa_qk_norm_rope_backward_workspace_bytes(int64_t d) {
     if (!known(d)) return 0;
-    return static_cast<size_t>(sm_count_or_default()) * kBlocksPerSm * 2 * static_cast<size_t>(d) * sizeof(float);
+    return static_cast<size_t>(sm_count_or_default()) * kBackwardBlocksPerSm * 2 * static_cast<size_t>(d) * sizeof(float);
 }
 
 fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_rows *dq_out,
@@ -382,15 +385,15 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
     p.H = static_cast<int>(H);
     p.H_kv = static_cast<int>(H_kv);
     p.N = static_cast<int>(N);
-    p.tokens = B * N;
+    p.tokens = static_cast<int>(B * N);
     p.positions = positions;
     set_rope(p, *rope);
     if (!wq) p.wq = nullptr;
     if (!wk) p.wk = nullptr;
     p.part = wq || wk ? static_cast<float *>(workspace) : nullptr;
-    set_blocks(p, d, p.H + p.H_kv, di.sm_count);
-    const int64_t most = static_cast<int64_t>(di.sm_count) * kBlocksPerSm;
-    const unsigned blocks = static_cast<unsigned>(p.tiles < most ? p.tiles : most);
+    const int most = di.sm_count * kBackwardBlocksPerSm;
+    set_items(p, d, 1, most);
+    const unsigned blocks = blocks_of(p, most);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (backward(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks, st) != cudaSuccess) return FA_ERR_CUDA;
     fa_host::count_launches(1);
@@ -470,7 +473,7 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     p.H = static_cast<int>(H);
     p.H_kv = p.H_v = static_cast<int>(H_kv);
     p.N = static_cast<int>(total_q);
-    p.tokens = total_q;
+    p.tokens = static_cast<int>(total_q);
     set_rope(p, r);
     p.kc = static_cast<uint16_t *>(cache->k);
     p.vc = static_cast<uint16_t *>(cache->v);
@@ -484,10 +487,10 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     p.max_pages = static_cast<int>(max_pages);
     while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
     p.num_pages = static_cast<int>(cache->num_pages);
-    set_blocks(p, d, p.H + p.H_kv + p.H_v, di.sm_count);
-    if (p.tiles > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    if (forward<true>(p, d, cache->dtype == FA_DTYPE_BF16, mode_of(r), static_cast<cudaStream_t>(stream)) !=
-        cudaSuccess)
+    const int most = di.sm_count * kBlocksPerSm;
+    set_items(p, d, fa::rope::kRows, most);
+    if (forward<true>(p, d, cache->dtype == FA_DTYPE_BF16, mode_of(r), blocks_of(p, most),
+                      static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
     fa_host::count_launches(1);
     return FA_OK;
