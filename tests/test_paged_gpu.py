@@ -105,9 +105,9 @@ def test_masks_and_lengths(lens, mask, window, d, dtype):
 
 @pytest.mark.parametrize("page", [8, 16, 64, 128, 512])
 @pytest.mark.parametrize("layout", ["token", "head", "both"])
-@pytest.mark.parametrize("d", [64, 128, 256])
-def test_pages(page, layout, d):
-    lens = [(1, 600), (20, 130), (1, 127), (3, 1025)]
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("lens", [[(1, 600), (20, 130), (1, 127), (3, 1025)], [(1, 600), (1, 7), (2, 1025)]])
+def test_pages(lens, page, layout, d):
     b = paged(lens, 6, 2, d, torch.bfloat16, page, layout, seed=page)
     o, lse = run(*b[:5], d ** -0.5, "causal")
     check(o, lse, b[5], d ** -0.5, "causal", (0, 0), torch.bfloat16)
@@ -123,19 +123,22 @@ def test_heads(H, Hk):
 
 @pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float16), (256, torch.bfloat16)])
 @pytest.mark.parametrize("mask,window", [("causal", (0, 0)), ("window", (20000, 0))])
-def test_long_sequences_are_cut_and_joined(d, dtype, mask, window):
-    """A unit of 300 tiles over all CTAs, with short ones around it."""
-    b = paged([(1, 40), (2, 38500), (1, 2000)], 4, 1, d, dtype, 64, "head", seed=1)
+@pytest.mark.parametrize("new", [2, 50])
+def test_long_sequences_are_cut_and_joined(new, d, dtype, mask, window):
+    """A unit of some hundred tiles over all workers, with short ones around it."""
+    b = paged([(1, 40), (new, 38500), (1, 2000)], 4, 1, d, dtype, 64, "head", seed=1)
     o, lse = run(*b[:5], d ** -0.5, mask, window)
     check(o, lse, b[5], d ** -0.5, mask, window, dtype)
     again = run(*b[:5], d ** -0.5, mask, window)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
-def test_many_sequences():
+@pytest.mark.parametrize("new", [[0, 1, 1, 1, 2, 30], [0, 1, 1, 1, 2]])
+@pytest.mark.parametrize("H,Hk", [(4, 2), (24, 1)])
+def test_many_sequences(H, Hk, new):
     rng = random.Random(3)
-    lens = [(rng.choice([0, 1, 1, 1, 2, 30]), rng.choice([0, 1, 50, 400])) for _ in range(700)]
-    b = paged(lens, 4, 2, 64, torch.bfloat16, 16, seed=9)
+    lens = [(rng.choice(new), rng.choice([0, 1, 50, 400])) for _ in range(700)]
+    b = paged(lens, H, Hk, 64, torch.bfloat16, 16, seed=9)
     o, lse = run(*b[:5], 0.125, "causal")
     check(o, lse, b[5], 0.125, "causal", (0, 0), torch.bfloat16)
 
@@ -146,19 +149,23 @@ def test_long_prompt_chunk():
     check(o, lse, b[5], 128 ** -0.5, "causal", (0, 0), torch.bfloat16)
 
 
-def test_peaky_scores():
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_peaky_scores(d, new):
     """Scores of a few hundred: the reference maximum moves and O is rescaled."""
-    d, dtype = 128, torch.bfloat16
-    b = paged([(1, 900), (40, 700)], 4, 4, d, dtype, 16, seed=6)
+    dtype = torch.bfloat16
+    b = paged([(1, 900), (new, 700)], 4, 4, d, dtype, 16, seed=6)
     o, lse = run(*b[:5], 3.0, "causal")
     check(o, lse, b[5], 3.0, "causal", (0, 0), dtype)
 
 
-def test_window_does_not_look_at_what_it_left_behind():
+@pytest.mark.parametrize("H", [8, 80])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_window_does_not_look_at_what_it_left_behind(d, H):
     """Before the window of the only query, a page may have been given away: NaN in its
     keys and values and a nonsense page number change nothing."""
-    d, dtype, page = 128, torch.bfloat16, 16
-    q, cache, table, cu, lens, seqs = paged([(1, 500), (1, 300)], 8, 2, d, dtype, page, seed=8)
+    dtype, page = torch.bfloat16, 16
+    q, cache, table, cu, lens, seqs = paged([(1, 500), (1, 300)], H, 2, d, dtype, page, seed=8)
     want = run(q, cache, table, cu, lens, 0.1, "window", (100, 0))
     for b, n in ((0, 500), (1, 300)):
         first = n - 1 - 100
@@ -171,16 +178,18 @@ def test_window_does_not_look_at_what_it_left_behind():
     check(*got, seqs, 0.1, "window", (100, 0), dtype)
 
 
-def test_nan_in_a_visible_key_is_seen():
-    q, cache, table, cu, lens, _ = paged([(1, 200), (1, 200)], 2, 1, 64, torch.float16, 16, seed=2)
+@pytest.mark.parametrize("H", [2, 40])
+def test_nan_in_a_visible_key_is_seen(H):
+    q, cache, table, cu, lens, _ = paged([(1, 200), (1, 200)], H, 1, 64, torch.float16, 16, seed=2)
     cache.k[int(table[0, 3]), 5] = NAN
     o, lse = run(q, cache, table, cu, lens, 0.125, "causal")
     assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
     assert bool(torch.isfinite(o[1]).all()) and bool(torch.isfinite(lse[1]).all())
 
 
-def test_page_numbers_outside_the_cache_read_as_zeros():
-    q, cache, table, cu, lens, _ = paged([(1, 40)], 2, 2, 64, torch.bfloat16, 16, seed=2)
+@pytest.mark.parametrize("H", [2, 40])
+def test_page_numbers_outside_the_cache_read_as_zeros(H):
+    q, cache, table, cu, lens, _ = paged([(1, 40)], H, 2, 64, torch.bfloat16, 16, seed=2)
     zero_k, zero_v = cache.k.clone(), cache.v.clone()
     zero_k[int(table[0, 1])] = 0
     zero_v[int(table[0, 1])] = 0
@@ -369,6 +378,7 @@ def test_capture_follows_the_lengths():
             graph.replay()
         torch.cuda.synchronize()
         got = o.clone(), lse.clone()
+        o.fill_(NAN)
         step(other)
         torch.cuda.synchronize()
         assert torch.equal(got[0], o) and torch.equal(got[1], lse)
@@ -376,10 +386,11 @@ def test_capture_follows_the_lengths():
     assert fa.fa_sync_status() == fa.FA_OK
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("new", [1, 60])
+def test_two_streams_at_once(new):
     """Two calls that may overlap, without a workspace of the caller's, on streams of their
     own; many times, against the same calls one after the other."""
-    bs = [paged([(1, 3000), (5, 700)], 8, 2, 128, torch.bfloat16, 16, seed=i) for i in range(2)]
+    bs = [paged([(new, 3000), (2, 700)], 8, 2, 128, torch.bfloat16, 16, seed=i) for i in range(2)]
     want = [run(*b[:5], 0.1, "causal") for b in bs]
     streams = [torch.cuda.Stream() for _ in bs]
     torch.cuda.synchronize()
@@ -396,7 +407,7 @@ def test_two_streams_at_once():
 def test_the_fault_hook_ends_in_a_timeout():
     """A K load that never comes: the waits run out, the call reports it, and the next
     call is right."""
-    b = paged([(1, 600)], 2, 1, 128, torch.bfloat16, 16, seed=3)
+    b = paged([(40, 600)], 2, 1, 128, torch.bfloat16, 16, seed=3)
     want = run(*b[:5], 0.1, "causal")
     fa.fa_set_wait_budget_ns(20_000_000)
     try:

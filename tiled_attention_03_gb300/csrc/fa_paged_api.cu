@@ -9,6 +9,7 @@
 
 #include "fa.h"
 #include "fa_host.h"
+#include "fa_paged_decode_kernel.cuh"
 #include "fa_paged_host.h"
 #include "fa_paged_kernel.cuh"
 
@@ -18,9 +19,9 @@ using fa_host::align256;
 
 constexpr int kMaxDevices = 64;
 
-// K/V tiles per CTA at least: shares of one tile (a merge of as many pieces) measured
-// no slower than longer ones at small sizes.
+// Shares at least, in K/V tiles (chunk kernel) and ticks (decode kernel).
 constexpr int kMinTiles = 1;
+constexpr int kMinTicks = 8;
 
 struct Configured {
     std::once_flag once;
@@ -30,9 +31,13 @@ Configured g_configured[kMaxDevices];
 
 template <int D, bool BF16>
 cudaError_t opt_in() {
-    return cudaFuncSetAttribute(fa::paged::fa_paged_kernel<D, BF16>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                fa::paged::Smem<D>::kAlloc);
+    const cudaError_t e = cudaFuncSetAttribute(fa::paged::fa_paged_kernel<D, BF16>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               fa::paged::Smem<D>::kAlloc);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(fa::paged::fa_paged_decode_kernel<D, BF16>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   fa::paged::Small<D>::kBytes);
 }
 
 bool configured(int dev) {
@@ -51,29 +56,57 @@ bool configured(int dev) {
     return c.err == cudaSuccess;
 }
 
-// Two partial results of 128 rows per CTA, and what the merge needs to know of each CTA.
+// Two partial results per worker, and what the merge needs to know of each. The chunk
+// kernel has a worker of 128 rows per SM, the decode kernel eight (four at d = 256) of 16.
+constexpr int kMaxWorkersPerSm = 8;
+static_assert(fa::paged::kBM == kMaxWorkersPerSm * fa::paged::kSmallRows, "one layout for both kernels");
 struct Layout {
     size_t lse, o, bytes;  // info at 0
 };
-Layout layout_of(int64_t d, int64_t ctas) {
+Layout layout_of(int64_t d, int64_t sms) {
+    const size_t rows = static_cast<size_t>(2 * sms) * fa::paged::kBM;
     Layout l;
-    l.lse = align256(static_cast<size_t>(ctas) * sizeof(fa::paged::MergeInfo));
-    l.o = l.lse + align256(static_cast<size_t>(2 * ctas) * fa::paged::kBM * sizeof(float));
-    l.bytes = l.o + static_cast<size_t>(2 * ctas) * fa::paged::kBM * static_cast<size_t>(d) * sizeof(float);
+    l.lse = align256(static_cast<size_t>(sms) * kMaxWorkersPerSm * sizeof(fa::paged::MergeInfo));
+    l.o = l.lse + align256(rows * sizeof(float));
+    l.bytes = l.o + rows * static_cast<size_t>(d) * sizeof(float);
     return l;
+}
+
+// The merge, launched while the attention kernel runs (see wait_for_previous_grid).
+template <int D, bool BF16, int kRows>
+cudaError_t launch_merge(const fa::paged::MergeParams &m, unsigned blocks, cudaStream_t st) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(fa::paged::kMergeWarps * 32);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa::paged::fa_paged_merge_kernel<D, BF16, kRows>, m);
 }
 
 template <int D, bool BF16>
 cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                   const fa::paged::Params &p, const fa::paged::MergeParams &m, unsigned ctas,
-                   unsigned row_blocks, cudaStream_t st) {
+                   const fa::paged::Params &p, fa::paged::MergeParams m, unsigned sms, cudaStream_t st) {
     fa::paged::fa_paged_kernel<D, BF16>
-        <<<ctas, fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st>>>(q, k, v, p);
-    cudaError_t e = cudaGetLastError();
+        <<<sms, fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st>>>(q, k, v, p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    fa::paged::fa_paged_merge_kernel<D, BF16>
-        <<<dim3(ctas, row_blocks), fa::paged::kMergeWarps * 32, 0, st>>>(m);
-    return cudaGetLastError();
+    m.workers = static_cast<int>(sms);
+    return launch_merge<D, BF16, fa::paged::kBM>(m, sms, st);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_decode(const fa::paged::SmallParams &p, fa::paged::MergeParams m, unsigned sms,
+                          cudaStream_t st) {
+    using L = fa::paged::Small<D>;
+    fa::paged::fa_paged_decode_kernel<D, BF16><<<sms, L::kWarps * 32, L::kBytes, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    m.workers = static_cast<int>(sms) * L::kWarps;
+    return launch_merge<D, BF16, fa::paged::kSmallRows>(m, sms * L::kWarps / 2, st);
 }
 
 int sm_count_or_default() {
@@ -110,7 +143,10 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     int64_t pf = group;
     if (pf > fa::paged::kBM)
         for (pf = fa::paged::kBM; group % pf != 0;) --pf;
-    const int64_t tpt = fa::paged::kBM / pf, spaces = H / pf;
+    // Few tokens per sequence on average: the decode kernel, 16 rows per unit. A longer
+    // sequence among them is cut into more units, each reading its keys again.
+    const bool decode = pf <= fa::paged::kSmallRows && total_q * pf <= B * fa::paged::kSmallRows;
+    const int64_t tpt = (decode ? fa::paged::kSmallRows : fa::paged::kBM) / pf, spaces = H / pf;
     const int64_t max_keys = max_pages * cache->page_size;
     // Size limits of this implementation: 32-bit token and key indices, and a line of
     // work below 2^31 tiles.
@@ -118,11 +154,11 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     if (total_q > kLimit || max_pages > kLimit || max_keys > kLimit || B > kLimit || H > kLimit ||
         total_q * H > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;
-    const double tiles = static_cast<double>(max_keys / fa::paged::bn(static_cast<int>(d)) + 2);
+    const int64_t tile = decode ? (d <= 64 ? 32 : 16) : fa::paged::bn(static_cast<int>(d));
+    const double tiles = static_cast<double>(max_keys / tile + 2 + fa::paged::kUnitTicks);
     if (static_cast<double>(spaces) * static_cast<double>(total_q / tpt + B) * tiles > 2147483647.0)
         return FA_ERR_UNSUPPORTED;
-    const int ctas_needed = sm_count_or_default();
-    const Layout lay = layout_of(d, ctas_needed);
+    const Layout lay = layout_of(d, sm_count_or_default());
     if (workspace == nullptr || !fa_host::aligned32(workspace) || workspace_bytes < lay.bytes)
         return FA_ERR_INVALID_ARG;
     const size_t tbytes = static_cast<size_t>(total_q) * H * d * 2;
@@ -159,6 +195,73 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     if (!configured(dev)) return FA_ERR_CUDA;
 
     const bool bf16 = cache->dtype == FA_DTYPE_BF16;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned sms = static_cast<unsigned>(di.sm_count);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    int page_log2 = 0;
+    while ((int64_t{1} << page_log2) < cache->page_size) ++page_log2;
+    // "all keys" is a window wider than any offset
+    const int64_t every = total_q + max_keys;
+    int64_t wl = every, wr = every;
+    if (mask_mode == FA_MASK_CAUSAL) wr = 0;
+    if (mask_mode == FA_MASK_WINDOW) {
+        wl = window_left < every ? window_left : every;
+        wr = window_right < every ? window_right : every;
+    }
+    const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    fa::paged::MergeParams m{};
+    m.info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
+    m.part_LSE = reinterpret_cast<float *>(ws + lay.lse);
+    m.part_O = reinterpret_cast<float *>(ws + lay.o);
+    m.O = O;
+    m.LSE = LSE;
+    m.H = static_cast<int>(H);
+    m.pf = static_cast<int>(pf);
+    cudaError_t e;
+    const int fault = fa_host::take_fault_position();  // the decode kernel has no wait to run out
+    if (decode) {
+        fa::paged::SmallParams p{};
+        p.Q = static_cast<const uint16_t *>(Q);
+        p.O = O;
+        p.LSE = LSE;
+        p.part_O = reinterpret_cast<float *>(ws + lay.o);
+        p.part_LSE = reinterpret_cast<float *>(ws + lay.lse);
+        p.info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
+        p.k = static_cast<const uint16_t *>(cache->k);
+        p.v = static_cast<const uint16_t *>(cache->v);
+        p.page_stride = cache->page_stride;
+        p.token_stride = cache->token_stride;
+        p.head_stride = cache->head_stride;
+        p.cu_q = cu_q;
+        p.seq_k = seq_k;
+        p.table = table;
+        p.B = static_cast<int>(B);
+        p.H = m.H;
+        p.kv_group = static_cast<int>(group);
+        p.pf = m.pf;
+        p.spaces = static_cast<int>(spaces);
+        p.tpt = static_cast<int>(tpt);
+        p.total_q = static_cast<int>(total_q);
+        p.max_pages = static_cast<int>(max_pages);
+        p.page_log2 = page_log2;
+        p.num_pages = static_cast<int>(cache->num_pages);
+        p.max_keys = static_cast<int>(max_keys);
+        p.wl = static_cast<int>(wl);
+        p.wr = static_cast<int>(wr);
+        p.scale_log2 = scale_log2;
+        p.min_ticks = kMinTicks;
+        if (d == 32)
+            e = bf16 ? launch_decode<32, true>(p, m, sms, st) : launch_decode<32, false>(p, m, sms, st);
+        else if (d == 64)
+            e = bf16 ? launch_decode<64, true>(p, m, sms, st) : launch_decode<64, false>(p, m, sms, st);
+        else if (d == 128)
+            e = bf16 ? launch_decode<128, true>(p, m, sms, st) : launch_decode<128, false>(p, m, sms, st);
+        else
+            e = bf16 ? launch_decode<256, true>(p, m, sms, st) : launch_decode<256, false>(p, m, sms, st);
+        if (e != cudaSuccess) return FA_ERR_CUDA;
+        fa_host::count_launches(2);
+        return FA_OK;
+    }
     const int kbn = fa::paged::bn(static_cast<int>(d));
     const int64_t chunk = cache->page_size < kbn ? cache->page_size : kbn;
     CUtensorMap mq, mk, mv;
@@ -168,7 +271,6 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         !fa_host::make_map_pages(&mv, cache->v, *cache, static_cast<uint32_t>(chunk)))
         return FA_ERR_CUDA;
 
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
     fa::paged::Params p{};
     p.O = O;
     p.LSE = LSE;
@@ -186,52 +288,29 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     p.tpt = static_cast<int>(tpt);
     p.total_q = static_cast<int>(total_q);
     p.max_pages = static_cast<int>(max_pages);
-    p.page_log2 = 0;
-    while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
+    p.page_log2 = page_log2;
     p.num_pages = static_cast<int>(cache->num_pages);
     p.max_keys = static_cast<int>(max_keys);
     p.chunk = static_cast<int>(chunk);
-    // "all keys" is a window wider than any offset
-    const int64_t every = total_q + max_keys;
-    int64_t wl = every, wr = every;
-    if (mask_mode == FA_MASK_CAUSAL) wr = 0;
-    if (mask_mode == FA_MASK_WINDOW) {
-        wl = window_left < every ? window_left : every;
-        wr = window_right < every ? window_right : every;
-    }
     p.wl = static_cast<int>(wl);
     p.wr = static_cast<int>(wr);
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.scale_log2 = scale_log2;
     p.min_tiles = kMinTiles;
     p.wait_budget_ns = fa_host::wait_budget();
     p.status = di.status;
-    p.fault_skip_k = fa_host::take_fault_position();
-    fa::paged::MergeParams m{};
-    m.info = p.info;
-    m.part_O = p.part_O;
-    m.part_LSE = p.part_LSE;
-    m.O = O;
-    m.LSE = LSE;
-    m.H = p.H;
-    m.pf = p.pf;
-    const unsigned ctas = static_cast<unsigned>(di.sm_count);
-    const int64_t max_rows = tpt * pf < total_q * pf ? tpt * pf : total_q * pf;
-    const unsigned row_blocks =
-        static_cast<unsigned>((max_rows + fa::paged::kMergeWarps - 1) / fa::paged::kMergeWarps);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
+    p.fault_skip_k = fault;
     if (d == 32)
-        e = bf16 ? launch<32, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
-                 : launch<32, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+        e = bf16 ? launch<32, true>(mq, mk, mv, p, m, sms, st)
+                 : launch<32, false>(mq, mk, mv, p, m, sms, st);
     else if (d == 64)
-        e = bf16 ? launch<64, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
-                 : launch<64, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+        e = bf16 ? launch<64, true>(mq, mk, mv, p, m, sms, st)
+                 : launch<64, false>(mq, mk, mv, p, m, sms, st);
     else if (d == 128)
-        e = bf16 ? launch<128, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
-                 : launch<128, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+        e = bf16 ? launch<128, true>(mq, mk, mv, p, m, sms, st)
+                 : launch<128, false>(mq, mk, mv, p, m, sms, st);
     else
-        e = bf16 ? launch<256, true>(mq, mk, mv, p, m, ctas, row_blocks, st)
-                 : launch<256, false>(mq, mk, mv, p, m, ctas, row_blocks, st);
+        e = bf16 ? launch<256, true>(mq, mk, mv, p, m, sms, st)
+                 : launch<256, false>(mq, mk, mv, p, m, sms, st);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     fa_host::count_launches(2);
     return FA_OK;

@@ -199,6 +199,11 @@ __device__ __forceinline__ void record_timeout(const Params &p, volatile int *ab
     }
 }
 
+// Lets the next grid of the stream be launched before this one ends (see the merge).
+__device__ __forceinline__ void allow_next_grid() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // 4-D tiled copy global -> shared, completion counted on mbarrier `bar`.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
@@ -276,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint64_t budget = p.wait_budget_ns;
+    allow_next_grid();
 
     // ---- this CTA's share of the line of work: tiles w0 .. w1 - 1 of W. B sequences are
     // summed, and then searched for w0, 256 at a time.
@@ -926,78 +932,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the pieces of the cut units: block (c, y) the unit whose first piece is the last
-// one of CTA c, one warp per row. With O_s, LSE_s of piece s:
+// Joins the pieces of the cut units, a unit per block in turn: with O_s, LSE_s of piece s
 //     LSE = ln sum_s exp(LSE_s)          O = sum_s exp(LSE_s - LSE) O_s
-// around the largest LSE_s, in the order of the pieces (the same result every time).
+// around the largest LSE_s. A row is summed by one warp, or by 2, 4 or 8 over as many
+// runs of its pieces when there are fewer rows than warps; always in the same order.
 struct MergeParams {
     const MergeInfo *info;
     const float *part_O, *part_LSE;
     void *O;
     float *LSE;
-    int H, pf;
+    int workers, H, pf;
 };
 
 constexpr int kMergeWarps = 8;
 
-template <int D, bool BF16>
+// Programmatic dependent launch: the merge is launched while the attention kernel still
+// runs (its blocks wait here until that grid has finished and its stores are visible), so
+// that its launch costs no time of its own.
+__device__ __forceinline__ void wait_for_previous_grid() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// kRows: rows of a partial slot.
+template <int D, bool BF16, int kRows>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const MergeParams p) {
-    const int c = blockIdx.x;
-    const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const MergeInfo u = p.info[c];
-    if (u.last_cta < 0 || row >= u.rows) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kV = D / 32;  // consecutive columns per lane
-    const int n = u.last_cta - c + 1;
-    auto prow = [&](int s) { return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * kBM + row; };
-    float m = -INFINITY;
-    bool bad = false;
-    for (int s = lane; s < n; s += 32) {
-        const float x = p.part_LSE[prow(s)];
-        bad |= x != x;
-        m = fmaxf(m, x);
-    }
+    __shared__ float red_o[kMergeWarps][D];
+    __shared__ float red_m[kMergeWarps], red_w[kMergeWarps];
+    wait_for_previous_grid();
+    for (int c = blockIdx.x; c < p.workers; c += gridDim.x) {
+        const MergeInfo u = p.info[c];
+        if (u.last_cta < 0) continue;
+        const int n = u.last_cta - c + 1;
+        int ways = 1;  // warps per row
+        while (ways < kMergeWarps && u.rows * ways * 2 <= kMergeWarps) ways *= 2;
+        const int per = (n + ways - 1) / ways, run = warp % ways;
+        const int s_lo = min(run * per, n), s_hi = min(s_lo + per, n);
+        for (int row0 = 0; row0 < u.rows; row0 += kMergeWarps / ways) {
+            const int row = row0 + warp / ways;
+            const bool there = row < u.rows;
+            auto prow = [&](int s) {
+                return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * kRows + row;
+            };
+            float m = -INFINITY, wsum = 0.f, acc[kV];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    bad = __any_sync(0xffffffffu, bad);
-    float acc[kV];
+            for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+            // every lane the weight of one piece, 32 at a time, around a running maximum;
+            // an empty piece (LSE = -inf) weighs 0
+            for (int s0 = s_lo; there && s0 < s_hi; s0 += 32) {
+                const float x = s0 + lane < s_hi ? p.part_LSE[prow(s0 + lane)] : -INFINITY;
+                float top = x;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-    float wsum = 0.f, lse = -INFINITY;
-    if (m != -INFINITY || bad) {
-        for (int s0 = 0; s0 < n; s0 += 32) {
-            // every lane the weight of one piece; an empty piece (LSE = -inf) weighs 0
-            float w = 0.f;
-            if (s0 + lane < n) {
-                const float x = p.part_LSE[prow(s0 + lane)];
-                w = x == -INFINITY ? 0.f : expf(x - m);
-            }
-            const int ns = min(32, n - s0);
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float m_new = fmaxf(m, top);
+                const float f = m == -INFINITY ? 0.f : expf(m - m_new);
+                m = m_new;
+                wsum *= f;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] *= f;
+                const float w = x == -INFINITY ? 0.f : expf(x - m);
+                const int ns = min(32, s_hi - s0);
 #pragma unroll 4
-            for (int s = 0; s < ns; ++s) {
-                const float ws = __shfl_sync(0xffffffffu, w, s);
-                const float *o = p.part_O + prow(s0 + s) * D + lane * kV;
-                wsum += ws;
+                for (int s = 0; s < ns; ++s) {
+                    const float ws = __shfl_sync(0xffffffffu, w, s);
+                    const float *o = p.part_O + prow(s0 + s) * D + lane * kV;
+                    wsum += ws;
 #pragma unroll
-                for (int e = 0; e < kV; ++e) acc[e] = fmaf(ws, o[e], acc[e]);
+                    for (int e = 0; e < kV; ++e) acc[e] = fmaf(ws, o[e], acc[e]);
+                }
             }
+            if (ways > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < kV; ++e) red_o[warp][lane * kV + e] = acc[e];
+                if (lane == 0) red_m[warp] = m, red_w[warp] = wsum;
+                __syncthreads();
+                if (run == 0) {
+                    float top = m;
+                    for (int i = 1; i < ways; ++i) top = fmaxf(top, red_m[warp + i]);
+                    float total = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+                    for (int i = 0; i < ways; ++i) {
+                        // a run that saw nothing adds nothing; one with NaN adds it
+                        if (red_m[warp + i] == -INFINITY && red_w[warp + i] == 0.f) continue;
+                        const float f = red_m[warp + i] == top ? 1.f : expf(red_m[warp + i] - top);
+                        total = fmaf(f, red_w[warp + i], total);
+#pragma unroll
+                        for (int e = 0; e < kV; ++e) acc[e] = fmaf(f, red_o[warp + i][lane * kV + e], acc[e]);
+                    }
+                    m = top;
+                    wsum = total;
+                }
+            }
+            if (!there || run != 0) continue;
+            const bool none = wsum == 0.f;
+            const float inv = none ? 0.f : 1.f / wsum;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) acc[e] *= inv;
+            const int i = row / p.pf;
+            const size_t g = (static_cast<size_t>(u.tok0) + i) * p.H + u.head0 + (row - i * p.pf);
+            uint16_t *orow = reinterpret_cast<uint16_t *>(p.O) + g * D + lane * kV;
+            if constexpr (kV == 1) {
+                orow[0] = static_cast<uint16_t>(pack2<BF16>(acc[0], 0.f) & 0xffffu);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kV; e += 2)
+                    *reinterpret_cast<uint32_t *>(orow + e) = pack2<BF16>(acc[e], acc[e + 1]);
+            }
+            if (lane == 0) p.LSE[g] = none ? -INFINITY : m + logf(wsum);
         }
-        const float inv = 1.f / wsum;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] *= inv;
-        lse = m + logf(wsum);
     }
-    const int i = row / p.pf;
-    const size_t g = (static_cast<size_t>(u.tok0) + i) * p.H + u.head0 + (row - i * p.pf);
-    uint16_t *orow = reinterpret_cast<uint16_t *>(p.O) + g * D + lane * kV;
-    if constexpr (kV == 1) {
-        orow[0] = static_cast<uint16_t>(pack2<BF16>(acc[0], 0.f) & 0xffffu);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kV; e += 2)
-            *reinterpret_cast<uint32_t *>(orow + e) = pack2<BF16>(acc[e], acc[e + 1]);
-    }
-    if (lane == 0) p.LSE[g] = lse;
 }
 
 }  // namespace paged
