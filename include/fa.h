@@ -322,8 +322,9 @@ size_t fa_backward_varlen_workspace_bytes(int64_t B, int64_t H, int64_t total_q)
  */
 
 /* A (batch, head, token, d) tensor: `data` is the element (0, 0, 0, 0) and the three
- * strides count elements; d is contiguous. Device memory, 16-byte aligned, every
- * stride a multiple of 8 elements and >= 0. data = NULL: the tensor is not there. */
+ * strides count elements; d is contiguous. Device memory, 16-byte aligned, the strides
+ * multiples of 8 elements and >= 0 (what a dimension of one entry has does not matter).
+ * data = NULL: the tensor is not there. */
 typedef struct {
     void *data;
     int64_t batch, head, token;
@@ -411,10 +412,12 @@ size_t fa_qk_norm_rope_backward_workspace_bytes(int64_t d);
 /*
  * A paged K/V cache: num_pages pages of page_size tokens of H_kv heads of d elements,
  * K and V alike, element (page, token, head, i) at data + page * page_stride + token *
- * token_stride + head * head_stride + i. The strides are multiples of 8 elements, > 0,
- * and place every element somewhere else: token-major pages, head-major pages and
- * K and V interleaved in one buffer are all fine. k, v: device memory, 16-byte aligned.
- * page_size: a power of two, 8 .. 2^20. d: 32, 64, 128 or 256. num_pages < 2^31.
+ * token_stride + head * head_stride + i. The strides (of dimensions with more than one
+ * entry) are multiples of 8 elements, > 0, and place every element somewhere else:
+ * token-major pages, head-major pages and K and V interleaved in one buffer are all
+ * fine. k, v: device memory, 16-byte aligned. page_size: a power of two, 8 .. 2^20. d: 32,
+ * 64, 128 or 256. num_pages < 2^31, and fewer than 2^31 steps of the page and head strides'
+ * greatest common divisor from the first to the last page (else FA_ERR_UNSUPPORTED).
  */
 typedef struct {
     void *k, *v;

@@ -19,8 +19,7 @@ using fa_host::align256;
 
 constexpr int kMaxDevices = 64;
 
-// Shares at least, in K/V tiles (chunk kernel) and ticks (decode kernel).
-constexpr int kMinTiles = 1;
+// Ticks of a decode worker's share at least.
 constexpr int kMinTicks = 8;
 
 struct Configured {
@@ -74,12 +73,12 @@ Layout layout_of(int64_t d, int64_t sms) {
 
 // The merge, launched while the attention kernel runs (see wait_for_previous_grid).
 template <int D, bool BF16, int kRows>
-cudaError_t launch_merge(const fa::paged::MergeParams &m, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_merge(const fa::paged::MergeParams &m, dim3 blocks, cudaStream_t st) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = blocks;
     cfg.blockDim = dim3(fa::paged::kMergeWarps * 32);
     cfg.stream = st;
     cfg.attrs = &attr;
@@ -95,7 +94,7 @@ cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     m.workers = static_cast<int>(sms);
-    return launch_merge<D, BF16, fa::paged::kBM>(m, sms, st);
+    return launch_merge<D, BF16, fa::paged::kBM>(m, dim3(sms, 8), st);
 }
 
 template <int D, bool BF16>
@@ -106,7 +105,7 @@ cudaError_t launch_decode(const fa::paged::SmallParams &p, fa::paged::MergeParam
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     m.workers = static_cast<int>(sms) * L::kWarps;
-    return launch_merge<D, BF16, fa::paged::kSmallRows>(m, sms * L::kWarps / 2, st);
+    return launch_merge<D, BF16, fa::paged::kSmallRows>(m, dim3(sms * L::kWarps / 2), st);
 }
 
 int sm_count_or_default() {
@@ -155,7 +154,7 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         total_q * H > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;
     const int64_t tile = decode ? (d <= 64 ? 32 : 16) : fa::paged::bn(static_cast<int>(d));
-    const double tiles = static_cast<double>(max_keys / tile + 2 + fa::paged::kUnitTicks);
+    const double tiles = static_cast<double>(max_keys / tile + 2 + fa::paged::kUnitTicks + fa::paged::kChunkTicks);
     if (static_cast<double>(spaces) * static_cast<double>(total_q / tpt + B) * tiles > 2147483647.0)
         return FA_ERR_UNSUPPORTED;
     const Layout lay = layout_of(d, sm_count_or_default());
@@ -265,10 +264,12 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     const int kbn = fa::paged::bn(static_cast<int>(d));
     const int64_t chunk = cache->page_size < kbn ? cache->page_size : kbn;
     CUtensorMap mq, mk, mv;
+    fa_host::PageSteps steps;
+    if (!fa_host::page_steps(*cache, &steps)) return FA_ERR_UNSUPPORTED;
     if (!fa_host::make_map_rows(&mq, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf),
                                 static_cast<uint32_t>(tpt)) ||
-        !fa_host::make_map_pages(&mk, cache->k, *cache, static_cast<uint32_t>(chunk)) ||
-        !fa_host::make_map_pages(&mv, cache->v, *cache, static_cast<uint32_t>(chunk)))
+        !fa_host::make_map_pages(&mk, cache->k, *cache, steps, static_cast<uint32_t>(chunk)) ||
+        !fa_host::make_map_pages(&mv, cache->v, *cache, steps, static_cast<uint32_t>(chunk)))
         return FA_ERR_CUDA;
 
     fa::paged::Params p{};
@@ -292,10 +293,12 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     p.num_pages = static_cast<int>(cache->num_pages);
     p.max_keys = static_cast<int>(max_keys);
     p.chunk = static_cast<int>(chunk);
+    p.page_step = static_cast<int>(steps.page);
+    p.head_step = static_cast<int>(steps.head);
+    p.page_none = static_cast<int>(steps.count);
     p.wl = static_cast<int>(wl);
     p.wr = static_cast<int>(wr);
     p.scale_log2 = scale_log2;
-    p.min_tiles = kMinTiles;
     p.wait_budget_ns = fa_host::wait_budget();
     p.status = di.status;
     p.fault_skip_k = fault;

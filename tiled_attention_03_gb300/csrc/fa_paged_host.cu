@@ -33,7 +33,7 @@ bool encode(CUtensorMap *map, const void *base, bool bf16, int rank, const cuuin
             const cuuint64_t *strides, const cuuint32_t *box, int64_t d) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -51,18 +51,19 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
     if (c.dtype != FA_DTYPE_FP16 && c.dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
     if (c.num_pages < 1 || c.H_kv < 1 || c.page_size < 1 || c.d < 1) return FA_ERR_INVALID_ARG;
     const int64_t st[3] = {c.page_stride, c.token_stride, c.head_stride};
-    for (int64_t s : st)
-        if (s < 1 || s % 8 != 0) return FA_ERR_INVALID_ARG;
+    const int64_t count[3] = {c.num_pages, c.page_size, c.H_kv};
+    for (int i = 0; i < 3; ++i)  // the stride of a single entry does not matter
+        if (count[i] > 1 && (st[i] < 1 || st[i] % 8 != 0)) return FA_ERR_INVALID_ARG;
     if (c.d != 32 && c.d != 64 && c.d != 128 && c.d != 256) return FA_ERR_UNSUPPORTED;
     if (c.page_size < 8 || c.page_size > (int64_t{1} << 20) || (c.page_size & (c.page_size - 1)) != 0)
         return FA_ERR_UNSUPPORTED;
     // what a tensor map and 64-bit extents hold
     if (c.num_pages >= (int64_t{1} << 31) || c.H_kv > (int64_t{1} << 20)) return FA_ERR_UNSUPPORTED;
-    for (int64_t s : st)
-        if (s >= (int64_t{1} << 39)) return FA_ERR_UNSUPPORTED;
-    const double extent = static_cast<double>(c.num_pages - 1) * static_cast<double>(c.page_stride) +
-                          static_cast<double>(c.page_size - 1) * static_cast<double>(c.token_stride) +
-                          static_cast<double>(c.H_kv - 1) * static_cast<double>(c.head_stride);
+    for (int i = 0; i < 3; ++i)
+        if (count[i] > 1 && st[i] >= (int64_t{1} << 35)) return FA_ERR_UNSUPPORTED;
+    double extent = 0;
+    for (int i = 0; i < 3; ++i)
+        if (count[i] > 1) extent += static_cast<double>(count[i] - 1) * static_cast<double>(st[i]);
     if (extent > 1e18) return FA_ERR_UNSUPPORTED;
     // every element at a place of its own: with the (extent > 1) dimensions sorted by
     // stride, each steps over all that the smaller ones span
@@ -96,16 +97,36 @@ bool make_map_rows(CUtensorMap *map, const void *base, bool bf16, int64_t tokens
     return encode(map, base, bf16, 3, dims, strides, box, d);
 }
 
-bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c,
+bool page_steps(const fa_paged_cache &c, PageSteps *s) {
+    const int64_t ps = c.num_pages > 1 ? c.page_stride : 0, hs = c.H_kv > 1 ? c.head_stride : 0;
+    int64_t a = ps, b = hs;
+    while (b != 0) {
+        const int64_t r = a % b;
+        a = b;
+        b = r;
+    }
+    s->stride = a > 0 ? a : c.d;
+    s->page = ps / s->stride;
+    s->head = hs / s->stride;
+    const double most = static_cast<double>(c.num_pages) * static_cast<double>(s->page) +
+                        static_cast<double>(c.H_kv) * static_cast<double>(s->head);
+    if (most >= 2147483647.0) return false;
+    s->count = (c.num_pages - 1) * s->page + (c.H_kv - 1) * s->head + 1;
+    return true;
+}
+
+bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c, const PageSteps &s,
                     uint32_t box_tokens) {
-    const cuuint64_t dims[4] = {
-        static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page_size),
-        static_cast<cuuint64_t>(c.H_kv), static_cast<cuuint64_t>(c.num_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride * 2),
-                                   static_cast<cuuint64_t>(c.head_stride * 2),
-                                   static_cast<cuuint64_t>(c.page_stride * 2)};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.d < 64 ? c.d : 64), box_tokens, 1, 1};
-    return encode(map, base, c.dtype == FA_DTYPE_BF16, 4, dims, strides, box, c.d);
+    const int64_t cols = c.d < 64 ? c.d : 64;
+    const cuuint64_t dims[5] = {
+        static_cast<cuuint64_t>(cols), 8, static_cast<cuuint64_t>(c.d / cols),
+        static_cast<cuuint64_t>(c.page_size / 8), static_cast<cuuint64_t>(s.count)};
+    const cuuint64_t strides[4] = {
+        static_cast<cuuint64_t>(c.token_stride * 2), static_cast<cuuint64_t>(cols * 2),
+        static_cast<cuuint64_t>(c.token_stride * 16), static_cast<cuuint64_t>(s.stride * 2)};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), 8, static_cast<cuuint32_t>(c.d / cols),
+                               box_tokens / 8, 1};
+    return encode(map, base, c.dtype == FA_DTYPE_BF16, 5, dims, strides, box, c.d);
 }
 
 }  // namespace fa_host

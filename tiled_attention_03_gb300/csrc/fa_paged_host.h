@@ -17,9 +17,17 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes);
 // tokens): box of min(d, 64) columns x box_heads x box_tokens.
 bool make_map_rows(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t heads,
                    int64_t d, uint32_t box_heads, uint32_t box_tokens);
-// 4-D TMA map over one tensor of a paged cache, ordered (d, token in page, head, page):
-// box of min(d, 64) columns x box_tokens tokens of one head of one page.
-bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c,
+// Page and head of a cache as one coordinate, page * page + head * head, in steps of the
+// strides' greatest common divisor; count: one past its last value. False when that does
+// not fit 31 bits.
+struct PageSteps {
+    int64_t page, head, count, stride;
+};
+bool page_steps(const fa_paged_cache &c, PageSteps *s);
+// 5-D TMA map over one tensor of a paged cache, ordered (column in a region of min(d, 64),
+// token in a group of 8, region, group of 8 tokens of a page, page and head as above): box
+// of all columns of box_tokens tokens of one head of one page.
+bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c, const PageSteps &s,
                     uint32_t box_tokens);
 
 }  // namespace fa_host

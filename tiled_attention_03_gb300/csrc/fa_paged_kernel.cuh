@@ -6,15 +6,19 @@
 // in tensor memory, O divided by l once). What differs:
 //   * K and V tiles are gathered from pages: the tile's keys are cut into chunks of
 //     min(page size, bn) tokens, lane c of the producer warp reads chunk c's page number
-//     and issues its TMA boxes; chunks that hold no key of the unit are not read.
+//     and issues its TMA box; chunks that hold no key of the unit are not read. A box is
+//     five-dimensional (64 columns, 8 tokens, column region, group of 8 tokens, page and
+//     head), so that one copy brings all of a chunk's columns: the copies are issued at
+//     about one per 60 cycles, and one per chunk and region had bound pages of 16 tokens.
 //   * Rows of a unit are (token, head) pairs: the pf query heads of one K/V head (or
 //     a divisor of them when there are more than 128) for 128 / pf tokens, token-major
 //     in the tile, so that every K/V tile is read once for all of them, at one token
 //     per sequence as well as in a chunk of a prompt.
 //   * The work is cut by K/V tiles, not by units: all units (sequence, head group,
-//     tile of tokens) with all their visible K/V tiles form one line of W tiles, and
-//     CTA c takes tiles c T .. c T + T - 1 of it (T = ceil(W / CTAs), at least
-//     min_tiles). Every CTA gets the same share whatever the lengths are, without counters.
+//     tile of tokens) with all their visible K/V tiles, and kChunkTicks more for each unit's
+//     start and end, form one line of W ticks, and CTA c takes ticks c T .. c T + T - 1 of it
+//     (T = ceil(W / CTAs)). Every CTA gets the same share whatever the lengths are,
+//     without counters.
 //     A unit cut by a share's end leaves one partial (O / l and LSE, fp32) per piece,
 //     which fa_paged_merge_kernel joins in the order of the pieces: at most two pieces
 //     per CTA are partial, so the workspace depends on the SM count and D alone. The
@@ -45,12 +49,17 @@ namespace paged {
 constexpr int kBM = 128;  // rows per unit (TMEM lanes)
 __host__ __device__ constexpr int bn(int D) { return D == 256 ? 64 : 128; }  // keys per tile
 constexpr int kThreads = 256;
+// A unit's start and end (its Q, its first scores, its outputs) in tiles.
+constexpr int kChunkTicks = 2;
 constexpr int kQKWarp = 4;
 constexpr int kMmaWarp = 5;
 constexpr int kVWarp = 6;
 constexpr int kSchedWarp = 7;
-// K and V ring depths: what shared memory holds next to the Q tile
-__host__ __device__ constexpr int k_stages(int D) { return D <= 64 ? 6 : 3; }
+// Q, K and V ring depths: what shared memory holds. Two Q tiles let the scores of the
+// next unit start while this one ends; K is read by its scores alone, soon after it
+// comes, V a few tiles later.
+__host__ __device__ constexpr int q_stages(int D) { return D == 256 ? 1 : 2; }
+__host__ __device__ constexpr int k_stages(int D) { return D <= 64 ? 5 : D == 128 ? 2 : 3; }
 __host__ __device__ constexpr int v_stages(int D) { return D <= 64 ? 6 : D == 128 ? 3 : 2; }
 constexpr int kMaxStages = 6;
 constexpr int kSBufs = 3;
@@ -64,7 +73,7 @@ constexpr uint32_t kTmemS = 0;
 constexpr uint32_t kTmemQ = 128;  // d = 256 only
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in fa_fwd_kernel.cuh
 constexpr unsigned kStatusTimeout = 4;
-constexpr int kUnitSlots = 2;
+constexpr int kUnitSlots = 8;
 constexpr int kUnitConsumers = 7;  // warps 0-6 arrive once each per piece
 constexpr int kMinPage = 8;        // tokens per page at least: a swizzle atom of a tile
 enum : int { kRoleSoftmax = 1, kRoleTma = 2, kRoleMma = 3 };
@@ -92,32 +101,36 @@ struct Params {
     int total_q, max_pages, page_log2, num_pages;
     int max_keys;      // max_pages pages of keys (a length above it counts as this)
     int chunk;         // tokens per TMA box: min(page size, bn(D))
+    int page_step, head_step;  // the maps' last coordinate: page * page_step + head * head_step
+    int page_none;     // one past its last value: reads as zeros
     int wl, wr;        // key j visible to the query at position i iff i - wl <= j <= i + wr
     float scale_log2;
-    int min_tiles;     // K/V tiles per CTA at least
     unsigned long long wait_budget_ns;
     unsigned int *status;
     int fault_skip_k;  // test hook: every CTA skips the K load at this ring position (-1: none)
 };
 
-// Tiles are stored as regions of min(D, 64) columns with the swizzle of that row width.
+// Tiles are stored as regions of min(D, 64) columns with the swizzle of that row width. Q: region
+// after region of 128 rows; K and V: groups of 8 rows, the regions of a group side by side.
 template <int D>
 struct Smem {
     static constexpr int kCols = D < 64 ? D : 64;
     static constexpr int kRowBytes = kCols * 2;
     static constexpr int kRegions = D / kCols;
     static constexpr int kQRegion = kBM * kRowBytes;
-    static constexpr int kKVRegion = bn(D) * kRowBytes;
     static constexpr int kQBytes = kRegions * kQRegion;
-    static constexpr int kKVBytes = kRegions * kKVRegion;
+    static constexpr int kAtom = 8 * kRowBytes;        // one region of a group
+    static constexpr int kGroup = kRegions * kAtom;
+    static constexpr int kKVBytes = bn(D) / 8 * kGroup;
     static constexpr int kQ = 0;
-    static constexpr int kK = kQ + kQBytes;
+    static constexpr int kK = kQ + q_stages(D) * kQBytes;
     static constexpr int kV = kK + k_stages(D) * kKVBytes;
     static constexpr int kBar = kV + v_stages(D) * kKVBytes;
-    static constexpr int kNumBars = 48;
+    static constexpr int kNumBars = 64;
     static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag
     static constexpr int kScan = kMisc + 16;           // 8 warp sums, start sequence and offset
     static constexpr int kUnitRing = kScan + 48;       // kUnitSlots pieces
+    static_assert(kUnitRing % 16 == 0, "ring alignment");
     static constexpr int kBytes = kUnitRing + kUnitSlots * 64;
     // more than half of the SM's shared memory: one CTA (and one holder of all 512
     // TMEM columns) per SM
@@ -126,9 +139,9 @@ struct Smem {
 };
 
 enum : int {
-    kBarQFull = 0,
-    kBarQEmpty = 1,
-    kBarKFull = 2,                         // + stage
+    kBarQFull = 0,                         // + stage (2)
+    kBarQEmpty = 2,                        // + stage (2)
+    kBarKFull = 4,                         // + stage
     kBarKEmpty = kBarKFull + kMaxStages,   // + stage
     kBarVFull = kBarKEmpty + kMaxStages,   // + stage
     kBarVEmpty = kBarVFull + kMaxStages,   // + stage
@@ -137,8 +150,8 @@ enum : int {
     kBarPVDone = kBarPFull + kSBufs,       // + parity of the block (2)
     kBarODone = kBarPVDone + 2,
     kBarOFree = kBarODone + 1,
-    kBarUnitFull = kBarOFree + 1,               // + slot (2)
-    kBarUnitEmpty = kBarUnitFull + kUnitSlots,  // + slot (2)
+    kBarUnitFull = kBarOFree + 1,               // + slot (8)
+    kBarUnitEmpty = kBarUnitFull + kUnitSlots,  // + slot (8)
     kBarDrain = kBarUnitEmpty + kUnitSlots,
     kBarQReady = kBarDrain + 1,            // Q copied into TMEM (d = 256)
     kNumBarsUsed = kBarQReady + 1,
@@ -179,13 +192,12 @@ __device__ __forceinline__ void unit_range(const Seq &s, int qb, const Params &p
     j0 = lo / kBN;
     j1 = hi < lo ? j0 - 1 : hi / kBN;
 }
-// A unit's share of the line of work: its tiles, and 1 when it has none (its rows are
-// written all the same).
+// A unit's K/V tiles (none when no row sees a key: its rows are written all the same).
 template <int kBN>
-__device__ __forceinline__ int unit_work(const Seq &s, int qb, const Params &p) {
+__device__ __forceinline__ int unit_tiles(const Seq &s, int qb, const Params &p) {
     int lo, hi, j0, j1;
     unit_range<kBN>(s, qb, p, lo, hi, j0, j1);
-    return max(j1 - j0 + 1, 1);
+    return j1 - j0 + 1;
 }
 
 __device__ __forceinline__ void record_timeout(const Params &p, volatile int *abort_flag, int role,
@@ -204,14 +216,27 @@ __device__ __forceinline__ void allow_next_grid() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// 4-D tiled copy global -> shared, completion counted on mbarrier `bar`.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+// 5-D tiled copy global -> shared, completion counted on mbarrier `bar`.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3, int32_t c4) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
+}
+
+// Shared-memory matrix descriptor as in ptx.cuh, with the byte distances of 64-column blocks
+// (MN-major operands) and of groups of 8 rows given.
+template <int kRowBytes>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(kRowBytes == 128 ? 2 : 4) << 61;
+    return d;
 }
 
 __device__ __forceinline__ unsigned warp_sum(unsigned v) {
@@ -220,7 +245,7 @@ __device__ __forceinline__ unsigned warp_sum(unsigned v) {
     return v;
 }
 
-// Work of one head group of sequence b (every thread of the warp calls it with its own
+// Ticks of one head group of sequence b (every thread of the warp calls it with its own
 // b; b >= B gives 0). Long sequences, with many token tiles, are summed by the whole
 // warp one after the other.
 template <int kBN>
@@ -231,7 +256,7 @@ __device__ __forceinline__ unsigned seq_work(int b, const Params &p) {
     unsigned w = 0;
     constexpr int kOwn = 4;
     if (nqb <= kOwn)
-        for (int qb = 0; qb < nqb; ++qb) w += unit_work<kBN>(s, qb, p);
+        for (int qb = 0; qb < nqb; ++qb) w += unit_tiles<kBN>(s, qb, p) + kChunkTicks;
     unsigned todo = __ballot_sync(0xffffffffu, nqb > kOwn);
     const int lane = threadIdx.x & 31;
     while (todo != 0) {
@@ -240,7 +265,7 @@ __device__ __forceinline__ unsigned seq_work(int b, const Params &p) {
         const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.nk, src)};
         const int n = __shfl_sync(0xffffffffu, nqb, src);
         unsigned part = 0;
-        for (int qb = lane; qb < n; qb += 32) part += unit_work<kBN>(o, qb, p);
+        for (int qb = lane; qb < n; qb += 32) part += unit_tiles<kBN>(o, qb, p) + kChunkTicks;
         part = warp_sum(part);
         if (lane == src) w = part;
     }
@@ -258,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kQT = q_in_tmem(D);
     constexpr int kKStages = k_stages(D);
     constexpr int kVStages = v_stages(D);
+    constexpr int kQStages = q_stages(D);
     static_assert(kQT ? (kSB * kBN <= static_cast<int>(kTmemQ) && kTmemQ + D / 2 <= kTmemO)
                       : kSB * kBN <= static_cast<int>(kTmemO),
                   "TMEM columns");
@@ -266,12 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t sQ = sbase + L::kQ;
     const uint32_t bar0 = sbase + L::kBar;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     volatile unsigned *scan = reinterpret_cast<volatile unsigned *>(smem + L::kScan);
     auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    auto sQ = [sbase](int k) { return sbase + L::kQ + (k % kQStages) * L::kQBytes; };
     auto sK = [sbase](int t) { return sbase + L::kK + (t % kKStages) * L::kKVBytes; };
     auto sV = [sbase](int t) { return sbase + L::kV + (t % kVStages) * L::kKVBytes; };
     auto slot_of = [smem](int k) {
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t budget = p.wait_budget_ns;
     allow_next_grid();
 
-    // ---- this CTA's share of the line of work: tiles w0 .. w1 - 1 of W. B sequences are
+    // ---- this CTA's share of the line of work: ticks w0 .. w1 - 1 of W. B sequences are
     // summed, and then searched for w0, 256 at a time.
     auto block_sum = [&](unsigned v) -> unsigned {
         v = warp_sum(v);
@@ -302,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mine += w;
     }
     const unsigned W = block_sum(mine);
-    const unsigned T = max((W + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(p.min_tiles));
+    const unsigned T = (W + gridDim.x - 1) / gridDim.x;
     const unsigned w0 = min(blockIdx.x * T, W), w1 = min(w0 + T, W);
     if (w0 >= w1) {  // nothing left for this CTA
         if (threadIdx.x == 0) p.info[blockIdx.x].last_cta = -1;
@@ -341,10 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if (threadIdx.x == kQKWarp * 32) {
-        mbar_init(bar(kBarQFull), 1);
-        // Q's shared-memory copy is released by the MMA warp's commit, or at d = 256
-        // by the softmax threads once they have copied it into TMEM
-        mbar_init(bar(kBarQEmpty), kQT ? 128 : 1);
+        for (int s = 0; s < kQStages; ++s) {
+            mbar_init(bar(kBarQFull + s), 1);
+            // Q's shared-memory copy is released by the MMA warp's commit, or at d = 256
+            // by the softmax threads once they have copied it into TMEM
+            mbar_init(bar(kBarQEmpty + s), kQT ? 128 : 1);
+        }
         mbar_init(bar(kBarQReady), 128);
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(bar(kBarKFull + s), 1);
@@ -402,20 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (need) {
             page = p.table[static_cast<size_t>(P.b) * p.max_pages + (k0 >> p.page_log2)];
             // a page number outside the cache reads as zeros
-            if (page < 0 || page >= p.num_pages) page = p.num_pages;
+            const int hkv = P.sp * p.pf / p.kv_group;
+            page = page >= 0 && page < p.num_pages ? page * p.page_step + hkv * p.head_step : p.page_none;
         }
         return __ballot_sync(0xffffffffu, need);
     };
     auto load_chunks = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, uint32_t need, int page,
-                           int tok, int hkv) {
+                           int tok) {
         if (lane == 0)
-            mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(need)) * p.chunk * L::kRowBytes *
-                                            L::kRegions);
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(need)) * p.chunk * (L::kGroup / 8));
         __syncwarp();
         if ((need >> lane) & 1u)
-            for (int g = 0; g < L::kRegions; ++g)
-                tma_load_4d(dst + g * L::kKVRegion + lane * p.chunk * L::kRowBytes, map, full,
-                            L::kCols * g, tok, hkv, page);
+            tma_load_5d(dst + lane * p.chunk * (L::kGroup / 8), map, full, 0, 0, 0, tok >> 3, page);
         __syncwarp();
     };
 
@@ -427,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             int nqb = (s.nq + p.tpt - 1) / p.tpt;
             {
                 int per = 0;
-                for (int x = 0; x < nqb; ++x) per += unit_work<kBN>(s, x, p);
+                for (int x = 0; x < nqb; ++x) per += unit_tiles<kBN>(s, x, p) + kChunkTicks;
                 sp = static_cast<int>(scan[9]) / per;
                 rem = static_cast<int>(scan[9]) - sp * per;
                 for (; qb < nqb - 1; ++qb) {
-                    const int n = unit_work<kBN>(s, qb, p);
+                    const int n = unit_tiles<kBN>(s, qb, p) + kChunkTicks;
                     if (rem < n) break;
                     rem -= n;
                 }
@@ -440,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             MergeInfo info{};
             info.last_cta = -1;
-            int k = 0;
+            int k = 0, pieces = 0;
             for (; ok; ++k) {
                 const int slot = k % kUnitSlots;
                 ok = mbar_wait_bounded(bar(kBarUnitEmpty + slot), ((k / kUnitSlots) & 1) ^ 1, abort_flag,
@@ -448,30 +474,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 Piece P{};
                 P.b = -1;
-                if (w < w1) {
+                while (w < w1 && P.b < 0) {
                     int lo, hi, j0, j1;
                     unit_range<kBN>(s, qb, p, lo, hi, j0, j1);
-                    const int n = max(j1 - j0 + 1, 1);
-                    const int len = min(n - rem, static_cast<int>(w1 - w));
-                    P.b = b;
-                    P.sp = sp;
-                    P.t0 = qb * p.tpt;
-                    P.rows = (min(P.t0 + p.tpt, s.nq) - P.t0) * p.pf;
-                    P.lo_key = lo;
-                    P.hi_key = hi;
-                    P.q_off = s.nk - s.nq;
-                    P.nk = s.nk;
-                    P.tok0 = s.q0 + P.t0;
-                    P.j0 = j0 + rem;
-                    P.j1 = j1 < j0 ? P.j0 - 1 : P.j0 + len - 1;
-                    const bool starts = rem == 0, ends = rem + len == n;
-                    P.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (k > 0);
-                    if (starts && !ends) {
-                        info.last_cta = static_cast<int>((w + n - 1) / T);
-                        info.slot = P.slot;
-                        info.rows = P.rows;
-                        info.tok0 = P.tok0;
-                        info.head0 = sp * p.pf;
+                    const int n = j1 - j0 + 1;
+                    const int len = min(n + kChunkTicks - rem, static_cast<int>(w1 - w));
+                    // this share's tiles of the unit: ja .. je - 1
+                    const int ja = max(rem - kChunkTicks, 0), je = rem + len - kChunkTicks;
+                    if (n == 0 ? rem == 0 : je > ja) {
+                        P.b = b;
+                        P.sp = sp;
+                        P.t0 = qb * p.tpt;
+                        P.rows = (min(P.t0 + p.tpt, s.nq) - P.t0) * p.pf;
+                        P.lo_key = lo;
+                        P.hi_key = hi;
+                        P.q_off = s.nk - s.nq;
+                        P.nk = s.nk;
+                        P.tok0 = s.q0 + P.t0;
+                        P.j0 = j0 + ja;
+                        P.j1 = n == 0 ? P.j0 - 1 : j0 + je - 1;
+                        const bool starts = ja == 0, ends = n == 0 || je == n;
+                        P.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (pieces > 0);
+                        if (n > 0) ++pieces;
+                        if (starts && !ends) {
+                            info.last_cta = static_cast<int>((w - rem + kChunkTicks + n - 1) / T);
+                            info.slot = P.slot;
+                            info.rows = P.rows;
+                            info.tok0 = P.tok0;
+                            info.head0 = sp * p.pf;
+                        }
                     }
                     w += len;
                     rem = 0;
@@ -503,16 +534,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Piece P = take(k, ok);
             if (!ok || P.b < 0) break;
             if (P.j1 < P.j0) continue;
-            const int hkv = P.sp * p.pf / p.kv_group;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty), (q_loads & 1) ^ 1, abort_flag,
-                                                           budget));
+            const int qs = q_loads % kQStages;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty + qs), ((q_loads / kQStages) & 1) ^ 1,
+                                                           abort_flag, budget));
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar(kBarQFull), static_cast<uint32_t>(p.pf * p.tpt) * L::kRowBytes *
-                                                          L::kRegions);
+                mbar_arrive_expect_tx(bar(kBarQFull + qs), static_cast<uint32_t>(p.pf * p.tpt) *
+                                                               L::kRowBytes * L::kRegions);
                 for (int g = 0; g < L::kRegions; ++g)
-                    tma_load_3d(sQ + g * L::kQRegion, &tmQ, bar(kBarQFull), L::kCols * g, P.sp * p.pf,
-                                P.tok0);
+                    tma_load_3d(sQ(q_loads) + g * L::kQRegion, &tmQ, bar(kBarQFull + qs), L::kCols * g,
+                                P.sp * p.pf, P.tok0);
             }
             ++q_loads;
             int page, tok;
@@ -526,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarKEmpty + st), ((t / kKStages) & 1) ^ 1,
                                                                abort_flag, budget));
                 if (!ok) break;
-                if (t != p.fault_skip_k) load_chunks(&tmK, sK(t), bar(kBarKFull + st), need, page, tok, hkv);
+                if (t != p.fault_skip_k) load_chunks(&tmK, sK(t), bar(kBarKFull + st), need, page, tok);
                 page = page_n;
                 tok = tok_n;
                 need = need_n;
@@ -534,7 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
             if (!ok) record_timeout(p, abort_flag, kRoleTma, -1);
-            if (q_loads > 0) mbar_wait_bounded(bar(kBarQFull), (q_loads - 1) & 1, nullptr, budget);
+            for (int s = 0; s < kQStages; ++s)
+                if (q_loads > s) {
+                    const int last = q_loads - 1 - ((q_loads - 1 - s) % kQStages);
+                    mbar_wait_bounded(bar(kBarQFull + s), (last / kQStages) & 1, nullptr, budget);
+                }
             for (int s = 0; s < kKStages; ++s)
                 if (t > s) {
                     const int last = t - 1 - ((t - 1 - s) % kKStages);
@@ -548,7 +583,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; ok; ++k) {
             const Piece P = take(k, ok);
             if (!ok || P.b < 0) break;
-            const int hkv = P.sp * p.pf / p.kv_group;
             int page, tok;
             uint32_t need = chunk_of(P, P.j0, page, tok);
             for (int j = P.j0; j <= P.j1; ++j, ++t) {
@@ -559,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarVEmpty + st), ((t / kVStages) & 1) ^ 1,
                                                                abort_flag, budget));
                 if (!ok) break;
-                load_chunks(&tmV, sV(t), bar(kBarVFull + st), need, page, tok, hkv);
+                load_chunks(&tmV, sV(t), bar(kBarVFull + st), need, page, tok);
                 page = page_n;
                 tok = tok_n;
                 need = need_n;
@@ -586,15 +620,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         };
         // S(t) = Q K_t^T into S buffer t mod kSB; Q from shared memory, or from TMEM.
-        auto issue_s = [&](int t) {
+        auto issue_s = [&](int t, int q) {
             tc_fence_after();
-            const uint64_t dq = swz_desc<L::kRowBytes>(sQ, 16);
-            const uint64_t dk = swz_desc<L::kRowBytes>(sK(t), 16);
+            const uint64_t dq = tile_desc<L::kRowBytes>(sQ(q), 16, L::kAtom);
+            const uint64_t dk = tile_desc<L::kRowBytes>(sK(t), 16, L::kGroup);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t offq = (k / kSteps) * (L::kQRegion >> 4) + (k % kSteps) * 2;
-                    const uint32_t offk = (k / kSteps) * (L::kKVRegion >> 4) + (k % kSteps) * 2;
+                    const uint32_t offk = (k / kSteps) * (L::kAtom >> 4) + (k % kSteps) * 2;
                     if constexpr (kQT)
                         umma_f16_ts(tmem + kTmemS + (t % kSB) * kBN, tmem + kTmemQ + k * 8, dk + offk,
                                     idesc_s, k > 0 ? 1u : 0u);
@@ -609,13 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O (+)= P(t) V_t, P read from the first kBN / 2 columns of S buffer t mod kSB.
         auto issue_pv = [&](int t, bool first_tile) {
             tc_fence_after();
-            const uint64_t dv = swz_desc<L::kRowBytes>(sV(t), L::kKVRegion);
+            const uint64_t dv = tile_desc<L::kRowBytes>(sV(t), L::kAtom, L::kGroup);
             const uint32_t acc0 = first_tile ? 0u : 1u;
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kBN / 16; ++k)
                     umma_f16_ts(tmem + kTmemO, tmem + kTmemS + (t % kSB) * kBN + k * 8,
-                                dv + k * ((16 * L::kRowBytes) >> 4), idesc_o, k > 0 ? 1u : acc0);
+                                dv + k * ((2 * L::kGroup) >> 4), idesc_o, k > 0 ? 1u : acc0);
                 umma_commit(bar(kBarPVDone + (t & 1)));
             }
             __syncwarp();
@@ -623,35 +657,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rows of V tile t (keys kv0 ..) outside keys lo .. hi: 0 times whatever the page
         // holds there must be 0.
         auto zero_rows = [&](int t, int kv0, int lo, int hi) {
-            const int head = min(max(lo - kv0, 0), kBN), tail = min(max(hi + 1 - kv0, 0), kBN);
             const uint4 z = make_uint4(0, 0, 0, 0);
-            for (int g = 0; g < L::kRegions; ++g) {
-                uint8_t *base = smem + L::kV + (t % kVStages) * L::kKVBytes + g * L::kKVRegion;
-                for (int c = lane; c < head * (L::kRowBytes / 16); c += 32)
-                    *reinterpret_cast<uint4 *>(base + c * 16) = z;
-                for (int c = tail * (L::kRowBytes / 16) + lane; c < kBN * (L::kRowBytes / 16); c += 32)
-                    *reinterpret_cast<uint4 *>(base + c * 16) = z;
+            uint8_t *base = smem + L::kV + (t % kVStages) * L::kKVBytes;
+            constexpr int kPer = D / 8;  // 16-byte pieces of a row
+            for (int c = lane; c < kBN * kPer; c += 32) {
+                const int r = c / kPer, x = c % kPer;  // a row's regions are kAtom apart
+                if (kv0 + r < lo || kv0 + r > hi)
+                    *reinterpret_cast<uint4 *>(base + (r >> 3) * L::kGroup + (r & 7) * L::kRowBytes +
+                                               (x / (L::kRowBytes / 16)) * L::kAtom +
+                                               (x % (L::kRowBytes / 16)) * 16) = z;
             }
             fence_proxy_async_smem();
             __syncwarp();
         };
-        int t = 0, live = 0;  // K/V tiles, and pieces with tiles, so far
-        bool ok = true;
+        // The scores run ahead of the outputs by up to kSB tiles, into the next pieces as
+        // well (at d = 256 within a piece only: the next Q replaces this one in TMEM once
+        // the softmax is through). A piece's ring slot is released when its outputs
+        // are issued.
+        auto peek = [&](int k, bool &ok) -> Piece {
+            Piece P{};
+            P.b = -1;
+            ok = wait(kBarUnitFull + k % kUnitSlots, (k / kUnitSlots) & 1);
+            if (ok) P = *slot_of(k);
+            __syncwarp();
+            return P;
+        };
+        auto release = [&](int k) {
+            if (lane == 0) mbar_arrive(bar(kBarUnitEmpty + k % kUnitSlots));
+            __syncwarp();
+        };
+        int t = 0, live = 0;            // tiles, and pieces with tiles, whose outputs are issued
+        int ts = 0, hk = -1, hl = -1;   // tiles, pieces, and pieces with tiles of the scores
+        int left = 0;                   // tiles of piece hk without scores yet
+        bool ok = true, ended = false;
         int k = 0;
+        auto scores_ahead = [&]() {
+            while (ok && ts - t < kSB) {
+                while (left == 0) {
+                    // the ring holds kUnitSlots pieces: never wait for one that cannot come
+                    if (ended || hk + 1 - k >= kUnitSlots - 1 || (kQT && ts > t)) return;
+                    const Piece N = peek(++hk, ok);
+                    if (!ok) return;
+                    if (N.b < 0) {
+                        ended = true;
+                        return;
+                    }
+                    left = N.j1 - N.j0 + 1;
+                    if (left > 0) {
+                        ++hl;
+                        ok = wait(kQT ? kBarQReady : kBarQFull + hl % kQStages, (hl / kQStages) & 1);
+                        if (!ok) return;
+                    }
+                }
+                ok = wait(kBarKFull + ts % kKStages, (ts / kKStages) & 1);
+                if (!ok) return;
+                issue_s(ts, hl);  // buffer ts mod kSB, whose P was read by an output issued before
+                commit(kBarKEmpty + ts % kKStages);  // K is read by S only
+                ++ts;
+                if (--left == 0 && !kQT) commit(kBarQEmpty + hl % kQStages);
+            }
+        };
         for (; ok; ++k) {
-            const Piece P = take(k, ok);
+            const Piece P = peek(k, ok);
             if (!ok || P.b < 0) break;
             const int n = P.j1 - P.j0 + 1;
-            if (n <= 0) continue;
-            ok = wait(kQT ? kBarQReady : kBarQFull, live & 1);
-            for (int x = 0; ok && x < n && x < kSB; ++x) {
-                ok = wait(kBarKFull + (t + x) % kKStages, ((t + x) / kKStages) & 1);
-                if (ok) {
-                    issue_s(t + x);
-                    commit(kBarKEmpty + (t + x) % kKStages);  // K is read by S only
-                }
-            }
             for (int x = 0; ok && x < n; ++x, ++t) {
+                scores_ahead();
+                if (!ok) break;
                 ok = wait(kBarPFull + t % kSB, (t / kSB) & 1) &&
                      wait(kBarVFull + t % kVStages, (t / kVStages) & 1);
                 if (ok && x == 0 && live > 0) ok = wait(kBarOFree, (live - 1) & 1);
@@ -660,17 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kv0 < P.lo_key || kv0 + kBN - 1 > P.hi_key) zero_rows(t, kv0, P.lo_key, P.hi_key);
                 issue_pv(t, x == 0);
                 commit(kBarVEmpty + t % kVStages);
-                if (x + kSB < n) {
-                    ok = wait(kBarKFull + (t + kSB) % kKStages, ((t + kSB) / kKStages) & 1);
-                    if (!ok) break;
-                    issue_s(t + kSB);  // reuses buffer t mod kSB after O += P(t) V_t
-                    commit(kBarKEmpty + (t + kSB) % kKStages);
-                }
             }
             if (!ok) break;
-            if constexpr (!kQT) commit(kBarQEmpty);
-            commit(kBarODone);
-            ++live;
+            if (n > 0) {
+                commit(kBarODone);
+                ++live;
+            }
+            if (hk < k) hk = k;  // the scores are not behind (a piece without tiles)
+            release(k);
         }
         if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleMma, k);
         if (elect_one()) umma_commit(bar(kBarDrain));
@@ -934,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the cut units, a unit per block in turn: with O_s, LSE_s of piece s
 //     LSE = ln sum_s exp(LSE_s)          O = sum_s exp(LSE_s - LSE) O_s
-// around the largest LSE_s. A row is summed by one warp, or by 2, 4 or 8 over as many
+// around the largest LSE_s (blockIdx.y shares a unit's rows). A row is summed by one warp, or by 2, 4 or 8 over as many
 // runs of its pieces when there are fewer rows than warps; always in the same order.
 struct MergeParams {
     const MergeInfo *info;
@@ -969,7 +1038,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
         while (ways < kMergeWarps && u.rows * ways * 2 <= kMergeWarps) ways *= 2;
         const int per = (n + ways - 1) / ways, run = warp % ways;
         const int s_lo = min(run * per, n), s_hi = min(s_lo + per, n);
-        for (int row0 = 0; row0 < u.rows; row0 += kMergeWarps / ways) {
+        for (int row0 = blockIdx.y * (kMergeWarps / ways); row0 < u.rows;
+             row0 += gridDim.y * (kMergeWarps / ways)) {
             const int row = row0 + warp / ways;
             const bool there = row < u.rows;
             auto prow = [&](int s) {

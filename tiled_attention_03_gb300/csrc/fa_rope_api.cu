@@ -30,11 +30,15 @@ bool there(const fa_rows *r) { return r != nullptr && r->data != nullptr; }
 
 // Elements from the first to the last of a tensor, or 0 when that does not fit 2^60.
 int64_t extent(const Tensor &t, int64_t d) {
-    const double e = static_cast<double>(t.B - 1) * static_cast<double>(t.r->batch) +
-                     static_cast<double>(t.heads - 1) * static_cast<double>(t.r->head) +
-                     static_cast<double>(t.N - 1) * static_cast<double>(t.r->token);
+    const int64_t st[3] = {t.r->batch, t.r->head, t.r->token}, n[3] = {t.B, t.heads, t.N};
+    double e = 0;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1) e += static_cast<double>(n[i] - 1) * static_cast<double>(st[i]);
     if (e > 1e18) return 0;
-    return (t.B - 1) * t.r->batch + (t.heads - 1) * t.r->head + (t.N - 1) * t.r->token + d;
+    int64_t sum = d;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1) sum += (n[i] - 1) * st[i];
+    return sum;
 }
 
 // Whether no two elements of a written tensor share a place: with the dimensions that
@@ -64,9 +68,10 @@ bool injective(const Tensor &t, int64_t d) {
 // each token's part shorter than s, and the two parts at different places modulo s.
 bool interleaved(const Tensor &a, const Tensor &b, int64_t d) {
     const int64_t s = a.r->token;
-    if (s < 1 || b.r->token != s) return false;
+    if (a.N < 2 || s < 1 || b.r->token != s) return false;
     if (a.B > 1 && (a.r->batch != b.r->batch || a.r->batch % s != 0)) return false;
-    const int64_t span_a = (a.heads - 1) * a.r->head + d, span_b = (b.heads - 1) * b.r->head + d;
+    const int64_t span_a = a.heads > 1 ? (a.heads - 1) * a.r->head + d : d;
+    const int64_t span_b = b.heads > 1 ? (b.heads - 1) * b.r->head + d : d;
     const intptr_t bytes = reinterpret_cast<intptr_t>(b.r->data) - reinterpret_cast<intptr_t>(a.r->data);
     int64_t off = (bytes / 2) % s;
     if (off < 0) off += s;
@@ -80,8 +85,10 @@ fa_status check_tensors(const Tensor *t, int count, int64_t d) {
         if (!there(t[i].r)) continue;
         const fa_rows &r = *t[i].r;
         if (!fa_host::aligned16(r.data)) return FA_ERR_INVALID_ARG;
-        for (int64_t s : {r.batch, r.head, r.token})
-            if (s < 0 || s % 8 != 0 || s >= (int64_t{1} << 40)) return FA_ERR_INVALID_ARG;
+        const int64_t st[3] = {r.batch, r.head, r.token}, n[3] = {t[i].B, t[i].heads, t[i].N};
+        for (int x = 0; x < 3; ++x)  // the stride of a single entry does not matter
+            if (n[x] > 1 && (st[x] < 0 || st[x] % 8 != 0 || st[x] >= (int64_t{1} << 40)))
+                return FA_ERR_INVALID_ARG;
         if (extent(t[i], d) == 0) return FA_ERR_UNSUPPORTED;
         if (t[i].written && !injective(t[i], d)) return FA_ERR_INVALID_ARG;
     }
