@@ -71,41 +71,26 @@ Layout layout_of(int64_t d, int64_t sms) {
     return l;
 }
 
-// The merge, launched while the attention kernel runs (see wait_for_previous_grid).
-template <int D, bool BF16, int kRows>
-cudaError_t launch_merge(const fa::paged::MergeParams &m, dim3 blocks, cudaStream_t st) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = blocks;
-    cfg.blockDim = dim3(fa::paged::kMergeWarps * 32);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa::paged::fa_paged_merge_kernel<D, BF16, kRows>, m);
-}
-
 template <int D, bool BF16>
 cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                   const fa::paged::Params &p, fa::paged::MergeParams m, unsigned sms, cudaStream_t st) {
-    fa::paged::fa_paged_kernel<D, BF16>
-        <<<sms, fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st>>>(q, k, v, p);
-    const cudaError_t e = cudaGetLastError();
+                   const fa::paged::Params &p, const fa::paged::MergeParams &m, unsigned sms, cudaStream_t st) {
+    const cudaError_t e = fa::launch_after(fa::paged::fa_paged_kernel<D, BF16>, dim3(sms),
+                                           fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st, q, k, v, p);
     if (e != cudaSuccess) return e;
-    m.workers = static_cast<int>(sms);
-    return launch_merge<D, BF16, fa::paged::kBM>(m, dim3(sms, 8), st);
+    return fa::launch_after(fa::paged::fa_paged_merge_kernel<D, BF16, fa::paged::kBM>, dim3(sms, 16),
+                            fa::paged::kMergeWarps * 32, 0, st, m);
 }
 
 template <int D, bool BF16>
-cudaError_t launch_decode(const fa::paged::SmallParams &p, fa::paged::MergeParams m, unsigned sms,
+cudaError_t launch_decode(const fa::paged::SmallParams &p, const fa::paged::MergeParams &m, unsigned sms,
                           cudaStream_t st) {
     using L = fa::paged::Small<D>;
-    fa::paged::fa_paged_decode_kernel<D, BF16><<<sms, L::kWarps * 32, L::kBytes, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = fa::launch_after(fa::paged::fa_paged_decode_kernel<D, BF16>, dim3(sms),
+                                           L::kWarps * 32, L::kBytes, st, p);
     if (e != cudaSuccess) return e;
-    m.workers = static_cast<int>(sms) * L::kWarps;
-    return launch_merge<D, BF16, fa::paged::kSmallRows>(m, dim3(sms * L::kWarps / 2), st);
+    return fa::launch_after(fa::paged::fa_paged_merge_kernel<D, BF16, fa::paged::kSmallRows>,
+                            dim3(sms * L::kWarps),
+                            fa::paged::kMergeWarps * 32, 0, st, m);
 }
 
 int sm_count_or_default() {

@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
     // neighbouring shares on different SMs: few shares still use all of them
     const unsigned worker = warp * gridDim.x + blockIdx.x;
     const unsigned workers = kWarps * gridDim.x;
-    allow_next_grid();
+    after_previous();
+    let_next_start();
 
     // ---- this warp's share: ticks w0 .. w1 - 1 of W
     unsigned mine = 0, first = 0;

@@ -40,6 +40,7 @@
 #include <cuda.h>
 
 #include "fa_mask.cuh"
+#include "fa_pdl.cuh"
 #include "fa_tmem_max.cuh"
 #include "ptx.cuh"
 
@@ -211,11 +212,6 @@ __device__ __forceinline__ void record_timeout(const Params &p, volatile int *ab
     }
 }
 
-// Lets the next grid of the stream be launched before this one ends (see the merge).
-__device__ __forceinline__ void allow_next_grid() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // 5-D tiled copy global -> shared, completion counted on mbarrier `bar`.
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                             int32_t c0, int32_t c1, int32_t c2, int32_t c3, int32_t c4) {
@@ -307,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint64_t budget = p.wait_budget_ns;
-    allow_next_grid();
+    after_previous();
+    let_next_start();
 
     // ---- this CTA's share of the line of work: ticks w0 .. w1 - 1 of W. B sequences are
     // summed, and then searched for w0, 256 at a time.
@@ -670,60 +667,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
         };
-        // The scores run ahead of the outputs by up to kSB tiles, into the next pieces as
-        // well (at d = 256 within a piece only: the next Q replaces this one in TMEM once
-        // the softmax is through). A piece's ring slot is released when its outputs
-        // are issued.
-        auto peek = [&](int k, bool &ok) -> Piece {
-            Piece P{};
-            P.b = -1;
-            ok = wait(kBarUnitFull + k % kUnitSlots, (k / kUnitSlots) & 1);
-            if (ok) P = *slot_of(k);
-            __syncwarp();
-            return P;
-        };
-        auto release = [&](int k) {
-            if (lane == 0) mbar_arrive(bar(kBarUnitEmpty + k % kUnitSlots));
-            __syncwarp();
-        };
-        int t = 0, live = 0;            // tiles, and pieces with tiles, whose outputs are issued
-        int ts = 0, hk = -1, hl = -1;   // tiles, pieces, and pieces with tiles of the scores
-        int left = 0;                   // tiles of piece hk without scores yet
-        bool ok = true, ended = false;
+        int t = 0, live = 0;
+        bool ok = true;
         int k = 0;
-        auto scores_ahead = [&]() {
-            while (ok && ts - t < kSB) {
-                while (left == 0) {
-                    // the ring holds kUnitSlots pieces: never wait for one that cannot come
-                    if (ended || hk + 1 - k >= kUnitSlots - 1 || (kQT && ts > t)) return;
-                    const Piece N = peek(++hk, ok);
-                    if (!ok) return;
-                    if (N.b < 0) {
-                        ended = true;
-                        return;
-                    }
-                    left = N.j1 - N.j0 + 1;
-                    if (left > 0) {
-                        ++hl;
-                        ok = wait(kQT ? kBarQReady : kBarQFull + hl % kQStages, (hl / kQStages) & 1);
-                        if (!ok) return;
-                    }
-                }
-                ok = wait(kBarKFull + ts % kKStages, (ts / kKStages) & 1);
-                if (!ok) return;
-                issue_s(ts, hl);  // buffer ts mod kSB, whose P was read by an output issued before
-                commit(kBarKEmpty + ts % kKStages);  // K is read by S only
-                ++ts;
-                if (--left == 0 && !kQT) commit(kBarQEmpty + hl % kQStages);
-            }
-        };
         for (; ok; ++k) {
-            const Piece P = peek(k, ok);
+            const Piece P = take(k, ok);
             if (!ok || P.b < 0) break;
             const int n = P.j1 - P.j0 + 1;
+            if (n <= 0) continue;
+            ok = wait(kQT ? kBarQReady : kBarQFull + live % kQStages, (live / kQStages) & 1);
+            for (int x = 0; ok && x < n && x < kSB; ++x) {
+                ok = wait(kBarKFull + (t + x) % kKStages, ((t + x) / kKStages) & 1);
+                if (ok) {
+                    issue_s(t + x, live);
+                    commit(kBarKEmpty + (t + x) % kKStages);  // K is read by S only
+                }
+            }
             for (int x = 0; ok && x < n; ++x, ++t) {
-                scores_ahead();
-                if (!ok) break;
                 ok = wait(kBarPFull + t % kSB, (t / kSB) & 1) &&
                      wait(kBarVFull + t % kVStages, (t / kVStages) & 1);
                 if (ok && x == 0 && live > 0) ok = wait(kBarOFree, (live - 1) & 1);
@@ -732,14 +692,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kv0 < P.lo_key || kv0 + kBN - 1 > P.hi_key) zero_rows(t, kv0, P.lo_key, P.hi_key);
                 issue_pv(t, x == 0);
                 commit(kBarVEmpty + t % kVStages);
+                if (x + kSB < n) {
+                    ok = wait(kBarKFull + (t + kSB) % kKStages, ((t + kSB) / kKStages) & 1);
+                    if (!ok) break;
+                    issue_s(t + kSB, live);
+                    commit(kBarKEmpty + (t + kSB) % kKStages);
+                }
             }
             if (!ok) break;
-            if (n > 0) {
-                commit(kBarODone);
-                ++live;
-            }
-            if (hk < k) hk = k;  // the scores are not behind (a piece without tiles)
-            release(k);
+            if constexpr (!kQT) commit(kBarQEmpty + live % kQStages);
+            commit(kBarODone);
+            ++live;
         }
         if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleMma, k);
         if (elect_one()) umma_commit(bar(kBarDrain));
@@ -1001,118 +964,123 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the pieces of the cut units, a unit per block in turn: with O_s, LSE_s of piece s
+// Joins the pieces of the cut units, block c the unit that starts in worker c's share: with O_s, LSE_s of piece s
 //     LSE = ln sum_s exp(LSE_s)          O = sum_s exp(LSE_s - LSE) O_s
-// around the largest LSE_s (blockIdx.y shares a unit's rows). A row is summed by one warp, or by 2, 4 or 8 over as many
-// runs of its pieces when there are fewer rows than warps; always in the same order.
+// around the largest LSE_s (blockIdx.y shares a unit's rows). A row is summed by one warp, or
+// by 2 .. 8 over as many runs of its pieces when there are fewer rows than warps, always in
+// the same order. Bound by latency: every worker has a block of its own, all of them resident
+// at once, and a unit's statistics and outputs are requested together, kMergeBatch pieces
+// of a warp at a time (304 blocks that took several workers each in turn: 13 us after a
+// decode kernel of 157 us, against about 3).
 struct MergeParams {
     const MergeInfo *info;
     const float *part_O, *part_LSE;
     void *O;
     float *LSE;
-    int workers, H, pf;
+    int H, pf;
 };
 
 constexpr int kMergeWarps = 8;
-
-// Programmatic dependent launch: the merge is launched while the attention kernel still
-// runs (its blocks wait here until that grid has finished and its stores are visible), so
-// that its launch costs no time of its own.
-__device__ __forceinline__ void wait_for_previous_grid() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 
 // kRows: rows of a partial slot.
 template <int D, bool BF16, int kRows>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const MergeParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kV = D / 32;  // consecutive columns per lane
+    constexpr int kMergeBatch = D <= 128 ? 8 : 4;
     __shared__ float red_o[kMergeWarps][D];
     __shared__ float red_m[kMergeWarps], red_w[kMergeWarps];
-    wait_for_previous_grid();
-    for (int c = blockIdx.x; c < p.workers; c += gridDim.x) {
-        const MergeInfo u = p.info[c];
-        if (u.last_cta < 0) continue;
-        const int n = u.last_cta - c + 1;
-        int ways = 1;  // warps per row
-        while (ways < kMergeWarps && u.rows * ways * 2 <= kMergeWarps) ways *= 2;
-        const int per = (n + ways - 1) / ways, run = warp % ways;
-        const int s_lo = min(run * per, n), s_hi = min(s_lo + per, n);
-        for (int row0 = blockIdx.y * (kMergeWarps / ways); row0 < u.rows;
-             row0 += gridDim.y * (kMergeWarps / ways)) {
-            const int row = row0 + warp / ways;
-            const bool there = row < u.rows;
-            auto prow = [&](int s) {
-                return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * kRows + row;
-            };
-            float m = -INFINITY, wsum = 0.f, acc[kV];
+    after_previous();
+    let_next_start();
+    const int c = blockIdx.x;
+    const MergeInfo u = p.info[c];
+    if (u.last_cta < 0) return;
+    const int n = u.last_cta - c + 1;
+    int ways = 1;  // warps per row
+    while (ways < kMergeWarps && u.rows * ways * 2 <= kMergeWarps) ways *= 2;
+    const int per = (n + ways - 1) / ways, run = warp % ways;
+    const int s_lo = min(run * per, n), s_hi = min(s_lo + per, n);
+    for (int row0 = blockIdx.y * (kMergeWarps / ways); row0 < u.rows;
+         row0 += gridDim.y * (kMergeWarps / ways)) {
+        const int row = row0 + warp / ways;
+        const bool there = row < u.rows;
+        auto prow = [&](int s) {
+            return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * kRows + row;
+        };
+        float m = -INFINITY, wsum = 0.f, acc[kV];
 #pragma unroll
-            for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-            // every lane the weight of one piece, 32 at a time, around a running maximum;
-            // an empty piece (LSE = -inf) weighs 0
-            for (int s0 = s_lo; there && s0 < s_hi; s0 += 32) {
-                const float x = s0 + lane < s_hi ? p.part_LSE[prow(s0 + lane)] : -INFINITY;
-                float top = x;
+        for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+        for (int s0 = s_lo; there && s0 < s_hi; s0 += kMergeBatch) {
+            const int ns = min(kMergeBatch, s_hi - s0);
+            float o[kMergeBatch][kV];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float m_new = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.f : expf(m - m_new);
-                m = m_new;
-                wsum *= f;
+            for (int s = 0; s < kMergeBatch; ++s) {
+                const float *src = p.part_O + prow(s0 + min(s, ns - 1)) * D + lane * kV;
 #pragma unroll
-                for (int e = 0; e < kV; ++e) acc[e] *= f;
-                const float w = x == -INFINITY ? 0.f : expf(x - m);
-                const int ns = min(32, s_hi - s0);
-#pragma unroll 4
-                for (int s = 0; s < ns; ++s) {
-                    const float ws = __shfl_sync(0xffffffffu, w, s);
-                    const float *o = p.part_O + prow(s0 + s) * D + lane * kV;
-                    wsum += ws;
-#pragma unroll
-                    for (int e = 0; e < kV; ++e) acc[e] = fmaf(ws, o[e], acc[e]);
-                }
+                for (int e = 0; e < kV; ++e) o[s][e] = src[e];
             }
-            if (ways > 1) {
-                __syncthreads();
+            // lane s the statistic of piece s0 + s; an empty piece (-inf) weighs 0
+            const float x = lane < ns ? p.part_LSE[prow(s0 + lane)] : -INFINITY;
+            float top = x;
 #pragma unroll
-                for (int e = 0; e < kV; ++e) red_o[warp][lane * kV + e] = acc[e];
-                if (lane == 0) red_m[warp] = m, red_w[warp] = wsum;
-                __syncthreads();
-                if (run == 0) {
-                    float top = m;
-                    for (int i = 1; i < ways; ++i) top = fmaxf(top, red_m[warp + i]);
-                    float total = 0.f;
+            for (int d = kMergeBatch / 2; d > 0; d >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float m_new = fmaxf(m, __shfl_sync(0xffffffffu, top, 0));
+            const float f = m == -INFINITY ? 0.f : expf(m - m_new);
+            m = m_new;
+            wsum *= f;
 #pragma unroll
-                    for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-                    for (int i = 0; i < ways; ++i) {
-                        // a run that saw nothing adds nothing; one with NaN adds it
-                        if (red_m[warp + i] == -INFINITY && red_w[warp + i] == 0.f) continue;
-                        const float f = red_m[warp + i] == top ? 1.f : expf(red_m[warp + i] - top);
-                        total = fmaf(f, red_w[warp + i], total);
+            for (int e = 0; e < kV; ++e) acc[e] *= f;
+            const float w = x == -INFINITY ? 0.f : expf(x - m);
 #pragma unroll
-                        for (int e = 0; e < kV; ++e) acc[e] = fmaf(f, red_o[warp + i][lane * kV + e], acc[e]);
-                    }
-                    m = top;
-                    wsum = total;
-                }
+            for (int s = 0; s < kMergeBatch; ++s) {
+                const float ws = __shfl_sync(0xffffffffu, w, s);
+                if (s >= ns) break;
+                wsum += ws;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] = fmaf(ws, o[s][e], acc[e]);
             }
-            if (!there || run != 0) continue;
-            const bool none = wsum == 0.f;
-            const float inv = none ? 0.f : 1.f / wsum;
-#pragma unroll
-            for (int e = 0; e < kV; ++e) acc[e] *= inv;
-            const int i = row / p.pf;
-            const size_t g = (static_cast<size_t>(u.tok0) + i) * p.H + u.head0 + (row - i * p.pf);
-            uint16_t *orow = reinterpret_cast<uint16_t *>(p.O) + g * D + lane * kV;
-            if constexpr (kV == 1) {
-                orow[0] = static_cast<uint16_t>(pack2<BF16>(acc[0], 0.f) & 0xffffu);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kV; e += 2)
-                    *reinterpret_cast<uint32_t *>(orow + e) = pack2<BF16>(acc[e], acc[e + 1]);
-            }
-            if (lane == 0) p.LSE[g] = none ? -INFINITY : m + logf(wsum);
         }
+        if (ways > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kV; ++e) red_o[warp][lane * kV + e] = acc[e];
+            if (lane == 0) red_m[warp] = m, red_w[warp] = wsum;
+            __syncthreads();
+            if (run == 0) {
+                float top = m;
+                for (int i = 1; i < ways; ++i) top = fmaxf(top, red_m[warp + i]);
+                float total = 0.f;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+                for (int i = 0; i < ways; ++i) {
+                    // a run that saw nothing adds nothing; one with NaN adds it
+                    if (red_m[warp + i] == -INFINITY && red_w[warp + i] == 0.f) continue;
+                    const float f = red_m[warp + i] == top ? 1.f : expf(red_m[warp + i] - top);
+                    total = fmaf(f, red_w[warp + i], total);
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) acc[e] = fmaf(f, red_o[warp + i][lane * kV + e], acc[e]);
+                }
+                m = top;
+                wsum = total;
+            }
+        }
+        if (!there || run != 0) continue;
+        const bool none = wsum == 0.f;
+        const float inv = none ? 0.f : 1.f / wsum;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] *= inv;
+        const int i = row / p.pf;
+        const size_t g = (static_cast<size_t>(u.tok0) + i) * p.H + u.head0 + (row - i * p.pf);
+        uint16_t *orow = reinterpret_cast<uint16_t *>(p.O) + g * D + lane * kV;
+        if constexpr (kV == 1) {
+            orow[0] = static_cast<uint16_t>(pack2<BF16>(acc[0], 0.f) & 0xffffu);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kV; e += 2)
+                *reinterpret_cast<uint32_t *>(orow + e) = pack2<BF16>(acc[e], acc[e + 1]);
+        }
+        if (lane == 0) p.LSE[g] = none ? -INFINITY : m + logf(wsum);
     }
 }
 

@@ -8,6 +8,7 @@
 #include "fa.h"
 #include "fa_host.h"
 #include "fa_paged_host.h"
+#include "fa_pdl.cuh"
 #include "fa_rope_kernel.cuh"
 
 namespace {
@@ -184,45 +185,37 @@ unsigned blocks_of(const Params &p, int most_blocks) {
 }
 
 template <int D, bool BF16, bool PAGED>
-void forward_mode(const Params &p, int mode, unsigned g, cudaStream_t st) {
-    if (mode == fa::rope::kBeside)
-        fa::rope::fa_norm_rope_kernel<D, BF16, fa::rope::kBeside, PAGED><<<g, fa::rope::kThreads, 0, st>>>(p);
-    else if (mode == fa::rope::kLane)
-        fa::rope::fa_norm_rope_kernel<D, BF16, fa::rope::kLane, PAGED><<<g, fa::rope::kThreads, 0, st>>>(p);
-    else
-        fa::rope::fa_norm_rope_kernel<D, BF16, fa::rope::kAnywhere, PAGED><<<g, fa::rope::kThreads, 0, st>>>(p);
+cudaError_t forward_mode(const Params &p, int mode, unsigned g, cudaStream_t st) {
+    using namespace fa::rope;
+    auto *k = mode == kBeside ? fa_norm_rope_kernel<D, BF16, kBeside, PAGED>
+              : mode == kLane ? fa_norm_rope_kernel<D, BF16, kLane, PAGED>
+                              : fa_norm_rope_kernel<D, BF16, kAnywhere, PAGED>;
+    return fa::launch_after(k, g, kThreads, 0, st, p);
 }
 template <int D, bool BF16>
-void backward_mode(const Params &p, int mode, unsigned g, cudaStream_t st) {
-    if (mode == fa::rope::kBeside)
-        fa::rope::fa_norm_rope_bwd_kernel<D, BF16, fa::rope::kBeside><<<g, fa::rope::kThreads, 0, st>>>(p);
-    else if (mode == fa::rope::kLane)
-        fa::rope::fa_norm_rope_bwd_kernel<D, BF16, fa::rope::kLane><<<g, fa::rope::kThreads, 0, st>>>(p);
-    else
-        fa::rope::fa_norm_rope_bwd_kernel<D, BF16, fa::rope::kAnywhere><<<g, fa::rope::kThreads, 0, st>>>(p);
+cudaError_t backward_mode(const Params &p, int mode, unsigned g, cudaStream_t st) {
+    using namespace fa::rope;
+    auto *k = mode == kBeside ? fa_norm_rope_bwd_kernel<D, BF16, kBeside>
+              : mode == kLane ? fa_norm_rope_bwd_kernel<D, BF16, kLane>
+                              : fa_norm_rope_bwd_kernel<D, BF16, kAnywhere>;
+    return fa::launch_after(k, g, kThreads, 0, st, p);
 }
 template <bool PAGED>
 cudaError_t forward(const Params &p, int64_t d, bool bf16, int mode, unsigned g, cudaStream_t st) {
-    if (d == 32)
-        bf16 ? forward_mode<32, true, PAGED>(p, mode, g, st) : forward_mode<32, false, PAGED>(p, mode, g, st);
-    else if (d == 64)
-        bf16 ? forward_mode<64, true, PAGED>(p, mode, g, st) : forward_mode<64, false, PAGED>(p, mode, g, st);
-    else if (d == 128)
-        bf16 ? forward_mode<128, true, PAGED>(p, mode, g, st) : forward_mode<128, false, PAGED>(p, mode, g, st);
-    else
-        bf16 ? forward_mode<256, true, PAGED>(p, mode, g, st) : forward_mode<256, false, PAGED>(p, mode, g, st);
-    return cudaGetLastError();
+    switch (d) {
+        case 32: return bf16 ? forward_mode<32, true, PAGED>(p, mode, g, st) : forward_mode<32, false, PAGED>(p, mode, g, st);
+        case 64: return bf16 ? forward_mode<64, true, PAGED>(p, mode, g, st) : forward_mode<64, false, PAGED>(p, mode, g, st);
+        case 128: return bf16 ? forward_mode<128, true, PAGED>(p, mode, g, st) : forward_mode<128, false, PAGED>(p, mode, g, st);
+        default: return bf16 ? forward_mode<256, true, PAGED>(p, mode, g, st) : forward_mode<256, false, PAGED>(p, mode, g, st);
+    }
 }
 cudaError_t backward(const Params &p, int64_t d, bool bf16, int mode, unsigned g, cudaStream_t st) {
-    if (d == 32)
-        bf16 ? backward_mode<32, true>(p, mode, g, st) : backward_mode<32, false>(p, mode, g, st);
-    else if (d == 64)
-        bf16 ? backward_mode<64, true>(p, mode, g, st) : backward_mode<64, false>(p, mode, g, st);
-    else if (d == 128)
-        bf16 ? backward_mode<128, true>(p, mode, g, st) : backward_mode<128, false>(p, mode, g, st);
-    else
-        bf16 ? backward_mode<256, true>(p, mode, g, st) : backward_mode<256, false>(p, mode, g, st);
-    return cudaGetLastError();
+    switch (d) {
+        case 32: return bf16 ? backward_mode<32, true>(p, mode, g, st) : backward_mode<32, false>(p, mode, g, st);
+        case 64: return bf16 ? backward_mode<64, true>(p, mode, g, st) : backward_mode<64, false>(p, mode, g, st);
+        case 128: return bf16 ? backward_mode<128, true>(p, mode, g, st) : backward_mode<128, false>(p, mode, g, st);
+        default: return bf16 ? backward_mode<256, true>(p, mode, g, st) : backward_mode<256, false>(p, mode, g, st);
+    }
 }
 
 // Resident blocks per SM (the kernels' launch bounds): the blocks of a launch at most.
@@ -405,9 +398,10 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
     if (backward(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks, st) != cudaSuccess) return FA_ERR_CUDA;
     fa_host::count_launches(1);
     if (p.part != nullptr) {
-        fa::rope::fa_norm_rope_sum_kernel<<<static_cast<unsigned>(2 * d / 32), fa::rope::kSumThreads, 0, st>>>(
-            p.part, static_cast<int>(blocks), static_cast<int>(d), dq_weight, dk_weight);
-        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+        if (fa::launch_after(fa::rope::fa_norm_rope_sum_kernel, static_cast<unsigned>(2 * d / 32),
+                             fa::rope::kSumThreads, 0, st, static_cast<const float *>(p.part),
+                             static_cast<int>(blocks), static_cast<int>(d), dq_weight, dk_weight) != cudaSuccess)
+            return FA_ERR_CUDA;
         fa_host::count_launches(1);
     }
     return FA_OK;

@@ -24,6 +24,7 @@
 #include <cstdint>
 
 #include "fa.h"
+#include "fa_pdl.cuh"
 #include "ptx.cuh"
 
 namespace fa {
@@ -332,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, 3) fa_norm_rope_kernel(const Params 
     Cursor in, at;
     in.start(p, static_cast<long long>(blockIdx.x) * kWarps + warp);
     at = in;
+    after_previous();
+    let_next_start();
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) {
         issue(in, i);
@@ -444,6 +447,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
     Cursor in, at;
     in.start(p, static_cast<long long>(blockIdx.x) * kWarps + warp);
     at = in;
+    after_previous();
+    let_next_start();
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) {
         issue(in, i);
@@ -539,6 +544,8 @@ constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads)
     fa_norm_rope_sum_kernel(const float *part, int blocks, int D, float *dwq, float *dwk) {
     __shared__ float red[32][33];
+    after_previous();
+    let_next_start();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
     float s = 0.f;
     for (int b = r; b < blocks; b += 32) s += part[static_cast<size_t>(b) * 2 * D + c];
