@@ -219,7 +219,7 @@ cudaError_t backward(const Params &p, int64_t d, bool bf16, int mode, unsigned g
 }
 
 // Resident blocks per SM (the kernels' launch bounds): the blocks of a launch at most.
-constexpr int kBlocksPerSm = 3;
+constexpr int kBlocksPerSm = 2;
 constexpr int kBackwardBlocksPerSm = 2;  // each leaves 2 d partial sums
 
 int sm_count_or_default() {

@@ -77,17 +77,55 @@ __device__ __forceinline__ void unpack2(uint32_t w, float &lo, float &hi) {
             : "r"(w));
     }
 }
+
+// Two floats in one 64-bit register pair. The rows stay packed from their 16-bit words to
+// the result's: every multiply and add below is one instruction for two elements.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 both(float x) { return f2_pack(x, x); }
+
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
-    unpack2<BF16>(v.x, x[0], x[1]);
-    unpack2<BF16>(v.y, x[2], x[3]);
-    unpack2<BF16>(v.z, x[4], x[5]);
-    unpack2<BF16>(v.w, x[6], x[7]);
+__device__ __forceinline__ f2 unpack_pair(uint32_t w) {
+    float lo, hi;
+    unpack2<BF16>(w, lo, hi);
+    return f2_pack(lo, hi);
 }
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
-    return make_uint4(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]), pack2<BF16>(y[4], y[5]),
-                      pack2<BF16>(y[6], y[7]));
+__device__ __forceinline__ void unpack8(const uint4 &v, f2 (&x)[4]) {
+    x[0] = unpack_pair<BF16>(v.x);
+    x[1] = unpack_pair<BF16>(v.y);
+    x[2] = unpack_pair<BF16>(v.z);
+    x[3] = unpack_pair<BF16>(v.w);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_pair(f2 x) {
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    return pack2<BF16>(lo, hi);
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const f2 (&y)[4]) {
+    return make_uint4(pack_pair<BF16>(y[0]), pack_pair<BF16>(y[1]), pack_pair<BF16>(y[2]),
+                      pack_pair<BF16>(y[3]));
+}
+__device__ __forceinline__ f2 swapped(f2 x) {
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    return f2_pack(hi, lo);
 }
 template <bool BF16>
 __device__ __forceinline__ float load1(const uint16_t *p) {
@@ -143,100 +181,109 @@ __device__ __forceinline__ void angles(float (&cs)[2][kMaxPairs], const Params &
 // the first element of a pair); C = 1, S = 0 past the rotated ones.
 template <int MODE>
 __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], int half_r, int l,
-                                             float (&C)[8], float (&S)[8]) {
+                                             f2 (&C)[4], f2 (&S)[4]) {
     if constexpr (MODE == kLane) {
         const bool first = 8 * l < half_r, rotated = 8 * l < 2 * half_r;
         const int j = first ? 8 * l : 8 * l - half_r;
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
+        for (int e = 0; e < 4; e += 2) {
             const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 c = rotated ? *reinterpret_cast<const float4 *>(&cs[0][j + e]) : one;
-            const float4 s = rotated ? *reinterpret_cast<const float4 *>(&cs[1][j + e]) : zero;
-            C[e] = c.x, C[e + 1] = c.y, C[e + 2] = c.z, C[e + 3] = c.w;
-            S[e] = first ? -s.x : s.x, S[e + 1] = first ? -s.y : s.y;
-            S[e + 2] = first ? -s.z : s.z, S[e + 3] = first ? -s.w : s.w;
+            const float4 c = rotated ? *reinterpret_cast<const float4 *>(&cs[0][j + 2 * e]) : one;
+            const float4 s = rotated ? *reinterpret_cast<const float4 *>(&cs[1][j + 2 * e]) : zero;
+            const f2 sign = both(first ? -1.f : 1.f);
+            C[e] = f2_pack(c.x, c.y), C[e + 1] = f2_pack(c.z, c.w);
+            S[e] = mul2(f2_pack(s.x, s.y), sign), S[e + 1] = mul2(f2_pack(s.z, s.w), sign);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = 8 * l + e;
-            C[e] = 1.f;
-            S[e] = 0.f;
-            if (i < 2 * half_r) {
-                const bool first = MODE == kBeside ? (e & 1) == 0 : i < half_r;
-                const int j = MODE == kBeside ? i >> 1 : (first ? i : i - half_r);
-                C[e] = cs[0][j];
-                const float s = cs[1][j];
-                S[e] = first ? -s : s;
+        for (int e = 0; e < 4; ++e) {
+            float c[2], t[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = 8 * l + 2 * e + x;
+                c[x] = 1.f;
+                t[x] = 0.f;
+                if (i < 2 * half_r) {
+                    const bool first = MODE == kBeside ? x == 0 : i < half_r;
+                    const int j = MODE == kBeside ? i >> 1 : (first ? i : i - half_r);
+                    c[x] = cs[0][j];
+                    t[x] = first ? -cs[1][j] : cs[1][j];
+                }
             }
+            C[e] = f2_pack(c[0], c[1]);
+            S[e] = f2_pack(t[0], t[1]);
         }
     }
 }
 
 // The weight at elements 8 l + e (1 without one), and at their partners.
 template <bool BF16>
-__device__ __forceinline__ void weights(const uint16_t *w, int l, float (&x)[8]) {
+__device__ __forceinline__ void weights(const uint16_t *w, int l, f2 (&x)[4]) {
     if (w == nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 1.f;
+        for (int e = 0; e < 4; ++e) x[e] = both(1.f);
     } else {
         unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(w + 8 * l)), x);
     }
 }
 template <bool BF16, int MODE>
-__device__ __forceinline__ void partner_weights(const uint16_t *w, int half_r, int l, float (&x)[8]) {
+__device__ __forceinline__ void partner_weights(const uint16_t *w, int half_r, int l, f2 (&x)[4]) {
     if (w == nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 1.f;
+        for (int e = 0; e < 4; ++e) x[e] = both(1.f);
     } else if (MODE == kLane) {
         weights<BF16>(w, partner<MODE>(8 * l, half_r) / 8, x);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = load1<BF16>(w + partner<MODE>(8 * l + e, half_r));
+        for (int e = 0; e < 4; ++e)
+            x[e] = f2_pack(load1<BF16>(w + partner<MODE>(8 * l + 2 * e, half_r)),
+                           load1<BF16>(w + partner<MODE>(8 * l + 2 * e + 1, half_r)));
     }
 }
 
 // A row in the ring: this lane's 16 bytes and its elements' partners. `at`: the lane's
 // own place; the row's first lane is at - l.
 template <int D, bool BF16, int MODE>
-__device__ __forceinline__ void read_row(const uint4 *at, int half_r, int l, int partner_l,
-                                         float (&x)[8], float (&xp)[8]) {
+__device__ __forceinline__ void read_row(const uint4 *at, int half_r, int l, int partner_l, f2 (&x)[4],
+                                         f2 (&xp)[4]) {
     unpack8<BF16>(*at, x);
     if constexpr (MODE == kBeside) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
+        for (int e = 0; e < 4; ++e) xp[e] = swapped(x[e]);
     } else if constexpr (MODE == kLane) {
         unpack8<BF16>(at[partner_l - l], xp);
     } else {
         const uint16_t *row = reinterpret_cast<const uint16_t *>(at - l);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) xp[e] = load1<BF16>(row + partner<MODE>(8 * l + e, half_r));
+        for (int e = 0; e < 4; ++e)
+            xp[e] = f2_pack(load1<BF16>(row + partner<MODE>(8 * l + 2 * e, half_r)),
+                            load1<BF16>(row + partner<MODE>(8 * l + 2 * e + 1, half_r)));
     }
-    if (2 * half_r < D) {  // no partner: not even an infinity times 0
+    if (2 * half_r < D) {  // no partner: not even an infinity times 0 (pairs are whole: 2 half_r is even)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (8 * l + e >= 2 * half_r) xp[e] = 0.f;
+        for (int e = 0; e < 4; ++e)
+            if (8 * l + 2 * e >= 2 * half_r) xp[e] = 0;
     }
 }
 
-// Sum over the lanes of a group.
+// Sum over the lanes of a group, of two values at once.
 template <int D>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ f2 group_sum(f2 v) {
 #pragma unroll
-    for (int o = Geometry<D>::kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = Geometry<D>::kLanes / 2; o > 0; o >>= 1) {
+        float a, b;
+        f2_unpack(v, a, b);
+        v = add2(v, f2_pack(__shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o)));
+    }
     return v;
 }
 
-// sum_e a_e b_e in four chains of two.
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-    float s0 = a[0], s1 = a[1], t0 = a[4], t1 = a[5];
-    fmul2(s0, s1, b[0], b[1]);
-    fmul2(t0, t1, b[4], b[5]);
-    float u0 = a[2], u1 = a[3], v0 = a[6], v1 = a[7];
-    ffma2(u0, u1, b[2], b[3], s0, s1);
-    ffma2(v0, v1, b[6], b[7], t0, t1);
-    fadd2(u0, u1, v0, v1);
-    return u0 + u1;
+// sum_e a_e b_e over this lane's 8 elements.
+__device__ __forceinline__ float dot8(const f2 (&a)[4], const f2 (&b)[4]) {
+    const f2 s = add2(fma2(a[2], b[2], mul2(a[0], b[0])), fma2(a[3], b[3], mul2(a[1], b[1])));
+    float x, y;
+    f2_unpack(s, x, y);
+    return x + y;
 }
 
 // Where token m stands: its position, and in an append whether it belongs to a sequence
@@ -275,33 +322,91 @@ __device__ __forceinline__ Place place(const Params &p, int m, int n) {
     return r;
 }
 
-// A walk over stages: stage s of item `item`, whose token is m = (b, n).
-struct Cursor {
-    long long item;
+// An item: token m = (b, n), stages s .. end of it.
+struct Item {
     int m, b, n, s, end;
-    __device__ __forceinline__ void start(const Params &p, long long x) {
-        item = x;
-        m = b = n = s = end = 0;
-        if (x >= p.items) return;
-        m = p.chunks == 1 ? static_cast<int>(x) : static_cast<int>(x / p.chunks);
-        s = static_cast<int>(x - static_cast<long long>(m) * p.chunks) * p.per_item;
-        end = min(s + p.per_item, p.s_q + p.s_k + p.s_v);
-        b = p.N == p.tokens ? 0 : m / p.N;
-        n = m - b * p.N;
+};
+__device__ __forceinline__ Item item_of(const Params &p, long long x) {
+    Item t;
+    t.m = p.chunks == 1 ? static_cast<int>(x) : static_cast<int>(x / p.chunks);
+    t.s = static_cast<int>(x - static_cast<long long>(t.m) * p.chunks) * p.per_item;
+    t.end = min(t.s + p.per_item, p.s_q + p.s_k + p.s_v);
+    t.b = p.N == p.tokens ? 0 : t.m / p.N;
+    t.n = t.m - t.b * p.N;
+    return t;
+}
+
+// The run of an item's stages from stage s on that belong to one tensor (0 queries, 1
+// keys, 2 values): its stages, and the head of its first row (this lane's group adds g).
+struct Run {
+    int kind, stages, head, heads;
+};
+template <int kStageHeads>
+__device__ __forceinline__ Run run_of(const Params &p, int s, int end) {
+    Run r;
+    r.kind = s < p.s_q ? 0 : s < p.s_q + p.s_k ? 1 : 2;
+    const int first = r.kind == 0 ? 0 : r.kind == 1 ? p.s_q : p.s_q + p.s_k;
+    const int count = r.kind == 0 ? p.s_q : r.kind == 1 ? p.s_k : p.s_v;
+    r.stages = min(end, first + count) - s;
+    r.head = (s - first) * kStageHeads;
+    r.heads = r.kind == 0 ? p.H : r.kind == 1 ? p.H_kv : p.H_v;
+    return r;
+}
+
+__device__ __forceinline__ uint16_t *row_at(const Rows &t, const Item &i, int h) {
+    return t.p + i.b * t.batch + i.n * t.token + h * t.head;
+}
+
+// The walk of a warp's copies, ahead of its products: row pointers of up to two tensors
+// that step from stage to stage, set anew only where a run ends.
+template <int kTensors, int kStageHeads>
+struct Ahead {
+    long long item;
+    Item at;
+    int stages;                     // left in this run (0: nothing more to copy)
+    int h, heads;                   // this lane's first head of the stage, and their number
+    const uint16_t *src[kTensors];  // its row
+    long long head[kTensors];       // elements between heads (-1: a tensor that is not there)
+
+    // which(kind, i): the i-th tensor of a run of that kind
+    template <typename Which>
+    __device__ __forceinline__ void run(const Params &p, int g, int l, const Which &which) {
+        const Run r = run_of<kStageHeads>(p, at.s, at.end);
+        stages = r.stages;
+        at.s += r.stages;
+        h = r.head + g;
+        heads = r.heads;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) {
+            const Rows &t = which(r.kind, i);
+            src[i] = row_at(t, at, h) + 8 * l;
+            head[i] = t.p ? t.head : -1;
+        }
     }
-    __device__ __forceinline__ bool more(const Params &p) const { return item < p.items; }
-    __device__ __forceinline__ void next(const Params &p, long long warps) {
-        if (++s == end) start(p, item + warps);
+    template <typename Which>
+    __device__ __forceinline__ void start(const Params &p, long long x, int g, int l, const Which &which) {
+        item = x;
+        stages = 0;
+        if (x < p.items) {
+            at = item_of(p, x);
+            run(p, g, l, which);
+        }
+    }
+    template <typename Which>
+    __device__ __forceinline__ void next(const Params &p, long long warps, int g, int l, const Which &which) {
+        h += kStageHeads;
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i) src[i] += kStageHeads * head[i];
+        if (--stages == 0) {
+            if (at.s < at.end) run(p, g, l, which);
+            else start(p, item + warps, g, l, which);
+        }
     }
 };
 
-__device__ __forceinline__ const uint16_t *row_at(const Rows &t, const Cursor &c) {
-    return t.p + c.b * t.batch + c.n * t.token;
-}
-
 // Forward (PAGED = false) and append (PAGED = true).
 template <int D, bool BF16, int MODE, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 3) fa_norm_rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params p) {
     using G = Geometry<D>;
     constexpr int U = kRows;
     constexpr int kStageHeads = G::kGroups * U;
@@ -310,105 +415,102 @@ __global__ void __launch_bounds__(kThreads, 3) fa_norm_rope_kernel(const Params 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % G::kLanes, g = lane / G::kLanes;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps;
+    const long long x0 = static_cast<long long>(blockIdx.x) * kWarps + warp;
     float(&cs)[2][kMaxPairs] = cs_all[warp];
     const int partner_l = MODE == kLane ? partner<MODE>(8 * l, p.half_r) / 8 : l;
+    auto which = [&](int kind, int) -> const Rows & { return kind == 0 ? p.q : kind == 1 ? p.k : p.v; };
 
-    // rows of a stage: head first + u * groups + g of the stage's tensor
-    auto issue = [&](const Cursor &c, int slot) {
-        if (c.more(p)) {
-            const bool is_q = c.s < p.s_q, is_k = !is_q && (!PAGED || c.s < p.s_q + p.s_k);
-            const Rows &t = is_q ? p.q : is_k ? p.k : p.v;
-            const int heads = is_q ? p.H : is_k ? p.H_kv : p.H_v;
-            const int first = (c.s - (is_q ? 0 : is_k ? p.s_q : p.s_q + p.s_k)) * kStageHeads + g;
-            const uint16_t *src = row_at(t, c) + 8 * l;
+    after_previous();
+    let_next_start();
+    Ahead<1, kStageHeads> in;
+    in.start(p, x0, g, l, which);
+    auto issue = [&](int slot) {
+        if (in.stages > 0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = first + u * G::kGroups;
-                if (h < heads) copy16(&ring[warp][slot][u][lane], src + h * t.head);
-            }
+            for (int u = 0; u < U; ++u)
+                if (in.h + u * G::kGroups < in.heads)
+                    copy16(&ring[warp][slot][u][lane], in.src[0] + u * G::kGroups * in.head[0]);
+            in.next(p, warps, g, l, which);
         }
         copy_commit();
     };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) issue(i);
 
-    Cursor in, at;
-    in.start(p, static_cast<long long>(blockIdx.x) * kWarps + warp);
-    at = in;
-    after_previous();
-    let_next_start();
+    int slot = 0;
+    for (long long x = x0; x < p.items; x += warps) {
+        const Item at = item_of(p, x);
+        const Place where = place<PAGED>(p, at.m, at.n);
+        angles(cs, p, where.pos);
+        for (int s = at.s; s < at.end;) {
+            const Run run = run_of<kStageHeads>(p, s, at.end);
+            s += run.stages;
+            const uint16_t *w = run.kind == 0 ? p.wq : p.wk;
+            f2 A[4], Bc[4];
+            if (!PAGED || run.kind < 2) {
+                f2 wt[4];
+                coefficients<MODE>(cs, p.half_r, l, A, Bc);
+                weights<BF16>(w, l, wt);
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) {
-        issue(in, i);
-        if (in.more(p)) in.next(p, warps);
-    }
-    float A[8], Bc[8];
-    Place where{0, false, -1};
-    long long known = -1;  // the item whose angles are in cs
-    int kind = -1;         // the tensor whose coefficients are in A and Bc
-    int i = 0;
-    for (; at.more(p); at.next(p, warps), ++i) {
-        const bool is_q = at.s < p.s_q, is_k = !is_q && (!PAGED || at.s < p.s_q + p.s_k);
-        if (known != at.item) {
-            known = at.item;
-            kind = -1;
-            where = place<PAGED>(p, at.m, at.n);
-            angles(cs, p, where.pos);
-        }
-        const uint16_t *w = is_q ? p.wq : p.wk;
-        if (kind != (is_q ? 0 : 1) && (is_q || is_k)) {
-            kind = is_q ? 0 : 1;
-            float wt[8];
-            coefficients<MODE>(cs, p.half_r, l, A, Bc);
-            weights<BF16>(w, l, wt);
+                for (int e = 0; e < 4; ++e) A[e] = mul2(A[e], wt[e]);
+                partner_weights<BF16, MODE>(w, p.half_r, l, wt);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) A[e] *= wt[e];
-            partner_weights<BF16, MODE>(w, p.half_r, l, wt);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) Bc[e] *= wt[e];
-        }
-        const int heads = is_q ? p.H : is_k ? p.H_kv : p.H_v;
-        const int first = (at.s - (is_q ? 0 : is_k ? p.s_q : p.s_q + p.s_k)) * kStageHeads + g;
-        uint16_t *dst;
-        long long head_stride;
-        bool store = true;
-        if (PAGED && !is_q) {
-            store = where.slot >= 0;
-            dst = (is_k ? p.kc : p.vc) + (store ? where.slot : 0);
-            head_stride = p.head_stride;
-        } else {
-            if (PAGED) store = where.live;
-            const Rows &t = is_q ? p.q_out : p.k_out;
-            dst = const_cast<uint16_t *>(row_at(t, at));
-            head_stride = t.head;
-        }
-        dst += 8 * l;
-        copy_wait<kDepth - 2>();
-        __syncwarp();  // the stage is there, and the one of the previous round has been read
-        issue(in, (i + kDepth - 1) % kDepth);
-        if (in.more(p)) in.next(p, warps);
-        const uint4(&stage)[U][32] = ring[warp][i % kDepth];
-        uint4 out[U];
-        if (PAGED && !is_q && !is_k) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) out[u] = stage[u][lane];
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float x[8], xp[8], r = 1.f;
-                read_row<D, BF16, MODE>(&stage[u][lane], p.half_r, l, partner_l, x, xp);
-                if (w) r = rsqrtf(group_sum<D>(dot8(x, x)) * (1.f / D) + p.eps);
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    fmul2(xp[e], xp[e + 1], Bc[e], Bc[e + 1]);
-                    ffma2(x[e], x[e + 1], A[e], A[e + 1], xp[e], xp[e + 1]);
-                    fmul2(x[e], x[e + 1], r, r);
-                }
-                out[u] = pack8<BF16>(x);
+                for (int e = 0; e < 4; ++e) Bc[e] = mul2(Bc[e], wt[e]);
             }
-        }
+            int h = run.head + g;
+            // heads of this run that are stored: none where the token has no place
+            int heads = run.heads;
+            long long dst_head;
+            uint16_t *dst;
+            if (PAGED && run.kind > 0) {
+                if (where.slot < 0) heads = 0;
+                dst_head = p.head_stride;
+                dst = (run.kind == 1 ? p.kc : p.vc) + where.slot + h * dst_head + 8 * l;
+            } else {
+                if (PAGED && !where.live) heads = 0;
+                const Rows &t = run.kind == 0 ? p.q_out : p.k_out;
+                dst_head = t.head;
+                dst = row_at(t, at, h) + 8 * l;
+            }
+            for (int j = 0; j < run.stages; ++j) {
+                copy_wait<kDepth - 2>();
+                __syncwarp();  // the stage is there, and the one before has been read
+                issue((slot + kDepth - 1) % kDepth);
+                const uint4(&stage)[U][32] = ring[warp][slot];
+                slot = (slot + 1) % kDepth;
+                uint4 out[U];
+                if (PAGED && run.kind == 2) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = first + u * G::kGroups;
-            if (store && h < heads) *reinterpret_cast<uint4 *>(dst + h * head_stride) = out[u];
+                    for (int u = 0; u < U; ++u) out[u] = stage[u][lane];
+                } else {
+f2 y[U][4], yp[U][4], r = both(1.f);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        read_row<D, BF16, MODE>(&stage[u][lane], p.half_r, l, partner_l, y[u], yp[u]);
+                    if (w) {
+                        static_assert(U == 2, "the rows' sums go through the lanes as one pair");
+                        float s0, s1;
+                        f2_unpack(group_sum<D>(f2_pack(dot8(y[0], y[0]), dot8(y[1], y[1]))), s0, s1);
+                        r = f2_pack(rsqrtf(s0 * (1.f / D) + p.eps), rsqrtf(s1 * (1.f / D) + p.eps));
+                    }
+                    float r0, r1;
+                    f2_unpack(r, r0, r1);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const f2 ru = both(u == 0 ? r0 : r1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[u][e] = mul2(fma2(y[u][e], A[e], mul2(yp[u][e], Bc[e])), ru);
+                        out[u] = pack8<BF16>(y[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h + u * G::kGroups < heads)
+                        *reinterpret_cast<uint4 *>(dst + u * G::kGroups * dst_head) = out[u];
+                h += kStageHeads;
+                dst += kStageHeads * dst_head;
+            }
         }
     }
     copy_wait<0>();
@@ -419,120 +521,114 @@ __global__ void __launch_bounds__(kThreads, 3) fa_norm_rope_kernel(const Params 
 template <int D, bool BF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Params p) {
     using G = Geometry<D>;
+    constexpr int kStageHeads = G::kGroups;
     __shared__ uint4 ring[kWarps][kDepth][2][32];  // gradient and input rows
     __shared__ __align__(16) float cs_all[kWarps][2][kMaxPairs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % G::kLanes, g = lane / G::kLanes;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps;
+    const long long x0 = static_cast<long long>(blockIdx.x) * kWarps + warp;
     float(&cs)[2][kMaxPairs] = cs_all[warp];
     const int partner_l = MODE == kLane ? partner<MODE>(8 * l, p.half_r) / 8 : l;
-    float dwq[8], dwk[8];
+    f2 dwq[4], dwk[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
+    for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = 0;
+    auto which = [&](int kind, int i) -> const Rows & {
+        return i == 0 ? (kind == 0 ? p.q_out : p.k_out) : kind == 0 ? p.q : p.k;
+    };
 
-    auto issue = [&](const Cursor &c, int slot) {
-        if (c.more(p)) {
-            const bool is_q = c.s < p.s_q;
-            const int h = (c.s - (is_q ? 0 : p.s_q)) * G::kGroups + g;
-            if (h < (is_q ? p.H : p.H_kv)) {
-                const Rows &dy = is_q ? p.q_out : p.k_out, &x = is_q ? p.q : p.k;
-                copy16(&ring[warp][slot][0][lane], row_at(dy, c) + h * dy.head + 8 * l);
-                if (is_q ? p.wq != nullptr : p.wk != nullptr)
-                    copy16(&ring[warp][slot][1][lane], row_at(x, c) + h * x.head + 8 * l);
+    after_previous();
+    let_next_start();
+    Ahead<2, kStageHeads> in;
+    in.start(p, x0, g, l, which);
+    auto issue = [&](int slot) {
+        if (in.stages > 0) {
+            if (in.h < in.heads) {
+                copy16(&ring[warp][slot][0][lane], in.src[0]);
+                if (in.head[1] >= 0) copy16(&ring[warp][slot][1][lane], in.src[1]);
             }
+            in.next(p, warps, g, l, which);
         }
         copy_commit();
     };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) issue(i);
 
-    Cursor in, at;
-    in.start(p, static_cast<long long>(blockIdx.x) * kWarps + warp);
-    at = in;
-    after_previous();
-    let_next_start();
+    int slot = 0;
+    for (long long x = x0; x < p.items; x += warps) {
+        const Item at = item_of(p, x);
+        angles(cs, p, place<false>(p, at.m, at.n).pos);
+        f2 C[4], S[4];
+        coefficients<MODE>(cs, p.half_r, l, C, S);
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) {
-        issue(in, i);
-        if (in.more(p)) in.next(p, warps);
-    }
-    float C[8], S[8], wt[8];
-    long long known = -1;
-    int kind = -1, i = 0;
-    for (; at.more(p); at.next(p, warps), ++i) {
-        const bool is_q = at.s < p.s_q;
-        const uint16_t *w = is_q ? p.wq : p.wk;
-        if (known != at.item) {
-            known = at.item;
-            angles(cs, p, place<false>(p, at.m, at.n).pos);
-            coefficients<MODE>(cs, p.half_r, l, C, S);
-        }
-        if (kind != (is_q ? 0 : 1)) {
-            kind = is_q ? 0 : 1;
+        for (int e = 0; e < 4; ++e) S[e] = mul2(S[e], both(-1.f));  // the transposed rotation
+        for (int s = at.s; s < at.end;) {
+            const Run run = run_of<kStageHeads>(p, s, at.end);
+            s += run.stages;
+            const uint16_t *w = run.kind == 0 ? p.wq : p.wk;
+            const Rows &t = run.kind == 0 ? p.dq : p.dk;
+            int h = run.head + g;
+            uint16_t *dst = row_at(t, at, h) + 8 * l;
+            f2 wt[4], dw[4];
             weights<BF16>(w, l, wt);
-        }
-        const int h = (at.s - (is_q ? 0 : p.s_q)) * G::kGroups + g;
-        const bool there = h < (is_q ? p.H : p.H_kv);
-        const Rows &dx = is_q ? p.dq : p.dk;
-        copy_wait<kDepth - 2>();
-        __syncwarp();  // the stage is there, and the one of the previous round has been read
-        issue(in, (i + kDepth - 1) % kDepth);
-        if (in.more(p)) in.next(p, warps);
-        const uint4(&stage)[2][32] = ring[warp][i % kDepth];
-        float o[8], yp[8];
-        read_row<D, BF16, MODE>(&stage[0][lane], p.half_r, l, partner_l, o, yp);
-        // the transposed rotation: the sine's sign is the other one
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            fmul2(yp[e], yp[e + 1], -S[e], -S[e + 1]);
-            ffma2(o[e], o[e + 1], C[e], C[e + 1], yp[e], yp[e + 1]);
-        }
-        if (w) {
-            float x[8], uw[8];
-            unpack8<BF16>(stage[1][lane], x);
+            for (int e = 0; e < 4; ++e) dw[e] = 0;
+            for (int j = 0; j < run.stages; ++j) {
+                copy_wait<kDepth - 2>();
+                __syncwarp();
+                issue((slot + kDepth - 1) % kDepth);
+                const uint4(&stage)[2][32] = ring[warp][slot];
+                slot = (slot + 1) % kDepth;
+                const bool there = h < run.heads;
+                f2 o[4], yp[4];
+                read_row<D, BF16, MODE>(&stage[0][lane], p.half_r, l, partner_l, o, yp);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                uw[e] = o[e], uw[e + 1] = o[e + 1];
-                fmul2(uw[e], uw[e + 1], wt[e], wt[e + 1]);
-            }
-            const float r = rsqrtf(group_sum<D>(dot8(x, x)) * (1.f / D) + p.eps);
-            const float k = -group_sum<D>(dot8(uw, x)) * (1.f / D) * r * r * r;
-            auto add = [&](float(&dw)[8]) {
+                for (int e = 0; e < 4; ++e) o[e] = fma2(o[e], C[e], mul2(yp[e], S[e]));
+                if (w) {
+                    f2 x8[4], uw[4];
+                    unpack8<BF16>(stage[1][lane], x8);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    float z0 = x[e], z1 = x[e + 1];
-                    fmul2(z0, z1, r, r);
-                    ffma2(z0, z1, o[e], o[e + 1], dw[e], dw[e + 1]);
-                    dw[e] = z0, dw[e + 1] = z1;
+                    for (int e = 0; e < 4; ++e) uw[e] = mul2(o[e], wt[e]);
+                    float xx, ux;
+                    f2_unpack(group_sum<D>(f2_pack(dot8(x8, x8), dot8(uw, x8))), xx, ux);
+                    const float r = rsqrtf(xx * (1.f / D) + p.eps);
+                    const f2 rr = both(r), k = both(-ux * (1.f / D) * r * r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f2 z = mul2(x8[e], rr);
+                        if (there) dw[e] = fma2(o[e], z, dw[e]);  // a row that is not there adds nothing
+                        o[e] = fma2(z, k, mul2(uw[e], rr));
+                    }
                 }
-            };
-            if (there) {  // a row that is not there adds nothing
-                if (is_q) add(dwq);
-                else add(dwk);
+                if (there) *reinterpret_cast<uint4 *>(dst) = pack8<BF16>(o);
+                h += kStageHeads;
+                dst += kStageHeads * t.head;
             }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                fmul2(uw[e], uw[e + 1], r, r);
-                ffma2(x[e], x[e + 1], k, k, uw[e], uw[e + 1]);
-                o[e] = x[e], o[e + 1] = x[e + 1];
+            for (int e = 0; e < 4; ++e) {
+                if (run.kind == 0) dwq[e] = add2(dwq[e], dw[e]);
+                else dwk[e] = add2(dwk[e], dw[e]);
             }
         }
-        if (there)
-            *reinterpret_cast<uint4 *>(const_cast<uint16_t *>(row_at(dx, at)) + h * dx.head + 8 * l) =
-                pack8<BF16>(o);
     }
     copy_wait<0>();
     if (p.part == nullptr) return;
     // the groups' sums, column by column, in one order
     float *red = reinterpret_cast<float *>(&ring[0][0][0][0]);
     constexpr int kAll = kWarps * G::kGroups;
-    auto reduce = [&](const float (&dw)[8], int which) {
+    auto reduce = [&](const f2 (&dw)[4], int which_w) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[threadIdx.x * 8 + e] = dw[e];
+        for (int e = 0; e < 4; ++e) {
+            float a, b;
+            f2_unpack(dw[e], a, b);
+            *reinterpret_cast<float2 *>(&red[threadIdx.x * 8 + 2 * e]) = make_float2(a, b);
+        }
         __syncthreads();
         if (threadIdx.x < D) {
             float s = 0.f;
             for (int r = 0; r < kAll; ++r) s += red[r * D + threadIdx.x];
-            p.part[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = s;
+            p.part[(static_cast<size_t>(blockIdx.x) * 2 + which_w) * D + threadIdx.x] = s;
         }
     };
     reduce(dwq, 0);
