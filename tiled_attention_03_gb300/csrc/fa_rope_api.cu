@@ -163,25 +163,17 @@ int mode_of(const fa_norm_rope &r) {
     return r.rotary_dim % 16 == 0 ? fa::rope::kLane : fa::rope::kAnywhere;
 }
 
-// Stages of a token and items (see the kernels): a whole token per warp, which computes its
-// angles once, or parts of it when the tokens alone would leave warps of the launch idle.
-void set_items(Params &p, int64_t d, int rows, int most_blocks) {
-    const int heads = static_cast<int>(256 / d) * rows;  // of a stage
+// The stages of a token, `rows` rows per group each, and the blocks of a launch: as many as
+// stay resident, or fewer when there is less than a stage for each of their warps.
+unsigned set_stages(Params &p, int64_t d, int rows, int most_blocks) {
+    const int heads = static_cast<int>(256 / d) * rows;
     auto stages = [heads](int h) { return (h + heads - 1) / heads; };
     p.s_q = stages(p.H);
     p.s_k = stages(p.H_kv);
     p.s_v = stages(p.H_v);
-    const int all = p.s_q + p.s_k + p.s_v;
-    const int64_t warps = static_cast<int64_t>(most_blocks) * fa::rope::kWarps;
-    int64_t chunks = warps / p.tokens;
-    chunks = chunks < 1 ? 1 : chunks > all ? all : chunks;
-    p.per_item = static_cast<int>((all + chunks - 1) / chunks);
-    p.chunks = (all + p.per_item - 1) / p.per_item;
-    p.items = static_cast<int64_t>(p.tokens) * p.chunks;
-}
-unsigned blocks_of(const Params &p, int most_blocks) {
-    const int64_t b = (p.items + fa::rope::kWarps - 1) / fa::rope::kWarps;
-    return static_cast<unsigned>(b < most_blocks ? b : most_blocks);
+    p.stages = static_cast<long long>(p.tokens) * (p.s_q + p.s_k + p.s_v);
+    const long long blocks = (p.stages + fa::rope::kWarps - 1) / fa::rope::kWarps;
+    return static_cast<unsigned>(blocks < most_blocks ? blocks : most_blocks);
 }
 
 template <int D, bool BF16, bool PAGED>
@@ -304,9 +296,8 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
     p.tokens = static_cast<int>(B * N);
     p.positions = positions;
     set_rope(p, *rope);
-    const int most = di.sm_count * kBlocksPerSm;
-    set_items(p, d, fa::rope::kRows, most);
-    if (forward<false>(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks_of(p, most),
+    const unsigned blocks = set_stages(p, d, fa::rope::kRows, di.sm_count * kBlocksPerSm);
+    if (forward<false>(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks,
                        static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
     fa_host::count_launches(1);
@@ -391,9 +382,7 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
     if (!wq) p.wq = nullptr;
     if (!wk) p.wk = nullptr;
     p.part = wq || wk ? static_cast<float *>(workspace) : nullptr;
-    const int most = di.sm_count * kBackwardBlocksPerSm;
-    set_items(p, d, 1, most);
-    const unsigned blocks = blocks_of(p, most);
+    const unsigned blocks = set_stages(p, d, 1, di.sm_count * kBackwardBlocksPerSm);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (backward(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks, st) != cudaSuccess) return FA_ERR_CUDA;
     fa_host::count_launches(1);
@@ -488,9 +477,8 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     p.max_pages = static_cast<int>(max_pages);
     while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
     p.num_pages = static_cast<int>(cache->num_pages);
-    const int most = di.sm_count * kBlocksPerSm;
-    set_items(p, d, fa::rope::kRows, most);
-    if (forward<true>(p, d, cache->dtype == FA_DTYPE_BF16, mode_of(r), blocks_of(p, most),
+    const unsigned blocks = set_stages(p, d, fa::rope::kRows, di.sm_count * kBlocksPerSm);
+    if (forward<true>(p, d, cache->dtype == FA_DTYPE_BF16, mode_of(r), blocks,
                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
     fa_host::count_launches(1);

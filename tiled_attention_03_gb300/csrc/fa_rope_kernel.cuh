@@ -12,11 +12,12 @@
 // around 2^64 is the exact reduction by whole turns, and the upper bits, as a signed
 // number of half turns in [-1, 1), go through sincospif.
 //
-// A warp works alone: an item is one token (or a part of its heads, when there are few
-// tokens), whose cosines and sines its lanes compute once; the rows stream through a ring
-// of asynchronous 16-byte copies into shared memory, kDepth - 1 stages ahead and across
-// items, so that the bytes in flight do not cost registers and no block barrier stops
-// them. Partners in another lane (half layout) are read from the ring as well.
+// A warp works alone on an equal share of the line of all tokens' stages (a stage is a few
+// heads of one tensor of one token). Its lanes compute a token's cosines and sines once;
+// the rows stream through a ring of asynchronous 16-byte copies into shared memory, kDepth -
+// 1 stages ahead and across tokens, so that the bytes in flight do not cost registers
+// and no block barrier stops them. Partners in another lane (half layout) are read from
+// the ring as well.
 //
 // Bound by memory: 4 bytes per element forward, 6 backward.
 #pragma once
@@ -54,10 +55,9 @@ struct Params {
     int half_r;                    // rotated pairs
     float magnitude, eps;
     const uint16_t *wq, *wk;       // null: not normalised
-    // a token's stages: s_q of queries, then s_k of keys, then s_v of values; an item is
-    // `per_item` of them, `chunks` items a token
-    int s_q, s_k, s_v, per_item, chunks;
-    long long items;
+    // a token's stages: s_q of queries, then s_k of keys, then s_v of values; all tokens'
+    int s_q, s_k, s_v;
+    long long stages;
     // paged
     uint16_t *kc, *vc;
     long long page_stride, token_stride, head_stride;
@@ -322,19 +322,33 @@ __device__ __forceinline__ Place place(const Params &p, int m, int n) {
     return r;
 }
 
-// An item: token m = (b, n), stages s .. end of it.
+// A warp's part of a token: token m = (b, n), its stages s .. end - 1, with `left` stages
+// of the warp's share from s on. m >= 0 while there is one.
 struct Item {
     int m, b, n, s, end;
+    long long left;
+    __device__ __forceinline__ void place_token(const Params &p) {
+        end = static_cast<int>(min(static_cast<long long>(p.s_q + p.s_k + p.s_v), s + left));
+        b = p.N == p.tokens ? 0 : m / p.N;
+        n = m - b * p.N;
+    }
+    // this warp's share: the w-th of `warps` equal ones
+    __device__ __forceinline__ void first(const Params &p, long long w, long long warps) {
+        const long long x = p.stages * w / warps;
+        left = p.stages * (w + 1) / warps - x;
+        const int per = p.s_q + p.s_k + p.s_v;
+        m = static_cast<int>(x / per);
+        s = static_cast<int>(x - static_cast<long long>(m) * per);
+        if (left > 0) place_token(p);
+    }
+    // the next token (its stages from 0 on)
+    __device__ __forceinline__ void next(const Params &p, int done) {
+        left -= done;
+        ++m;
+        s = 0;
+        if (left > 0) place_token(p);
+    }
 };
-__device__ __forceinline__ Item item_of(const Params &p, long long x) {
-    Item t;
-    t.m = p.chunks == 1 ? static_cast<int>(x) : static_cast<int>(x / p.chunks);
-    t.s = static_cast<int>(x - static_cast<long long>(t.m) * p.chunks) * p.per_item;
-    t.end = min(t.s + p.per_item, p.s_q + p.s_k + p.s_v);
-    t.b = p.N == p.tokens ? 0 : t.m / p.N;
-    t.n = t.m - t.b * p.N;
-    return t;
-}
 
 // The run of an item's stages from stage s on that belong to one tensor (0 queries, 1
 // keys, 2 values): its stages, and the head of its first row (this lane's group adds g).
@@ -361,8 +375,8 @@ __device__ __forceinline__ uint16_t *row_at(const Rows &t, const Item &i, int h)
 // that step from stage to stage, set anew only where a run ends.
 template <int kTensors, int kStageHeads>
 struct Ahead {
-    long long item;
     Item at;
+    int done;                       // stages of this token taken into runs
     int stages;                     // left in this run (0: nothing more to copy)
     int h, heads;                   // this lane's first head of the stage, and their number
     const uint16_t *src[kTensors];  // its row
@@ -373,6 +387,7 @@ struct Ahead {
     __device__ __forceinline__ void run(const Params &p, int g, int l, const Which &which) {
         const Run r = run_of<kStageHeads>(p, at.s, at.end);
         stages = r.stages;
+        done += r.stages;
         at.s += r.stages;
         h = r.head + g;
         heads = r.heads;
@@ -384,22 +399,22 @@ struct Ahead {
         }
     }
     template <typename Which>
-    __device__ __forceinline__ void start(const Params &p, long long x, int g, int l, const Which &which) {
-        item = x;
-        stages = 0;
-        if (x < p.items) {
-            at = item_of(p, x);
-            run(p, g, l, which);
-        }
+    __device__ __forceinline__ void start(const Params &p, int g, int l, const Which &which) {
+        stages = done = 0;
+        if (at.left > 0) run(p, g, l, which);
     }
     template <typename Which>
-    __device__ __forceinline__ void next(const Params &p, long long warps, int g, int l, const Which &which) {
+    __device__ __forceinline__ void next(const Params &p, int g, int l, const Which &which) {
         h += kStageHeads;
 #pragma unroll
         for (int i = 0; i < kTensors; ++i) src[i] += kStageHeads * head[i];
         if (--stages == 0) {
-            if (at.s < at.end) run(p, g, l, which);
-            else start(p, item + warps, g, l, which);
+            if (at.s < at.end) {
+                run(p, g, l, which);
+            } else {
+                at.next(p, done);
+                start(p, g, l, which);
+            }
         }
     }
 };
@@ -415,22 +430,25 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % G::kLanes, g = lane / G::kLanes;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps;
-    const long long x0 = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const long long share = static_cast<long long>(blockIdx.x) * kWarps + warp;
     float(&cs)[2][kMaxPairs] = cs_all[warp];
     const int partner_l = MODE == kLane ? partner<MODE>(8 * l, p.half_r) / 8 : l;
     auto which = [&](int kind, int) -> const Rows & { return kind == 0 ? p.q : kind == 1 ? p.k : p.v; };
 
     after_previous();
     let_next_start();
+    Item at;
+    at.first(p, share, warps);
     Ahead<1, kStageHeads> in;
-    in.start(p, x0, g, l, which);
+    in.at = at;
+    in.start(p, g, l, which);
     auto issue = [&](int slot) {
         if (in.stages > 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (in.h + u * G::kGroups < in.heads)
                     copy16(&ring[warp][slot][u][lane], in.src[0] + u * G::kGroups * in.head[0]);
-            in.next(p, warps, g, l, which);
+            in.next(p, g, l, which);
         }
         copy_commit();
     };
@@ -438,8 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
     for (int i = 0; i < kDepth - 1; ++i) issue(i);
 
     int slot = 0;
-    for (long long x = x0; x < p.items; x += warps) {
-        const Item at = item_of(p, x);
+    for (; at.left > 0; at.next(p, at.end - at.s)) {
         const Place where = place<PAGED>(p, at.m, at.n);
         angles(cs, p, where.pos);
         for (int s = at.s; s < at.end;) {
@@ -527,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % G::kLanes, g = lane / G::kLanes;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps;
-    const long long x0 = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const long long share = static_cast<long long>(blockIdx.x) * kWarps + warp;
     float(&cs)[2][kMaxPairs] = cs_all[warp];
     const int partner_l = MODE == kLane ? partner<MODE>(8 * l, p.half_r) / 8 : l;
     f2 dwq[4], dwk[4];
@@ -539,15 +556,18 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
 
     after_previous();
     let_next_start();
+    Item at;
+    at.first(p, share, warps);
     Ahead<2, kStageHeads> in;
-    in.start(p, x0, g, l, which);
+    in.at = at;
+    in.start(p, g, l, which);
     auto issue = [&](int slot) {
         if (in.stages > 0) {
             if (in.h < in.heads) {
                 copy16(&ring[warp][slot][0][lane], in.src[0]);
                 if (in.head[1] >= 0) copy16(&ring[warp][slot][1][lane], in.src[1]);
             }
-            in.next(p, warps, g, l, which);
+            in.next(p, g, l, which);
         }
         copy_commit();
     };
@@ -555,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
     for (int i = 0; i < kDepth - 1; ++i) issue(i);
 
     int slot = 0;
-    for (long long x = x0; x < p.items; x += warps) {
-        const Item at = item_of(p, x);
+    for (; at.left > 0; at.next(p, at.end - at.s)) {
         angles(cs, p, place<false>(p, at.m, at.n).pos);
         f2 C[4], S[4];
         coefficients<MODE>(cs, p.half_r, l, C, S);
