@@ -35,7 +35,11 @@ struct Small {
     static constexpr int kChunks = D / 8;            // 16-byte chunks per row
     static constexpr int kCopyRows = 32 / kChunks;   // rows per copy instruction of a warp
     static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
-    static constexpr int kScan = kRing;              // 256 prefixes, 256 works, warp sums
+    // Q as A operands stays in registers, except at d = 256, where it would take 64 next
+    // to the outputs' 128: there each warp keeps its rows in shared memory
+    static constexpr bool kQShared = D == 256;
+    static constexpr int kQBytes = kQShared ? kSmallRows * kRowBytes : 0;
+    static constexpr int kScan = kRing + kWarps * kQBytes;  // 256 prefixes, 256 works, warp sums
     static constexpr int kBytes = kScan + 2 * 256 * 4 + 64;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -50,6 +54,9 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return static_cast<uint32_t>(row * Small<D>::kRowBytes + ((chunk ^ x) << 4));
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
                  : "memory");
@@ -118,9 +125,13 @@ __device__ __forceinline__ Seq small_seq(int b, const SmallParams &p) {
     s.nk = min(max(p.seq_k[b], 0), p.max_keys);
     return s;
 }
+// Units of a sequence per head group (mostly one: the division is worth avoiding).
+__device__ __forceinline__ int small_units(const Seq &s, const SmallParams &p) {
+    return s.nq <= p.tpt ? min(s.nq, 1) : (s.nq + p.tpt - 1) / p.tpt;
+}
 template <int kKeys>
 __device__ __forceinline__ unsigned small_work(const Seq &s, const SmallParams &p) {
-    const int nqb = (s.nq + p.tpt - 1) / p.tpt;
+    const int nqb = small_units(s, p);
     unsigned w = 0;
     for (int qb = 0; qb < nqb; ++qb) {
         int lo, hi, j0;
@@ -145,58 +156,117 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
     after_previous();
     let_next_start();
 
-    // ---- this warp's share: ticks w0 .. w1 - 1 of W
-    unsigned mine = 0, first = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThr) {
-        const unsigned w = small_work<kKeys>(small_seq(b, p), p) * p.spaces;
-        if (b < kThr) first = w;
-        mine += w;
-    }
-    mine = warp_sum(mine);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    unsigned W = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) W += sums[i];
-    const unsigned T = max((W + workers - 1) / workers, static_cast<unsigned>(p.min_ticks));
-    const unsigned w0 = min(worker * T, W), w1 = min(w0 + T, W);
+    // ---- this warp's share: ticks w0 .. w1 - 1 of W, and the sequence b that holds w0, `off`
+    // ticks into it. Up to 128 sequences every warp finds its own, one to four to a lane,
+    // without a barrier; more are summed and searched by the block.
+    unsigned W, T, w0, w1, off = 0, per = 0;  // per: ticks of one head group of sequence b
     int b = -1;
-    unsigned off = 0, carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThr) {
-        const int x = b0 + static_cast<int>(threadIdx.x);
-        const unsigned w = b0 == 0 ? first : x < p.B ? small_work<kKeys>(small_seq(x, p), p) * p.spaces : 0;
-        unsigned incl = w;
+    Seq s{0, 0, 0};
+    constexpr int kOwn = 4;
+    if (p.B <= 32 * kOwn) {
+        const int own = (p.B + 31) >> 5;
+        Seq q[kOwn];
+        unsigned w[kOwn], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            q[i] = Seq{0, 0, 0};
+            if (i < own && own * lane + i < p.B) q[i] = small_seq(own * lane + i, p);
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            w[i] = 0;
+            if (i < own) w[i] = small_work<kKeys>(q[i], p);
+            sum += w[i] * p.spaces;
+        }
+        unsigned incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        __syncthreads();
-        if (lane == 31) sums[warp] = incl;
-        __syncthreads();
-        unsigned before = carry;
+        W = __shfl_sync(0xffffffffu, incl, 31);
+        T = max((W + workers - 1) / workers, static_cast<unsigned>(p.min_ticks));
+        w0 = min(worker * T, W);
+        w1 = min(w0 + T, W);
+        unsigned lo = incl - sum;
+        const unsigned hit = __ballot_sync(0xffffffffu, lo <= w0 && w0 < incl);
+        if (w0 < w1) {
+            // in the lane that holds w0: which of its sequences
+            int at = 0;
+            Seq mine = q[0];
+            per = w[0];
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += sums[i];
-            carry += sums[i];
+            for (int i = 0; i < kOwn - 1; ++i)
+                if (at == i && i + 1 < own && w0 >= lo + w[i] * p.spaces) {
+                    lo += w[i] * p.spaces;
+                    at = i + 1;
+                    mine = q[i + 1];
+                    per = w[i + 1];
+                }
+            const int src = __ffs(hit) - 1;
+            b = own * src + __shfl_sync(0xffffffffu, at, src);
+            off = w0 - __shfl_sync(0xffffffffu, lo, src);
+            per = __shfl_sync(0xffffffffu, per, src);
+            s.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+            s.nq = __shfl_sync(0xffffffffu, mine.nq, src);
+            s.nk = __shfl_sync(0xffffffffu, mine.nk, src);
         }
-        pre[threadIdx.x] = before + incl - w;
-        wrk[threadIdx.x] = w;
+    } else {
+        unsigned mine = 0, first = 0, carry = 0;
+        for (int x = threadIdx.x; x < p.B; x += kThr) {
+            const unsigned w = small_work<kKeys>(small_seq(x, p), p) * p.spaces;
+            if (x < kThr) first = w;
+            mine += w;
+        }
+        mine = warp_sum(mine);
+        if (lane == 0) sums[warp] = mine;
         __syncthreads();
-        if (b < 0 && w0 < w1) {
+        W = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) W += sums[i];
+        T = max((W + workers - 1) / workers, static_cast<unsigned>(p.min_ticks));
+        w0 = min(worker * T, W);
+        w1 = min(w0 + T, W);
+        for (int b0 = 0; b0 < p.B; b0 += kThr) {
+            const int x = b0 + static_cast<int>(threadIdx.x);
+            const unsigned w = b0 == 0 ? first : x < p.B ? small_work<kKeys>(small_seq(x, p), p) * p.spaces : 0;
+            unsigned incl = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            __syncthreads();
+            if (lane == 31) sums[warp] = incl;
+            __syncthreads();
+            unsigned before = carry;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
-                const unsigned lo = pre[32 * i + lane];
-                const unsigned hit = __ballot_sync(0xffffffffu, lo <= w0 && w0 < lo + wrk[32 * i + lane]);
-                if (hit != 0) {
-                    const int at = 32 * i + __ffs(hit) - 1;
-                    b = b0 + at;
-                    off = w0 - pre[at];
+                if (i < warp) before += sums[i];
+                carry += sums[i];
+            }
+            pre[threadIdx.x] = before + incl - w;
+            wrk[threadIdx.x] = w;
+            __syncthreads();
+            if (b < 0 && w0 < w1) {
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) {
+                    const unsigned lo = pre[32 * i + lane];
+                    const unsigned hit = __ballot_sync(0xffffffffu, lo <= w0 && w0 < lo + wrk[32 * i + lane]);
+                    if (hit != 0) {
+                        const int at = 32 * i + __ffs(hit) - 1;
+                        b = b0 + at;
+                        off = w0 - pre[at];
+                    }
                 }
             }
+            // the block's largest share start is its last warp's
+            if (((kWarps - 1) * gridDim.x + blockIdx.x) * static_cast<unsigned long long>(T) < carry) break;
         }
-        // the block's largest share start is its last warp's
-        if (((kWarps - 1) * gridDim.x + blockIdx.x) * static_cast<unsigned long long>(T) < carry) break;
+        if (b >= 0) {
+            s = small_seq(b, p);
+            per = small_work<kKeys>(s, p);
+        }
     }
     MergeInfo info{};
     info.last_cta = -1;
@@ -205,13 +275,11 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
         return;
     }
 
-    Seq s = small_seq(b, p);
-    int nqb = (s.nq + p.tpt - 1) / p.tpt, qb = 0, sp;
+    int nqb = small_units(s, p), qb = 0, sp;
     int skip;  // ticks of the current unit before this share
     {
-        const int per = static_cast<int>(small_work<kKeys>(s, p));
-        sp = static_cast<int>(off) / per;
-        skip = static_cast<int>(off) - sp * per;
+        sp = static_cast<int>(off / per);
+        skip = static_cast<int>(off - sp * per);
         for (; qb < nqb - 1; ++qb) {
             int lo, hi, j0;
             const int n = small_unit<kKeys>(s, qb, p, lo, hi, j0) + kUnitTicks;
@@ -223,6 +291,7 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
     const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // this lane's rows r0, r0 + 8; first column
     const long long copy_off =
         static_cast<long long>(lane / L::kChunks) * p.token_stride + (lane % L::kChunks) * 8;
+    const long long copy_step = L::kCopyRows * p.token_stride;
     int pieces = 0;
     for (unsigned w = w0; w < w1;) {
         int lo, hi, j0;
@@ -266,26 +335,42 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
                         const bool known = page >= 0 && page < p.num_pages;
                         const long long at = (known ? page : 0) * p.page_stride +
                                              (key0 & ((1 << p.page_log2) - 1)) * p.token_stride + head_off;
+                        const uint16_t *pk = p.k + at, *pv = p.v + at;
+                        const bool all = known && key0 >= lo && key0 + 7 <= hi;
 #pragma unroll
                         for (int i = 0; i < 8 / L::kCopyRows; ++i) {
                             const int row = i * L::kCopyRows + lane / L::kChunks;
-                            const int key = key0 + row;
-                            const bool there = known && key >= lo && key <= hi;
-                            const long long o = there ? at + i * L::kCopyRows * p.token_stride : 0;
                             const uint32_t d = tile_at<D>(8 * g + row, lane % L::kChunks);
-                            copy16_or_zero(dk + d, p.k + o, there);
-                            copy16_or_zero(dv + d, p.v + o, there);
+                            if (all) {
+                                copy16(dk + d, pk);
+                                copy16(dv + d, pv);
+                            } else {
+                                const int key = key0 + row;
+                                const bool there = known && key >= lo && key <= hi;
+                                copy16_or_zero(dk + d, there ? pk : p.k, there);
+                                copy16_or_zero(dv + d, there ? pv : p.v, there);
+                            }
+                            pk += copy_step;
+                            pv += copy_step;
                         }
                     }
                 }
                 copies_commit();
             };
             __syncwarp();  // every lane is done with the ring of the piece before
+            const uint32_t q_tile = smem_u32(small_smem) + L::kRing + warp * L::kQBytes;
+            if constexpr (L::kQShared) {
 #pragma unroll
-            for (int i = 0; i < L::kStages - 1; ++i) issue(ja + i, i);
-            // Q as the A operand of every k-step: rows r0 and r0 + 8, columns c0 and c0 + 8
-            uint32_t qa[D / 16][4];
-            {
+                for (int i = 0; i < kSmallRows / L::kCopyRows; ++i) {
+                    const int r = i * L::kCopyRows + lane / L::kChunks;
+                    copy16_or_zero(q_tile + tile_at<D>(r, lane % L::kChunks),
+                                   p.Q + out_row(r < rows ? r : 0) * D + (lane % L::kChunks) * 8, r < rows);
+                }
+            }
+            // Q as the A operand of every k-step: rows r0 and r0 + 8, columns c0 and c0 + 8 (on
+            // its way while the first copies look up their pages)
+            uint32_t qa[L::kQShared ? 1 : D / 16][4];
+            if constexpr (!L::kQShared) {
                 const uint32_t *q0 =
                     reinterpret_cast<const uint32_t *>(p.Q + out_row(r0 < rows ? r0 : 0) * D + c0);
                 const uint32_t *q1 =
@@ -298,6 +383,8 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
                     qa[k][3] = r0 + 8 < rows ? q1[8 * k + 4] : 0;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < L::kStages - 1; ++i) issue(ja + i, i);
             float o[D / 8][4];
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
@@ -315,20 +402,31 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
                 const uint32_t sk = ring + slot * 2 * L::kTileBytes, sv = sk + L::kTileBytes;
                 slot = slot + 1 == L::kStages ? 0 : slot + 1;
                 const int kv0 = (j0 + j) * kKeys;
-                float x[kKeys / 8][4];
+                // scores in two chains of products, of the even and of the odd steps: one chain
+                // of d / 16 dependent products is most of a lone warp's time
+                float x[kKeys / 8][4], y[kKeys / 8][4];
 #pragma unroll
-                for (int c = 0; c < kKeys / 8; ++c) x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.f;
+                for (int c = 0; c < kKeys / 8; ++c)
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
+                    for (int e = 0; e < 4; ++e) x[c][e] = y[c][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t(&a)[4] = qa[L::kQShared ? 0 : k];
+                    if constexpr (L::kQShared) ldmatrix4(q_tile + tile_at<D>(lane & 15, 2 * k + (lane >> 4)), a);
 #pragma unroll
                     for (int c = 0; c < kKeys / 16; ++c) {
                         uint32_t kb[4];
                         ldmatrix4(sk + tile_at<D>(16 * c + (lane & 7) + ((lane >> 4) << 3),
                                                   2 * k + ((lane >> 3) & 1)),
                                   kb);
-                        mma16816<BF16>(x[2 * c], qa[k], kb[0], kb[1]);
-                        mma16816<BF16>(x[2 * c + 1], qa[k], kb[2], kb[3]);
+                        mma16816<BF16>(k & 1 ? y[2 * c] : x[2 * c], a, kb[0], kb[1]);
+                        mma16816<BF16>(k & 1 ? y[2 * c + 1] : x[2 * c + 1], a, kb[2], kb[3]);
                     }
+                }
+#pragma unroll
+                for (int c = 0; c < kKeys / 8; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[c][e] += y[c][e];
                 if (kv0 < lo_last || kv0 + kKeys - 1 > hi_first) {
 #pragma unroll
                     for (int c = 0; c < kKeys / 8; ++c)
@@ -444,7 +542,7 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
                 sp = 0;
                 while (w < w1 && ++b < p.B) {
                     s = small_seq(b, p);
-                    nqb = (s.nq + p.tpt - 1) / p.tpt;
+                    nqb = small_units(s, p);
                     if (nqb > 0) break;
                 }
                 if (b >= p.B) break;

@@ -953,9 +953,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 16; ++e)
                             pk[e] = pack2<BF16>(__uint_as_float(o[2 * e]) * inv_l,
                                                 __uint_as_float(o[2 * e + 1]) * inv_l);
-                        if (l == 0.f)
+                        if (l == 0.f) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0;
+                        }
                         if (active) {
                             st_global_v8(orow + c * 64, pk);
                             st_global_v8(orow + c * 64 + 32, pk + 8);
