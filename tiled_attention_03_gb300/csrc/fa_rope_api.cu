@@ -163,17 +163,26 @@ int mode_of(const fa_norm_rope &r) {
     return r.rotary_dim % 16 == 0 ? fa::rope::kLane : fa::rope::kAnywhere;
 }
 
-// The stages of a token, `rows` rows per group each, and the blocks of a launch: as many as
-// stay resident, or fewer when there is less than a stage for each of their warps.
-unsigned set_stages(Params &p, int64_t d, int rows, int most_blocks) {
+// The stages of a token, `rows` rows per group each, and the blocks of a launch. Up to
+// `resident` blocks (what the SMs hold at once) every warp takes a stage at least; more,
+// up to `most`, only where their warps still have kLongShare stages each: blocks that
+// start as others end even out what the SMs get (forward, B4 N4096 H32+32 d128: 97 us with
+// resident blocks alone, 88 us with shares of 28 stages, 91 us with 14), but a short share is
+// mostly its start (24 prompts appended at d 64: 25.6 us with shares of 28, 29.5 us with 14).
+// The backward keeps to resident blocks: its longer start and end and the sums of more
+// blocks cost more than they even out (92 us, 97 to 104 us with more).
+constexpr int kLongShare = 28;
+unsigned set_stages(Params &p, int64_t d, int rows, long long resident, long long most) {
     const int heads = static_cast<int>(256 / d) * rows;
     auto stages = [heads](int h) { return (h + heads - 1) / heads; };
     p.s_q = stages(p.H);
     p.s_k = stages(p.H_kv);
     p.s_v = stages(p.H_v);
     p.stages = static_cast<long long>(p.tokens) * (p.s_q + p.s_k + p.s_v);
-    const long long blocks = (p.stages + fa::rope::kWarps - 1) / fa::rope::kWarps;
-    return static_cast<unsigned>(blocks < most_blocks ? blocks : most_blocks);
+    const long long each = (p.stages + fa::rope::kWarps - 1) / fa::rope::kWarps;
+    const long long longer = p.stages / (fa::rope::kWarps * kLongShare);
+    const long long blocks = longer > resident ? longer : each < resident ? each : resident;
+    return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
 template <int D, bool BF16, bool PAGED>
@@ -210,9 +219,10 @@ cudaError_t backward(const Params &p, int64_t d, bool bf16, int mode, unsigned g
     }
 }
 
-// Resident blocks per SM (the kernels' launch bounds): the blocks of a launch at most.
+// Resident blocks per SM (the kernels' launch bounds).
 constexpr int kBlocksPerSm = 2;
-constexpr int kBackwardBlocksPerSm = 2;  // each leaves 2 d partial sums
+// Blocks of a backward launch at most: each leaves 2 d partial sums.
+constexpr int kBackwardBlocksPerSm = 2;
 
 int sm_count_or_default() {
     int dev = 0, sms = 152;
@@ -296,7 +306,8 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
     p.tokens = static_cast<int>(B * N);
     p.positions = positions;
     set_rope(p, *rope);
-    const unsigned blocks = set_stages(p, d, fa::rope::kRows, di.sm_count * kBlocksPerSm);
+    const unsigned blocks = set_stages(p, d, fa::rope::kRows, di.sm_count * kBlocksPerSm,
+                                       int64_t{1} << 30);
     if (forward<false>(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks,
                        static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
@@ -382,7 +393,7 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
     if (!wq) p.wq = nullptr;
     if (!wk) p.wk = nullptr;
     p.part = wq || wk ? static_cast<float *>(workspace) : nullptr;
-    const unsigned blocks = set_stages(p, d, 1, di.sm_count * kBackwardBlocksPerSm);
+    const unsigned blocks = set_stages(p, d, 1, di.sm_count * kBlocksPerSm, di.sm_count * kBackwardBlocksPerSm);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (backward(p, d, dtype == FA_DTYPE_BF16, mode_of(*rope), blocks, st) != cudaSuccess) return FA_ERR_CUDA;
     fa_host::count_launches(1);
@@ -477,7 +488,8 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     p.max_pages = static_cast<int>(max_pages);
     while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
     p.num_pages = static_cast<int>(cache->num_pages);
-    const unsigned blocks = set_stages(p, d, fa::rope::kRows, di.sm_count * kBlocksPerSm);
+    const unsigned blocks = set_stages(p, d, fa::rope::kRows, di.sm_count * kBlocksPerSm,
+                                       int64_t{1} << 30);
     if (forward<true>(p, d, cache->dtype == FA_DTYPE_BF16, mode_of(r), blocks,
                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
