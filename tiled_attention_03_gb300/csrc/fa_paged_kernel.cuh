@@ -29,9 +29,22 @@
 //   * A row that sees no key (a sequence without keys, or more queries than keys under
 //     a mask) gets O = 0 and LSE = -inf.
 //
-// Warps (256 threads): 0-3 softmax, 4 Q and K producer, 5 MMA issuer, 6 V producer,
-// 7 scheduler (walks the CTA's share and publishes its pieces). A softmax warp none of
-// whose rows exists (decode: pf rows of 128) passes its blocks on without touching them.
+// Warps (256 threads; a ninth warp would cost the softmax its registers): 0-3 softmax, 4
+// scheduler (walks the CTA's share and publishes its pieces, one ahead) and Q and K
+// producer, 5 issuer of S = Q K^T, 6 V producer, 7 issuer of O += P V. A softmax warp
+// none of whose rows exists (decode: pf rows of 128) passes its blocks on without
+// touching them.
+//
+// Two warps issue the products because the tensor pipe holds only about one operation
+// ahead: a single issuer spent 1,032 cycles of a 128-key tile at d = 128 issuing and 410 in
+// its waits for P, V and K, all of them ready, with the pipe empty meanwhile and the
+// softmax waiting for scores. With two, the waits of one fall into the products of the
+// other. What one thread's issue order used to give is then a barrier: S(t) goes into the
+// TMEM buffer of P(t - 3) once the product with P(t - 3) has completed. The scores run
+// ahead by the three buffers (two at d = 256), across units as well. 2048 queries on
+// 32048 keys, 32 / 8 heads: 790 -> 700 us at d = 128, 768 -> 690 us at d = 256 (16 / 4
+// heads). At d <= 64 the softmax sets the pace and a second issuer only took its
+// instruction slots (620 and 657 us): one warp issues both there.
 // Every wait is bounded; on expiry the CTA records the failure, drains its copies and
 // MMAs, frees its tensor memory and returns.
 #pragma once
@@ -56,9 +69,9 @@ constexpr int kThreads = 256;
 // of chunks and single steps.
 constexpr int kChunkTicks = 5;
 constexpr int kQKWarp = 4;
-constexpr int kMmaWarp = 5;
+constexpr int kScoreWarp = 5;
 constexpr int kVWarp = 6;
-constexpr int kSchedWarp = 7;
+constexpr int kOutWarp = 7;
 // Q, K and V ring depths: what shared memory holds. Two Q tiles let the scores of the
 // next unit start while this one ends; K is read by its scores alone, soon after it
 // comes, V a few tiles later.
@@ -78,7 +91,11 @@ constexpr uint32_t kTmemQ = 128;  // d = 256 only
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in fa_fwd_kernel.cuh
 constexpr unsigned kStatusTimeout = 4;
 constexpr int kUnitSlots = 8;
-constexpr int kUnitConsumers = 7;  // warps 0-6 arrive once each per piece
+// Whether S and O += P V are issued by a warp each.
+__host__ __device__ constexpr bool two_issuers(int D) { return D >= 128; }
+// Warps that take the pieces: all but the scheduler (and an idle issuer); each arrives
+// once per piece.
+__host__ __device__ constexpr int unit_consumers(int D) { return two_issuers(D) ? 7 : 6; }
 constexpr int kMinPage = 8;        // tokens per page at least: a swizzle atom of a tile
 enum : int { kRoleSoftmax = 1, kRoleTma = 2, kRoleMma = 3 };
 
@@ -151,13 +168,13 @@ enum : int {
     kBarVEmpty = kBarVFull + kMaxStages,   // + stage
     kBarSFull = kBarVEmpty + kMaxStages,   // + buffer (3)
     kBarPFull = kBarSFull + kSBufs,        // + buffer (3)
-    kBarPVDone = kBarPFull + kSBufs,       // + parity of the block (2)
-    kBarODone = kBarPVDone + 2,
+    kBarPVDone = kBarPFull + kSBufs,       // + buffer (3)
+    kBarODone = kBarPVDone + kSBufs,
     kBarOFree = kBarODone + 1,
     kBarUnitFull = kBarOFree + 1,               // + slot (8)
     kBarUnitEmpty = kBarUnitFull + kUnitSlots,  // + slot (8)
-    kBarDrain = kBarUnitEmpty + kUnitSlots,
-    kBarQReady = kBarDrain + 1,            // Q copied into TMEM (d = 256)
+    kBarDrain = kBarUnitEmpty + kUnitSlots,  // + issuer (2)
+    kBarQReady = kBarDrain + 2,            // Q copied into TMEM (d = 256)
     kNumBarsUsed = kBarQReady + 1,
 };
 static_assert(kNumBarsUsed <= Smem<256>::kNumBars, "barrier slots");
@@ -301,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar0 = sbase + L::kBar;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+    constexpr int kStartSeq = kThreads / 32, kStartOff = kStartSeq + 1;
     volatile unsigned *scan = reinterpret_cast<volatile unsigned *>(smem + L::kScan);
     auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     auto sQ = [sbase](int k) { return sbase + L::kQ + (k % kQStages) * L::kQBytes; };
@@ -317,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     let_next_start();
 
     // ---- this CTA's share of the line of work: ticks w0 .. w1 - 1 of W. B sequences are
-    // summed, and then searched for w0, 256 at a time.
+    // summed, and then searched for w0, one to a thread at a time.
     auto block_sum = [&](unsigned v) -> unsigned {
         v = warp_sum(v);
         __syncthreads();
@@ -362,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const unsigned lo = before + incl - w;
         if (lo <= w0 && w0 < lo + w) {
-            scan[8] = static_cast<unsigned>(b);
-            scan[9] = w0 - lo;
+            scan[kStartSeq] = static_cast<unsigned>(b);
+            scan[kStartOff] = w0 - lo;
         }
         carry = all;
         if (w0 < carry) break;
@@ -376,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == kQKWarp * 32) {
         for (int s = 0; s < kQStages; ++s) {
             mbar_init(bar(kBarQFull + s), 1);
-            // Q's shared-memory copy is released by the MMA warp's commit, or at d = 256
+            // Q's shared-memory copy is released by the score issuer's commit, or at d = 256
             // by the softmax threads once they have copied it into TMEM
             mbar_init(bar(kBarQEmpty + s), kQT ? 128 : 1);
         }
@@ -392,16 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < kSB; ++b) {
             mbar_init(bar(kBarSFull + b), 1);
             mbar_init(bar(kBarPFull + b), 128);
+            mbar_init(bar(kBarPVDone + b), 1);
         }
-        mbar_init(bar(kBarPVDone + 0), 1);
-        mbar_init(bar(kBarPVDone + 1), 1);
         mbar_init(bar(kBarODone), 1);
         mbar_init(bar(kBarOFree), 128);
         for (int k = 0; k < kUnitSlots; ++k) {
             mbar_init(bar(kBarUnitFull + k), 1);
-            mbar_init(bar(kBarUnitEmpty + k), kUnitConsumers);
+            mbar_init(bar(kBarUnitEmpty + k), unit_consumers(D));
         }
-        mbar_init(bar(kBarDrain), 1);
+        mbar_init(bar(kBarDrain + 0), 1);
+        mbar_init(bar(kBarDrain + 1), 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -452,19 +470,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     };
 
-    if (warp == kSchedWarp) {
-        // ================================================================ scheduler
+    if (warp == kQKWarp) {
+        // ================================================================ scheduler, Q and K
         // the unit that holds tick w0, by the whole warp: head group sp, token tile qb, and
         // the ticks `rem` of it that belong to the CTA before
-        int b = static_cast<int>(scan[8]), sp, qb = 0, rem;
+        int b = static_cast<int>(scan[kStartSeq]), sp, qb = 0, rem;
         Seq s = load_seq(b, p);
         int nqb = (s.nq + p.tpt - 1) / p.tpt;
         {
             unsigned per = 0;
             for (int x = lane; x < nqb; x += 32) per += unit_tiles<kBN>(s, x, p) + kChunkTicks;
             per = warp_sum(per);
-            sp = static_cast<int>(scan[9] / per);
-            rem = static_cast<int>(scan[9] - sp * per);
+            sp = static_cast<int>(scan[kStartOff] / per);
+            rem = static_cast<int>(scan[kStartOff] - sp * per);
             for (int x0 = 0; x0 < nqb; x0 += 32) {
                 const int n = x0 + lane < nqb ? unit_tiles<kBN>(s, x0 + lane, p) + kChunkTicks : 0;
                 int incl = n;
@@ -483,79 +501,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rem -= __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        if (lane == 0) {
-            unsigned w = w0;
-            bool ok = true;
-            MergeInfo info{};
-            info.last_cta = -1;
-            int k = 0, pieces = 0;
-            for (; ok; ++k) {
-                const int slot = k % kUnitSlots;
-                ok = mbar_wait_bounded(bar(kBarUnitEmpty + slot), ((k / kUnitSlots) & 1) ^ 1, abort_flag,
-                                       budget);
-                if (!ok) break;
-                Piece P{};
-                P.b = -1;
-                while (w < w1 && P.b < 0) {
-                    int lo, hi, j0, j1;
-                    unit_range<kBN>(s, qb, p, lo, hi, j0, j1);
-                    const int n = j1 - j0 + 1;
-                    const int len = min(n + kChunkTicks - rem, static_cast<int>(w1 - w));
-                    // this share's tiles of the unit: ja .. je - 1
-                    const int ja = max(rem - kChunkTicks, 0), je = rem + len - kChunkTicks;
-                    if (n == 0 ? rem == 0 : je > ja) {
-                        P.b = b;
-                        P.sp = sp;
-                        P.t0 = qb * p.tpt;
-                        P.rows = (min(P.t0 + p.tpt, s.nq) - P.t0) * p.pf;
-                        P.lo_key = lo;
-                        P.hi_key = hi;
-                        P.q_off = s.nk - s.nq;
-                        P.nk = s.nk;
-                        P.tok0 = s.q0 + P.t0;
-                        P.j0 = j0 + ja;
-                        P.n = n == 0 ? 0 : je - ja;
-                        P.first = n == 0 ? 0 : P.j0 + static_cast<int>((w - w0) % P.n);
-                        const bool starts = ja == 0, ends = n == 0 || je == n;
-                        P.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (pieces > 0);
-                        if (n > 0) ++pieces;
-                        if (starts && !ends) {
-                            info.last_cta = static_cast<int>((w - rem + kChunkTicks + n - 1) / T);
-                            info.slot = P.slot;
-                            info.rows = P.rows;
-                            info.tok0 = P.tok0;
-                            info.head0 = sp * p.pf;
-                        }
-                    }
-                    w += len;
-                    rem = 0;
-                    if (++qb == nqb) {
-                        qb = 0;
-                        if (++sp == p.spaces) {
-                            sp = 0;
-                            while (w < w1 && ++b < p.B) {
-                                s = load_seq(b, p);
-                                nqb = (s.nq + p.tpt - 1) / p.tpt;
-                                if (nqb > 0) break;
-                            }
-                            if (b >= p.B) w = w1;
-                        }
+        unsigned w = w0;
+        bool ok = true;
+        MergeInfo info{};
+        info.last_cta = -1;
+        int pieces = 0;
+        // Finds the k-th piece and publishes it (by the whole warp, uniformly).
+        auto publish = [&](int k) -> Piece {
+            Piece P{};
+            P.b = -1;
+            const int slot = k % kUnitSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarUnitEmpty + slot),
+                                                           ((k / kUnitSlots) & 1) ^ 1, abort_flag, budget));
+            if (!ok) return P;
+            while (w < w1 && P.b < 0) {
+                int lo, hi, j0, j1;
+                unit_range<kBN>(s, qb, p, lo, hi, j0, j1);
+                const int n = j1 - j0 + 1;
+                const int len = min(n + kChunkTicks - rem, static_cast<int>(w1 - w));
+                // this share's tiles of the unit: ja .. je - 1
+                const int ja = max(rem - kChunkTicks, 0), je = rem + len - kChunkTicks;
+                if (n == 0 ? rem == 0 : je > ja) {
+                    P.b = b;
+                    P.sp = sp;
+                    P.t0 = qb * p.tpt;
+                    P.rows = (min(P.t0 + p.tpt, s.nq) - P.t0) * p.pf;
+                    P.lo_key = lo;
+                    P.hi_key = hi;
+                    P.q_off = s.nk - s.nq;
+                    P.nk = s.nk;
+                    P.tok0 = s.q0 + P.t0;
+                    P.j0 = j0 + ja;
+                    P.n = n == 0 ? 0 : je - ja;
+                    P.first = n == 0 ? 0 : P.j0 + static_cast<int>((w - w0) % P.n);
+                    const bool starts = ja == 0, ends = n == 0 || je == n;
+                    P.slot = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (pieces > 0);
+                    if (n > 0) ++pieces;
+                    if (starts && !ends) {
+                        info.last_cta = static_cast<int>((w - rem + kChunkTicks + n - 1) / T);
+                        info.slot = P.slot;
+                        info.rows = P.rows;
+                        info.tok0 = P.tok0;
+                        info.head0 = sp * p.pf;
                     }
                 }
+                w += len;
+                rem = 0;
+                if (++qb == nqb) {
+                    qb = 0;
+                    if (++sp == p.spaces) {
+                        sp = 0;
+                        while (w < w1 && ++b < p.B) {
+                            s = load_seq(b, p);
+                            nqb = (s.nq + p.tpt - 1) / p.tpt;
+                            if (nqb > 0) break;
+                        }
+                        if (b >= p.B) w = w1;
+                    }
+                }
+            }
+            if (lane == 0) {
                 *slot_of(k) = P;
                 mbar_arrive(bar(kBarUnitFull + slot));
-                if (P.b < 0) break;
             }
-            if (!ok) record_timeout(p, abort_flag, kRoleTma, k);
-            p.info[blockIdx.x] = info;
-        }
-    } else if (warp == kQKWarp) {
-        // ================================================================ Q and K
+            __syncwarp();
+            return P;
+        };
         int t = 0, q_loads = 0;
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            const Piece P = take(k, ok);
-            if (!ok || P.b < 0) break;
+        Piece N = publish(0);
+        for (int k = 0; ok && N.b >= 0; ++k) {
+            const Piece P = N;
+            N = publish(k + 1);
+            if (!ok) break;
             if (P.n == 0) continue;
             const int qs = q_loads % kQStages;
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarQEmpty + qs), ((q_loads / kQStages) & 1) ^ 1,
@@ -587,16 +604,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0) {
+            p.info[blockIdx.x] = info;
             if (!ok) record_timeout(p, abort_flag, kRoleTma, -1);
-            for (int s = 0; s < kQStages; ++s)
-                if (q_loads > s) {
-                    const int last = q_loads - 1 - ((q_loads - 1 - s) % kQStages);
-                    mbar_wait_bounded(bar(kBarQFull + s), (last / kQStages) & 1, nullptr, budget);
+            for (int st = 0; st < kQStages; ++st)
+                if (q_loads > st) {
+                    const int last = q_loads - 1 - ((q_loads - 1 - st) % kQStages);
+                    mbar_wait_bounded(bar(kBarQFull + st), (last / kQStages) & 1, nullptr, budget);
                 }
-            for (int s = 0; s < kKStages; ++s)
-                if (t > s) {
-                    const int last = t - 1 - ((t - 1 - s) % kKStages);
-                    mbar_wait_bounded(bar(kBarKFull + s), (last / kKStages) & 1, nullptr, budget);
+            for (int st = 0; st < kKStages; ++st)
+                if (t > st) {
+                    const int last = t - 1 - ((t - 1 - st) % kKStages);
+                    mbar_wait_bounded(bar(kBarKFull + st), (last / kKStages) & 1, nullptr, budget);
                 }
         }
     } else if (warp == kVWarp) {
@@ -630,8 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait_bounded(bar(kBarVFull + s), (last / kVStages) & 1, nullptr, budget);
                 }
         }
-    } else if (warp == kMmaWarp) {
-        // ================================================================ MMA issuer
+    } else if (warp == kScoreWarp || (warp == kOutWarp && two_issuers(D))) {
+        // ================================================================ issuers of the products
+        const bool scores = warp == kScoreWarp;
         constexpr uint32_t idesc_s = idesc_f16_ab(BF16, kBM, kBN, false, false);
         constexpr uint32_t idesc_o = idesc_f16_ab(BF16, kBM, D, false, true);
         constexpr int kSteps = L::kCols / 16;  // K-steps of 16 columns per region
@@ -660,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     k > 0 ? 1u : 0u);
                 }
                 umma_commit(bar(kBarSFull + t % kSB));
+                umma_commit(bar(kBarKEmpty + t % kKStages));  // K is read by S only
             }
             __syncwarp();
         };
@@ -673,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kBN / 16; ++k)
                     umma_f16_ts(tmem + kTmemO, tmem + kTmemS + (t % kSB) * kBN + k * 8,
                                 dv + k * ((2 * L::kGroup) >> 4), idesc_o, k > 0 ? 1u : acc0);
-                umma_commit(bar(kBarPVDone + (t & 1)));
+                umma_commit(bar(kBarPVDone + t % kSB));
+                umma_commit(bar(kBarVEmpty + t % kVStages));
             }
             __syncwarp();
         };
@@ -696,54 +717,67 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
         };
-        int t = 0, live = 0;
+        int t = 0, live = 0;  // K/V tiles, and pieces with tiles, so far
         bool ok = true;
         int k = 0;
         for (; ok; ++k) {
             const Piece P = take(k, ok);
             if (!ok || P.b < 0) break;
-            const int n = P.n;
-            if (n == 0) continue;
-            ok = wait(kQT ? kBarQReady : kBarQFull + live % kQStages, (live / kQStages) & 1);
-            for (int x = 0; ok && x < n && x < kSB; ++x) {
-                ok = wait(kBarKFull + (t + x) % kKStages, ((t + x) / kKStages) & 1);
-                if (ok) {
-                    issue_s(t + x, live);
-                    commit(kBarKEmpty + (t + x) % kKStages);  // K is read by S only
-                }
-            }
-            for (int x = 0; ok && x < n; ++x, ++t) {
+            if (P.n == 0) continue;
+            auto q_ready = [&] {
+                return wait(kQT ? kBarQReady : kBarQFull + live % kQStages, (live / kQStages) & 1);
+            };
+            auto k_ready = [&](int tk) { return wait(kBarKFull + tk % kKStages, (tk / kKStages) & 1); };
+            auto output = [&](int x) {
+                ok = wait(kBarVFull + t % kVStages, (t / kVStages) & 1);
+                if (!ok) return;
                 const int kv0 = P.tile(x) * kBN;
-                if (kv0 < P.lo_key || kv0 + kBN - 1 > P.hi_key) {
-                    // while the softmax is still at this tile
-                    ok = wait(kBarVFull + t % kVStages, (t / kVStages) & 1);
-                    if (!ok) break;
-                    zero_rows(t, kv0, P.lo_key, P.hi_key);
-                }
-                ok = wait(kBarPFull + t % kSB, (t / kSB) & 1) &&
-                     wait(kBarVFull + t % kVStages, (t / kVStages) & 1);
+                if (kv0 < P.lo_key || kv0 + kBN - 1 > P.hi_key)
+                    zero_rows(t, kv0, P.lo_key, P.hi_key);  // while the softmax is still at this tile
+                ok = wait(kBarPFull + t % kSB, (t / kSB) & 1);
                 if (ok && x == 0 && live > 0) ok = wait(kBarOFree, (live - 1) & 1);
-                if (!ok) break;
-                issue_pv(t, x == 0);
-                commit(kBarVEmpty + t % kVStages);
-                if (x + kSB < n) {
-                    ok = wait(kBarKFull + (t + kSB) % kKStages, ((t + kSB) / kKStages) & 1);
-                    if (!ok) break;
-                    issue_s(t + kSB, live);
-                    commit(kBarKEmpty + (t + kSB) % kKStages);
+                if (ok) issue_pv(t, x == 0);
+            };
+            if constexpr (!two_issuers(D)) {
+                ok = q_ready();
+                for (int x = 0; ok && x < P.n && x < kSB; ++x) {
+                    ok = k_ready(t + x);
+                    if (ok) issue_s(t + x, live);
                 }
+                for (int x = 0; ok && x < P.n; ++x, ++t) {
+                    output(x);
+                    if (ok && x + kSB < P.n) {
+                        ok = k_ready(t + kSB);
+                        if (ok) issue_s(t + kSB, live);  // after the product with P(t), in issue order
+                    }
+                }
+                if (ok) {
+                    commit(kBarQEmpty + live % kQStages);
+                    commit(kBarODone);
+                }
+            } else if (scores) {
+                ok = q_ready();
+                for (int x = 0; ok && x < P.n; ++x, ++t) {
+                    ok = k_ready(t);
+                    // the buffer's last P has been multiplied (one wait per use, and the
+                    // next use's product needs this S: the phases cannot run ahead)
+                    if (ok && t >= kSB) ok = wait(kBarPVDone + t % kSB, (t / kSB - 1) & 1);
+                    if (ok) issue_s(t, live);
+                }
+                if (ok && !kQT) commit(kBarQEmpty + live % kQStages);
+            } else {
+                for (int x = 0; ok && x < P.n; ++x, ++t) output(x);
+                if (ok) commit(kBarODone);
             }
-            if (!ok) break;
-            if constexpr (!kQT) commit(kBarQEmpty + live % kQStages);
-            commit(kBarODone);
             ++live;
         }
         if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleMma, k);
-        if (elect_one()) umma_commit(bar(kBarDrain));
+        const int drain = kBarDrain + (scores ? 0 : 1);
+        if (elect_one()) umma_commit(bar(drain));
         __syncwarp();
-        if (lane == 0) mbar_wait_bounded(bar(kBarDrain), 0, nullptr, budget);
+        if (lane == 0) mbar_wait_bounded(bar(drain), 0, nullptr, budget);
         __syncwarp();
-    } else {
+    } else if (warp < 4) {
         // ================================================================ softmax warpgroup
         const int row = threadIdx.x & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -900,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // product completes; rescale this row's O before P(j) is released.
                 if (x0 > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
                     const int tp = t - 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarPVDone + (tp & 1)), (tp >> 1) & 1,
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarPVDone + tp % kSB), (tp / kSB) & 1,
                                                                    abort_flag, budget));
                     if (!ok) break;
                     tc_fence_after();
