@@ -143,6 +143,36 @@ def test_many_sequences(H, Hk, new):
     check(o, lse, b[5], 0.125, "causal", (0, 0), torch.bfloat16)
 
 
+@pytest.mark.parametrize("B", [12, 300])
+@pytest.mark.parametrize("kind", ["steps", "one chunk", "long steps"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_few_tokens_per_sequence(d, kind, B):
+    """A few tokens per sequence on average: every sequence some (the decode kernel), or one
+    a chunk and the others one (the chunk kernel), as the device finds."""
+    rng = random.Random(B)
+    lens = [(rng.choice([2, 3, 4]), rng.choice([4, 100, 700])) for _ in range(B)]
+    if kind == "one chunk":
+        lens = [(1, n) for _, n in lens]
+        lens[B // 2] = (4 * B, 4 * B + 321)
+    elif kind == "long steps":
+        lens[-1] = (16, 900)
+    b = paged(lens, 4, 2, d, torch.bfloat16, 16, seed=B)
+    o, lse = run(*b[:5], 0.1, "causal")
+    check(o, lse, b[5], 0.1, "causal", (0, 0), torch.bfloat16)
+
+
+def test_a_workspace_passed_on():
+    """One workspace, used by batches of all kinds in turn: what a call leaves there means
+    nothing to the next (each is larger than the one before)."""
+    ws = torch.zeros(fa.fa_forward_paged_workspace_bytes(128), dtype=torch.uint8, device=DEV)
+    batches = [[(1, 4000)], [(70, 3000), (1, 900)], [(1, 2000)] * 90, [(2, 500)] * 60, [(1, 300)] * 79 + [(150, 9000)],
+               [(1, 700)] * 500]
+    for i, lens in enumerate(batches + batches[3:]):
+        b = paged(lens, 4, 1, 128, torch.bfloat16, 64, "head", seed=i)
+        o, lse = run(*b[:5], 0.1, "causal", workspace=ws)
+        check(o, lse, b[5], 0.1, "causal", (0, 0), torch.bfloat16)
+
+
 def test_long_prompt_chunk():
     b = paged([(1500, 4100), (1, 100)], 8, 2, 128, torch.bfloat16, 16, seed=4)
     o, lse = run(*b[:5], 128 ** -0.5, "causal")

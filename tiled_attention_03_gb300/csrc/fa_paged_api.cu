@@ -71,26 +71,36 @@ Layout layout_of(int64_t d, int64_t sms) {
     return l;
 }
 
-template <int D, bool BF16>
-cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                   const fa::paged::Params &p, const fa::paged::MergeParams &m, unsigned sms, cudaStream_t st) {
-    const cudaError_t e = fa::launch_after(fa::paged::fa_paged_kernel<D, BF16>, dim3(sms),
-                                           fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st, q, k, v, p);
-    if (e != cudaSuccess) return e;
-    return fa::launch_after(fa::paged::fa_paged_merge_kernel<D, BF16, fa::paged::kBM>, dim3(sms, 16),
-                            fa::paged::kMergeWarps * 32, 0, st, m);
-}
+// What a call runs: one of the kernels, or both (see fa_paged_decode_kernel.cuh), and the merge.
+struct Plan {
+    bool decode, chunk;
+    fa::paged::SmallParams small;
+    fa::paged::Params p;
+    fa::paged::MergeParams merge;
+    CUtensorMap q, k, v;
+    unsigned sms;
+};
 
 template <int D, bool BF16>
-cudaError_t launch_decode(const fa::paged::SmallParams &p, const fa::paged::MergeParams &m, unsigned sms,
-                          cudaStream_t st) {
-    using L = fa::paged::Small<D>;
-    const cudaError_t e = fa::launch_after(fa::paged::fa_paged_decode_kernel<D, BF16>, dim3(sms),
-                                           L::kWarps * 32, L::kBytes, st, p);
-    if (e != cudaSuccess) return e;
-    return fa::launch_after(fa::paged::fa_paged_merge_kernel<D, BF16, fa::paged::kSmallRows>,
-                            dim3(sms * L::kWarps),
-                            fa::paged::kMergeWarps * 32, 0, st, m);
+cudaError_t launch(const Plan &x, cudaStream_t st) {
+    using S = fa::paged::Small<D>;
+    if (x.decode) {
+        const cudaError_t e = fa::launch_after(fa::paged::fa_paged_decode_kernel<D, BF16>, dim3(x.sms),
+                                               S::kWarps * 32, S::kBytes, st, x.small);
+        if (e != cudaSuccess) return e;
+    }
+    if (x.chunk) {
+        fa::paged::Params p = x.p;
+        p.infos = S::kWarps;
+        const cudaError_t e = fa::launch_after(fa::paged::fa_paged_kernel<D, BF16>, dim3(x.sms),
+                                               fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st, x.q,
+                                               x.k, x.v, p);
+        if (e != cudaSuccess) return e;
+    }
+    // a block per worker; a unit of the chunk kernel has 128 rows to share among several
+    const dim3 grid(x.decode ? x.sms * S::kWarps : x.sms, !x.chunk ? 1 : x.decode ? 4 : 16);
+    return fa::launch_after(fa::paged::fa_paged_merge_kernel<D, BF16>, grid, fa::paged::kMergeWarps * 32, 0,
+                            st, x.merge);
 }
 
 int sm_count_or_default() {
@@ -127,10 +137,17 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     int64_t pf = group;
     if (pf > fa::paged::kBM)
         for (pf = fa::paged::kBM; group % pf != 0;) --pf;
-    // Few tokens per sequence on average: the decode kernel, 16 rows per unit. A longer
-    // sequence among them is cut into more units, each reading its keys again.
-    const bool decode = pf <= fa::paged::kSmallRows && total_q * pf <= B * fa::paged::kSmallRows;
-    const int64_t tpt = (decode ? fa::paged::kSmallRows : fa::paged::kBM) / pf, spaces = H / pf;
+    // Steps, of no more tokens than sequences (or too few for a long one): the decode
+    // kernel. A few tokens per sequence on average: whichever kernel suits the longest, as
+    // it turns out on the device; its units re-read a sequence's keys kMaxReads times at most.
+    constexpr int64_t kMaxReads = 2;
+    const bool small = pf <= fa::paged::kSmallRows;
+    const int64_t tpt_small = small ? fa::paged::kSmallRows / pf : 0, tpt = fa::paged::kBM / pf;
+    const int64_t max_new = kMaxReads * tpt_small;
+    const bool steps_only = small && (total_q <= B || total_q <= max_new);
+    const bool either = small && !steps_only && total_q <= B * tpt_small;
+    const bool decode = steps_only || either, chunked = !steps_only;
+    const int64_t spaces = H / pf;
     const int64_t max_keys = max_pages * cache->page_size;
     // Size limits of this implementation: 32-bit token and key indices, and a line of
     // work below 2^31 tiles.
@@ -138,9 +155,12 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     if (total_q > kLimit || max_pages > kLimit || max_keys > kLimit || B > kLimit || H > kLimit ||
         total_q * H > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;
-    const int64_t tile = decode ? (d <= 64 ? 32 : 16) : fa::paged::bn(static_cast<int>(d));
-    const double tiles = static_cast<double>(max_keys / tile + 2 + fa::paged::kUnitTicks + fa::paged::kChunkTicks);
-    if (static_cast<double>(spaces) * static_cast<double>(total_q / tpt + B) * tiles > 2147483647.0)
+    auto line = [&](int64_t tokens, int64_t keys) {  // ticks of a line of work at most
+        return static_cast<double>(spaces) * static_cast<double>(total_q / tokens + B) *
+               static_cast<double>(max_keys / keys + 8);
+    };
+    if ((decode && line(tpt_small, d <= 64 ? 32 : 16) > 2147483647.0) ||
+        (chunked && line(tpt, fa::paged::bn(static_cast<int>(d))) > 2147483647.0))
         return FA_ERR_UNSUPPORTED;
     const Layout lay = layout_of(d, sm_count_or_default());
     if (workspace == nullptr || !fa_host::aligned32(workspace) || workspace_bytes < lay.bytes)
@@ -180,7 +200,6 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
 
     const bool bf16 = cache->dtype == FA_DTYPE_BF16;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned sms = static_cast<unsigned>(di.sm_count);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     int page_log2 = 0;
     while ((int64_t{1} << page_log2) < cache->page_size) ++page_log2;
@@ -193,38 +212,35 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         wr = window_right < every ? window_right : every;
     }
     const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-    fa::paged::MergeParams m{};
-    m.info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
-    m.part_LSE = reinterpret_cast<float *>(ws + lay.lse);
-    m.part_O = reinterpret_cast<float *>(ws + lay.o);
-    m.O = O;
-    m.LSE = LSE;
-    m.H = static_cast<int>(H);
-    m.pf = static_cast<int>(pf);
-    cudaError_t e;
+    Plan x{};
+    x.decode = decode;
+    x.chunk = chunked;
+    x.sms = static_cast<unsigned>(di.sm_count);
+    fa::paged::MergeInfo *info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
+    float *part_LSE = reinterpret_cast<float *>(ws + lay.lse), *part_O = reinterpret_cast<float *>(ws + lay.o);
+    x.merge.info = info;
+    x.merge.part_LSE = part_LSE;
+    x.merge.part_O = part_O;
+    x.merge.O = O;
+    x.merge.LSE = LSE;
+    x.merge.H = static_cast<int>(H);
+    x.merge.pf = static_cast<int>(pf);
     const int fault = fa_host::take_fault_position();  // the decode kernel has no wait to run out
-    if (decode) {
-        fa::paged::SmallParams p{};
-        p.Q = static_cast<const uint16_t *>(Q);
+    // what both kernels' parameters have alike
+    auto common = [&](auto &p) {
         p.O = O;
         p.LSE = LSE;
-        p.part_O = reinterpret_cast<float *>(ws + lay.o);
-        p.part_LSE = reinterpret_cast<float *>(ws + lay.lse);
-        p.info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
-        p.k = static_cast<const uint16_t *>(cache->k);
-        p.v = static_cast<const uint16_t *>(cache->v);
-        p.page_stride = cache->page_stride;
-        p.token_stride = cache->token_stride;
-        p.head_stride = cache->head_stride;
+        p.part_O = part_O;
+        p.part_LSE = part_LSE;
+        p.info = info;
         p.cu_q = cu_q;
         p.seq_k = seq_k;
         p.table = table;
         p.B = static_cast<int>(B);
-        p.H = m.H;
+        p.H = static_cast<int>(H);
         p.kv_group = static_cast<int>(group);
-        p.pf = m.pf;
+        p.pf = static_cast<int>(pf);
         p.spaces = static_cast<int>(spaces);
-        p.tpt = static_cast<int>(tpt);
         p.total_q = static_cast<int>(total_q);
         p.max_pages = static_cast<int>(max_pages);
         p.page_log2 = page_log2;
@@ -233,74 +249,51 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         p.wl = static_cast<int>(wl);
         p.wr = static_cast<int>(wr);
         p.scale_log2 = scale_log2;
+    };
+    if (decode) {
+        fa::paged::SmallParams &p = x.small;
+        common(p);
+        p.Q = static_cast<const uint16_t *>(Q);
+        p.k = static_cast<const uint16_t *>(cache->k);
+        p.v = static_cast<const uint16_t *>(cache->v);
+        p.page_stride = cache->page_stride;
+        p.token_stride = cache->token_stride;
+        p.head_stride = cache->head_stride;
+        p.tpt = static_cast<int>(tpt_small);
         p.min_ticks = kMinTicks;
-        if (d == 32)
-            e = bf16 ? launch_decode<32, true>(p, m, sms, st) : launch_decode<32, false>(p, m, sms, st);
-        else if (d == 64)
-            e = bf16 ? launch_decode<64, true>(p, m, sms, st) : launch_decode<64, false>(p, m, sms, st);
-        else if (d == 128)
-            e = bf16 ? launch_decode<128, true>(p, m, sms, st) : launch_decode<128, false>(p, m, sms, st);
-        else
-            e = bf16 ? launch_decode<256, true>(p, m, sms, st) : launch_decode<256, false>(p, m, sms, st);
-        if (e != cudaSuccess) return FA_ERR_CUDA;
-        fa_host::count_launches(2);
-        return FA_OK;
+        p.max_new = either ? static_cast<int>(max_new) : 0;
     }
-    const int kbn = fa::paged::bn(static_cast<int>(d));
-    const int64_t chunk = cache->page_size < kbn ? cache->page_size : kbn;
-    CUtensorMap mq, mk, mv;
-    fa_host::PageSteps steps;
-    if (!fa_host::page_steps(*cache, &steps)) return FA_ERR_UNSUPPORTED;
-    if (!fa_host::make_map_rows(&mq, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf),
-                                static_cast<uint32_t>(tpt)) ||
-        !fa_host::make_map_pages(&mk, cache->k, *cache, steps, static_cast<uint32_t>(chunk)) ||
-        !fa_host::make_map_pages(&mv, cache->v, *cache, steps, static_cast<uint32_t>(chunk)))
-        return FA_ERR_CUDA;
-
-    fa::paged::Params p{};
-    p.O = O;
-    p.LSE = LSE;
-    p.info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
-    p.part_LSE = reinterpret_cast<float *>(ws + lay.lse);
-    p.part_O = reinterpret_cast<float *>(ws + lay.o);
-    p.cu_q = cu_q;
-    p.seq_k = seq_k;
-    p.table = table;
-    p.B = static_cast<int>(B);
-    p.H = static_cast<int>(H);
-    p.kv_group = static_cast<int>(group);
-    p.pf = static_cast<int>(pf);
-    p.spaces = static_cast<int>(spaces);
-    p.tpt = static_cast<int>(tpt);
-    p.total_q = static_cast<int>(total_q);
-    p.max_pages = static_cast<int>(max_pages);
-    p.page_log2 = page_log2;
-    p.num_pages = static_cast<int>(cache->num_pages);
-    p.max_keys = static_cast<int>(max_keys);
-    p.chunk = static_cast<int>(chunk);
-    p.page_step = static_cast<int>(steps.page);
-    p.head_step = static_cast<int>(steps.head);
-    p.page_none = static_cast<int>(steps.count);
-    p.wl = static_cast<int>(wl);
-    p.wr = static_cast<int>(wr);
-    p.scale_log2 = scale_log2;
-    p.wait_budget_ns = fa_host::wait_budget();
-    p.status = di.status;
-    p.fault_skip_k = fault;
-    if (d == 32)
-        e = bf16 ? launch<32, true>(mq, mk, mv, p, m, sms, st)
-                 : launch<32, false>(mq, mk, mv, p, m, sms, st);
-    else if (d == 64)
-        e = bf16 ? launch<64, true>(mq, mk, mv, p, m, sms, st)
-                 : launch<64, false>(mq, mk, mv, p, m, sms, st);
-    else if (d == 128)
-        e = bf16 ? launch<128, true>(mq, mk, mv, p, m, sms, st)
-                 : launch<128, false>(mq, mk, mv, p, m, sms, st);
-    else
-        e = bf16 ? launch<256, true>(mq, mk, mv, p, m, sms, st)
-                 : launch<256, false>(mq, mk, mv, p, m, sms, st);
+    if (chunked) {
+        fa::paged::Params &p = x.p;
+        common(p);
+        const int kbn = fa::paged::bn(static_cast<int>(d));
+        const int64_t box = cache->page_size < kbn ? cache->page_size : kbn;
+        fa_host::PageSteps steps;
+        if (!fa_host::page_steps(*cache, &steps)) return FA_ERR_UNSUPPORTED;
+        if (!fa_host::make_map_rows(&x.q, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf),
+                                    static_cast<uint32_t>(tpt)) ||
+            !fa_host::make_map_pages(&x.k, cache->k, *cache, steps, static_cast<uint32_t>(box)) ||
+            !fa_host::make_map_pages(&x.v, cache->v, *cache, steps, static_cast<uint32_t>(box)))
+            return FA_ERR_CUDA;
+        p.tpt = static_cast<int>(tpt);
+        p.chunk = static_cast<int>(box);
+        p.page_step = static_cast<int>(steps.page);
+        p.head_step = static_cast<int>(steps.head);
+        p.page_none = static_cast<int>(steps.count);
+        p.wait_budget_ns = fa_host::wait_budget();
+        p.status = di.status;
+        p.fault_skip_k = fault;
+        p.min_new = either ? static_cast<int>(max_new + 1) : 0;
+    }
+    cudaError_t e;
+    switch (d) {
+        case 32: e = bf16 ? launch<32, true>(x, st) : launch<32, false>(x, st); break;
+        case 64: e = bf16 ? launch<64, true>(x, st) : launch<64, false>(x, st); break;
+        case 128: e = bf16 ? launch<128, true>(x, st) : launch<128, false>(x, st); break;
+        default: e = bf16 ? launch<256, true>(x, st) : launch<256, false>(x, st); break;
+    }
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    fa_host::count_launches(2);
+    fa_host::count_launches(either ? 3 : 2);
     return FA_OK;
 }
 

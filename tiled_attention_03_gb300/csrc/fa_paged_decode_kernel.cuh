@@ -14,6 +14,12 @@
 // tiles (its start and end cost that much), and worker w takes ticks w T .. w T + T - 1. A unit
 // that several workers share is joined by fa_paged_merge_kernel.
 //
+// Which of the two kernels a batch is for depends on its longest sequence, which only the
+// device knows: many rows of one sequence in units of 16 read its keys again and again. With
+// no more tokens than sequences the decode kernel takes the batch; with a few per
+// sequence on average both are launched and look for a sequence of more than max_new
+// tokens, and one of them returns at once.
+//
 // Keys that no row of the unit sees are not read: their rows are filled with zeros in
 // shared memory, whatever the pages hold.
 #pragma once
@@ -105,6 +111,7 @@ struct SmallParams {
     int wl, wr;
     float scale_log2;
     int min_ticks;
+    int max_new;  // > 0: leave the batch to the chunk kernel if a sequence has more new tokens
 };
 
 // Ticks of one head group of sequence b: its units' tiles and kUnitTicks each.
@@ -178,6 +185,12 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
             if (i < own) w[i] = small_work<kKeys>(q[i], p);
             sum += w[i] * p.spaces;
         }
+        if (p.max_new > 0) {
+            int longest = q[0].nq;
+#pragma unroll
+            for (int i = 1; i < kOwn; ++i) longest = max(longest, q[i].nq);
+            if (__any_sync(0xffffffffu, longest > p.max_new)) return;
+        }
         unsigned incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -213,6 +226,11 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
         }
     } else {
         unsigned mine = 0, first = 0, carry = 0;
+        if (p.max_new > 0) {
+            int longest = 0;
+            for (int x = threadIdx.x; x < p.B; x += kThr) longest = max(longest, small_seq(x, p).nq);
+            if (__syncthreads_or(longest > p.max_new)) return;
+        }
         for (int x = threadIdx.x; x < p.B; x += kThr) {
             const unsigned w = small_work<kKeys>(small_seq(x, p), p) * p.spaces;
             if (x < kThr) first = w;
@@ -501,6 +519,7 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
             if (starts && !ends) {
                 info.last_cta = static_cast<int>((w - skip + kUnitTicks + n - 1) / T);
                 info.slot = slot;
+                info.slot_rows = kSmallRows;
                 info.rows = rows;
                 info.tok0 = tok0;
                 info.head0 = head0;

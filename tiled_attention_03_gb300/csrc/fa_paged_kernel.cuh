@@ -106,7 +106,8 @@ struct MergeInfo {
     int slot;       // partial slot of the first piece (the others: 2 * cta)
     int rows;       // rows of the unit
     int tok0, head0;  // its first token (of all tokens) and head
-    int pad[3];
+    int slot_rows;  // rows of a partial slot
+    int pad[2];
 };
 
 struct Params {
@@ -129,6 +130,10 @@ struct Params {
     unsigned long long wait_budget_ns;
     unsigned int *status;
     int fault_skip_k;  // test hook: every CTA skips the K load at this ring position (-1: none)
+    // Where the decode kernel was launched before (min_new > 0): leave the batch to it
+    // unless a sequence has at least min_new new tokens. info then has `infos` entries
+    // per CTA, all to be written.
+    int min_new, infos;
 };
 
 // Tiles are stored as regions of min(D, 64) columns with the swizzle of that row width. Q: region
@@ -346,6 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kThreads / 32; ++i) s += scan[i];
         return s;
     };
+    if (p.min_new > 0) {
+        int longest = 0;
+        for (int b = threadIdx.x; b < p.B; b += kThreads) longest = max(longest, load_seq(b, p).nq);
+        if (!__syncthreads_or(longest >= p.min_new)) return;
+        for (int i = 1 + threadIdx.x; i < p.infos; i += kThreads)
+            p.info[i * gridDim.x + blockIdx.x].last_cta = -1;
+    }
     unsigned mine = 0, first = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const unsigned w = seq_work<kBN>(b0 + static_cast<int>(threadIdx.x), p) * p.spaces;
@@ -540,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (starts && !ends) {
                         info.last_cta = static_cast<int>((w - rem + kChunkTicks + n - 1) / T);
                         info.slot = P.slot;
+                        info.slot_rows = kBM;
                         info.rows = P.rows;
                         info.tok0 = P.tok0;
                         info.head0 = sp * p.pf;
@@ -1051,8 +1064,7 @@ struct MergeParams {
 
 constexpr int kMergeWarps = 8;
 
-// kRows: rows of a partial slot.
-template <int D, bool BF16, int kRows>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const MergeParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kV = D / 32;  // consecutive columns per lane
@@ -1074,7 +1086,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
         const int row = row0 + warp / ways;
         const bool there = row < u.rows;
         auto prow = [&](int s) {
-            return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * kRows + row;
+            return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * u.slot_rows + row;
         };
         float m = -INFINITY, wsum = 0.f, acc[kV];
 #pragma unroll

@@ -300,14 +300,21 @@ __device__ __forceinline__ Place place(const Params &p, int m, int n) {
     if constexpr (!PAGED) {
         r.pos = p.positions ? __ldg(p.positions + m) : n;
     } else {
+        // every lane probes the end of one of 32 parts of what is left to search
         int before = 0;
-        for (int b = threadIdx.x & 31; b < p.B; b += 32) before += p.cu_q[b + 1] <= m;
-        before = __reduce_add_sync(0xffffffffu, before);
+        for (int left = p.B; left > 0;) {
+            const int step = (left + 31) >> 5;
+            const int last = (static_cast<int>(threadIdx.x & 31) + 1) * step;
+            const bool past = last <= left && p.cu_q[before + last] <= m;
+            const int parts = __popc(__ballot_sync(0xffffffffu, past));
+            before += parts * step;
+            left = min(step - 1, left - parts * step);
+        }
         r.live = false;
         if (before < p.B) {
-            const int first = p.cu_q[before];
-            const long long at = static_cast<long long>(p.seq_k[before]) - (p.cu_q[before + 1] - m);
-            if (m >= first) {
+            const int first = p.cu_q[before], end = p.cu_q[before + 1];
+            const long long at = static_cast<long long>(p.seq_k[before]) - (end - m);
+            if (m >= first && m < end) {
                 r.live = true;
                 r.pos = static_cast<int>(at);
                 const long long page = at >> p.page_log2;
