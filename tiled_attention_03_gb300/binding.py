@@ -190,9 +190,10 @@ def fa_test_arm_fault(kv_position: int) -> None:
 
 def _stream_handle(stream) -> int | None:
     if stream is None:
-        if not torch.cuda.is_initialized():
+        try:  # the handle alone: a tenth of torch.cuda.current_stream()'s time
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except (AttributeError, RuntimeError, AssertionError):
             return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -622,22 +623,34 @@ def _rows(t: torch.Tensor | None, dtype, what: str) -> bytes:
 
 
 def _qk_sizes(q, k, what: str):
-    """B, H, H_kv, N, d of queries and keys that may each be None."""
+    """B, H, H_kv, N, d and dtype of queries and keys that may each be None."""
     some = q if q is not None else k
-    if some is None or some.dim() not in (3, 4) or some.dtype not in _DTYPES:
+    if some is None:
         raise FaError(FA_ERR_INVALID_ARG, what)
-    shape = some.shape
-    B, N, d = (shape[0], shape[2], shape[3]) if len(shape) == 4 else (1, shape[0], shape[2])
-    H, H_kv = (0 if t is None else t.shape[1] for t in (q, k))
-    if q is not None and k is not None:
+    dtype, shape = some.dtype, some.shape
+    if dtype not in _DTYPES or not 3 <= len(shape) <= 4:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    heads = shape[1]
+    if q is None:
+        H, H_kv = 0, heads
+    elif k is None:
+        H, H_kv = heads, 0
+    else:
         other = k.shape
-        if len(other) != len(shape) or other[0] != shape[0] or other[2:] != shape[2:]:
+        H, H_kv = heads, other[1]
+        if len(other) != len(shape) or other[0] != shape[0] or other[2] != shape[2] or \
+                other[-1] != shape[-1]:
             raise FaError(FA_ERR_INVALID_ARG, what)
-    return B, H, H_kv, N, d
+    if len(shape) == 4:
+        return shape[0], H, H_kv, shape[2], shape[3], dtype
+    return 1, H, H_kv, shape[0], shape[2], dtype
 
 
 def _same_shape(a, b, what: str) -> None:
-    if (a is None) != (b is None) or (a is not None and a.shape != b.shape):
+    if a is None or b is None:
+        if a is not b:
+            raise FaError(FA_ERR_INVALID_ARG, what)
+    elif a.shape != b.shape:
         raise FaError(FA_ERR_INVALID_ARG, what)
 
 
@@ -658,9 +671,9 @@ def _workspace(workspace, need: int, like: torch.Tensor, stream, what: str):
             workspace.record_stream(stream)
         elif stream is not None:
             workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=like.device))
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+    elif not workspace.is_contiguous():
         raise FaError(FA_ERR_INVALID_ARG, what)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def fa_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
@@ -670,12 +683,11 @@ def fa_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch
     (tokens, heads, d), any strides with d contiguous (slices of a fused projection);
     either pair may be None. positions: int32, one per token (B x N), None: 0 .. N-1."""
     what = "fa_qk_norm_rope"
-    B, H, H_kv, N, d = _qk_sizes(q, k, what)
-    dtype = (q if q is not None else k).dtype
+    B, H, H_kv, N, d, dtype = _qk_sizes(q, k, what)
     _same_shape(q, q_out, what)
     _same_shape(k, k_out, what)
     rope.check(dtype, d, what)
-    rc = load_library().fa_qk_norm_rope(
+    rc = (_lib or load_library()).fa_qk_norm_rope(
         _rows(q, dtype, what), _rows(k, dtype, what), _rows(q_out, dtype, what),
         _rows(k_out, dtype, what), rope.address, _int32(positions, B * N, what), B, H, H_kv, N, d,
         _DTYPES[dtype], _stream_handle(stream))
@@ -704,10 +716,8 @@ def fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
     dq_weight, dk_weight (d,) float32, each given exactly where `rope` has the weight.
     Without a workspace tensor one is taken from PyTorch's caching allocator."""
     what = "fa_qk_norm_rope_backward"
-    lib = load_library()
-    B, H, H_kv, N, d = _qk_sizes(dq, dk, what)
-    like = dq if dq is not None else dk
-    dtype = like.dtype
+    lib = _lib or load_library()
+    B, H, H_kv, N, d, dtype = _qk_sizes(dq, dk, what)
     for x, dy, dx, w, dw in ((q, dq_out, dq, rope.q_weight, dq_weight),
                              (k, dk_out, dk, rope.k_weight, dk_weight)):
         _same_shape(dy, dx, what)
@@ -722,7 +732,7 @@ def fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
     if dq_weight is not None or dk_weight is not None:
         ws, n, keep = _workspace(
             workspace, lib.fa_qk_norm_rope_backward_workspace_bytes(d) if workspace is None else 0,
-            like, stream, what)
+            dq if dq is not None else dk, stream, what)
     rc = lib.fa_qk_norm_rope_backward(
         _rows(q, dtype, what), _rows(k, dtype, what), _rows(dq_out, dtype, what),
         _rows(dk_out, dtype, what), _rows(dq, dtype, what), _rows(dk, dtype, what), ptr(dq_weight),
@@ -748,9 +758,10 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, rope: NormRope,
 def _batch(block_table, cu_seqlens_q, seqlens_k, what: str):
     """(table pointer, max_pages, cu pointer, seqlens pointer, B) of a serving batch."""
     B = seqlens_k.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or B < 1:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B or B < 1:
         raise FaError(FA_ERR_INVALID_ARG, what)
-    pages = block_table.shape[1]
+    pages = shape[1]
     return (_int32(block_table, B * pages, what), pages, _int32(cu_seqlens_q, B + 1, what),
             _int32(seqlens_k, B, what), B)
 
@@ -774,7 +785,7 @@ def fa_paged_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     if rope is not None:
         rope.check(dtype, d, what)
     table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
-    rc = load_library().fa_paged_append(
+    rc = (_lib or load_library()).fa_paged_append(
         _rows(q, dtype, what), _rows(k, dtype, what), _rows(v, dtype, what),
         _rows(q_out, dtype, what), cache.address, table, pages, cu, lens, B,
         0 if q is None else q.shape[1], total, None if rope is None else rope.address,
@@ -796,14 +807,13 @@ def fa_forward_paged(q: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, cache:
     contiguous; block_table (B, max_pages), cu_seqlens_q (B + 1,), seqlens_k (B,) int32.
     Without a workspace tensor one is taken from PyTorch's caching allocator."""
     what = "fa_forward_paged"
-    lib = load_library()
+    lib = _lib or load_library()
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.d or o.shape != shape or lse.shape != shape[:2] or \
             q.dtype != cache.dtype or o.dtype != q.dtype or lse.dtype != torch.float32:
         raise FaError(FA_ERR_INVALID_ARG, what)
-    for t in (q, o, lse):
-        if not t.is_cuda or not t.is_contiguous():
-            raise FaError(FA_ERR_INVALID_ARG, what)
+    if not (q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
+        raise FaError(FA_ERR_INVALID_ARG, what)
     table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
     ws, n, keep = _workspace(
         workspace, lib.fa_forward_paged_workspace_bytes(cache.d) if workspace is None else 0, q,
