@@ -1068,7 +1068,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const MergeParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kV = D / 32;  // consecutive columns per lane
-    constexpr int kMergeBatch = D <= 128 ? 8 : 4;
+    constexpr int kMergeBatch = D <= 128 ? 4 : 2;
     __shared__ float red_o[kMergeWarps][D];
     __shared__ float red_m[kMergeWarps], red_w[kMergeWarps];
     after_previous();
