@@ -68,6 +68,15 @@ def test_a_good_forward_passes_the_checks(lib):
     fused = dict(batch=16 * 8 * 64, head=64, token=8 * 64)
     q, k = rows(0, 4, 16, 64, **fused), rows(0, 2, 16, 64, data=AT + 4 * 64 * 2, **fused)
     assert past_checks(forward(lib, q=q, k=k, y=q, z=k))
+    # the same with one token per batch entry, and with the batch inside the tokens
+    for B, N, batch, token in ((3, 1, 8 * 64, 8), (3, 1, 8 * 64, 0), (2, 5, 8 * 64, 2 * 8 * 64)):
+        q = rows(0, 4, N, 64, batch=batch, head=64, token=token)
+        k = rows(0, 2, N, 64, data=AT + 4 * 64 * 2, batch=batch, head=64, token=token)
+        assert past_checks(forward(lib, B=B, N=N, q=q, k=k, y=q, z=k)), (B, N)
+        near = rows(0, 2, N, 64, data=AT + 3 * 64 * 2, batch=batch, head=64, token=token)
+        assert forward(lib, B=B, N=N, y=q, z=near) == INVALID  # k_out over q_out's last head
+        wide = rows(0, 2, N, 64, data=AT + 7 * 64 * 2, batch=batch, head=64, token=token)
+        assert forward(lib, B=B, N=N, y=q, z=wide) == INVALID  # into the next token's q_out
     # a broadcast input: stride 0
     assert past_checks(forward(lib, q=rows(0, 4, 16, 64, head=0)))
 

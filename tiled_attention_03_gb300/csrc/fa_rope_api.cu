@@ -65,12 +65,14 @@ bool injective(const Tensor &t, int64_t d) {
     return true;
 }
 
-// Slices of one fused buffer: equal token strides s (and batch strides, a multiple of s),
-// each token's part shorter than s, and the two parts at different places modulo s.
+// Slices of one fused buffer: equal strides of tokens and batch entries (those there are
+// more than one of), the larger a multiple of the smaller, s; each tensor's part of a
+// token is shorter than s, and the two parts lie at different places modulo s.
 bool interleaved(const Tensor &a, const Tensor &b, int64_t d) {
-    const int64_t s = a.r->token;
-    if (a.N < 2 || s < 1 || b.r->token != s) return false;
-    if (a.B > 1 && (a.r->batch != b.r->batch || a.r->batch % s != 0)) return false;
+    if ((a.N > 1 && a.r->token != b.r->token) || (a.B > 1 && a.r->batch != b.r->batch)) return false;
+    const int64_t token = a.N > 1 ? a.r->token : 0, batch = a.B > 1 ? a.r->batch : 0;
+    const int64_t s = token > 0 && (batch == 0 || token < batch) ? token : batch;
+    if (s < 1 || token % s != 0 || batch % s != 0) return false;
     const int64_t span_a = a.heads > 1 ? (a.heads - 1) * a.r->head + d : d;
     const int64_t span_b = b.heads > 1 ? (b.heads - 1) * b.r->head + d : d;
     const intptr_t bytes = reinterpret_cast<intptr_t>(b.r->data) - reinterpret_cast<intptr_t>(a.r->data);
