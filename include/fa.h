@@ -517,7 +517,9 @@ int64_t fa_launch_count(void);
  * usable. A negative position disarms the hook. When the next call is
  * fa_backward or fa_backward_varlen, the position counts units instead: every
  * CTA of its dK/dV kernel skips the K/V load of its unit number
- * `kv_position`, with the same outcome.
+ * `kv_position`, with the same outcome. fa_forward_paged takes the hook in the kernel
+ * that runs chunks of new tokens; calls and kernels without such waits (single steps
+ * over the paged cache, the append, norm and rotation) spend it without effect.
  */
 void fa_test_arm_fault(int32_t kv_position);
 

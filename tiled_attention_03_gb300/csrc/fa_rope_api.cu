@@ -297,6 +297,7 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
     if (!absent_or_on(positions, dev) || !absent_or_on(rope->rotary_dim > 0 ? rope->steps : nullptr, dev) ||
         !absent_or_on(rope->q_weight, dev) || !absent_or_on(rope->k_weight, dev))
         return FA_ERR_INVALID_ARG;
+    fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
     Params p{};
     p.q = rows_of(q);
     p.k = rows_of(k);
@@ -379,6 +380,7 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
         if (there(x.r) && !fa_host::on_device(x.r->data, dev)) return FA_ERR_INVALID_ARG;
     for (const auto &x : small)
         if (!absent_or_on(x.p, dev)) return FA_ERR_INVALID_ARG;
+    fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
     Params p{};
     p.q = rows_of(xq);
     p.k = rows_of(xk);
@@ -468,6 +470,7 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     for (const auto &x : small)
         if (!absent_or_on(x.p, dev)) return FA_ERR_INVALID_ARG;
     if (!fa_host::on_device(cache->k, dev) || !fa_host::on_device(cache->v, dev)) return FA_ERR_INVALID_ARG;
+    fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
     Params p{};
     p.q = rows_of(q);
     p.k = rows_of(k);
