@@ -8,8 +8,8 @@
 //     min(page size, bn) tokens, lane c of the producer warp reads chunk c's page number
 //     and issues its TMA box; chunks that hold no key of the unit are not read. A box is
 //     five-dimensional (64 columns, 8 tokens, column region, group of 8 tokens, page and
-//     head), so that one copy brings all of a chunk's columns: the copies are issued at
-//     about one per 60 cycles, and one per chunk and region had bound pages of 16 tokens.
+//     head), so that one copy brings all of a chunk's columns: with one copy per chunk and region
+//     pages of 16 tokens took 886 us where pages of 128 took 823 (the chunk named below).
 //   * Rows of a unit are (token, head) pairs: the pf query heads of one K/V head (or
 //     a divisor of them when there are more than 128) for 128 / pf tokens, token-major
 //     in the tile, so that every K/V tile is read once for all of them, at one token
@@ -37,8 +37,8 @@
 //
 // Two warps issue the products because the tensor pipe holds only about one operation
 // ahead: a single issuer spent 1,032 cycles of a 128-key tile at d = 128 issuing and 410 in
-// its waits for P, V and K, all of them ready, with the pipe empty meanwhile and the
-// softmax waiting for scores. With two, the waits of one fall into the products of the
+// its waits for P, V and K (with clock reads in the code), while the softmax waited 498 of
+// 1,771 for scores. With two, the waits of one fall into the products of the
 // other. What one thread's issue order used to give is then a barrier: S(t) goes into the
 // TMEM buffer of P(t - 3) once the product with P(t - 3) has completed. The scores run
 // ahead by the three buffers (two at d = 256), across units as well. 2048 queries on
@@ -65,8 +65,8 @@ __host__ __device__ constexpr int bn(int D) { return D == 256 ? 64 : 128; }  // 
 constexpr int kThreads = 256;
 // A unit's start and end (its first scores, its last product, its outputs) in tiles:
 // measured 3 to 4.5 us against 0.8 us for a tile of 64 keys at d = 256 and 0.94 us for one
-// of 128 at d = 128. Shares of equal tiles alone ended between 130 and 195 us on a batch
-// of chunks and single steps.
+// of 128 at d = 128. With 2 ticks the shares of a batch of chunks and
+// single steps at d = 256 ended between 130 and 195 us.
 constexpr int kChunkTicks = 5;
 constexpr int kQKWarp = 4;
 constexpr int kScoreWarp = 5;
