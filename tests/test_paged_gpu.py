@@ -231,6 +231,29 @@ def test_page_numbers_outside_the_cache_read_as_zeros(H):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("B,T,H,Hk,width", [
+    (8192, 4096, 64, 64, 128),   # units of 16 rows, sequences searched by the block
+    (128, 128, 64, 64, 13000),   # units of 16 rows, sequences searched by a warp
+    (8192, 4096, 64, 2, 128)])   # units of 128 rows
+def test_offsets_in_no_order_write_nothing_outside(B, T, H, Hk, width):
+    """Every second sequence owns all T tokens: the work of all of them passes 2^32."""
+    d, page, guard = 32, 512, 64
+    k, v = (torch.zeros(4, page, Hk, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    cache = fa.PagedCache(k, v)
+    table = torch.arange(B * width, device=DEV).remainder(4).to(torch.int32).view(B, width)
+    cu = torch.tensor([0, T] * (B // 2) + [0], dtype=torch.int32, device=DEV)
+    lens = torch.full((B,), width * page, dtype=torch.int32, device=DEV)
+    q = torch.zeros(T, H, d, dtype=torch.bfloat16, device=DEV)
+    o = torch.full((T + 2 * guard, H, d), -777.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T + 2 * guard, H), -777.0, device=DEV)
+    fa.fa_forward_paged(q, o[guard:-guard], lse[guard:-guard], cache, table, cu, lens, 1.0, "none", 0, 0)
+    assert fa.fa_sync_status() == fa.FA_OK
+    for x in (o, lse):
+        assert bool((x[:guard] == -777.0).all()) and bool((x[-guard:] == -777.0).all())
+    q, cache, table, cu, lens, seqs = paged([(1, 90), (1, 700)], H, Hk, d, torch.bfloat16, 16, seed=3)
+    check(*run(q, cache, table, cu, lens, d ** -0.5, "causal"), seqs, d ** -0.5, "causal", (0, 0), torch.bfloat16)
+
+
 def test_lengths_are_clamped_to_the_table():
     q, cache, table, cu, lens, _ = paged([(1, 48), (1, 30)], 2, 1, 64, torch.bfloat16, 16, seed=2)
     three = table[:, :3].contiguous()

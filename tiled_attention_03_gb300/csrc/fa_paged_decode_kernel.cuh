@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
         for (int i = 0; i < kOwn; ++i) {
             w[i] = 0;
             if (i < own) w[i] = small_work<kKeys>(q[i], p);
-            sum += w[i] * p.spaces;
+            sum = add_work(sum, w[i] * p.spaces);
         }
         if (p.max_new > 0) {
             int longest = q[0].nq;
@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            if (lane >= o) incl = add_work(incl, y);
         }
         W = __shfl_sync(0xffffffffu, incl, 31);
+        if (W == kNoLine) W = 0;
         T = max((W + workers - 1) / workers, static_cast<unsigned>(p.min_ticks));
         w0 = min(worker * T, W);
         w1 = min(w0 + T, W);
@@ -238,14 +239,15 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
         for (int x = threadIdx.x; x < p.B; x += kThr) {
             const unsigned w = small_work<kKeys>(small_seq(x, p), p) * p.spaces;
             if (x < kThr) first = w;
-            mine += w;
+            mine = add_work(mine, w);
         }
-        mine = warp_sum(mine);
+        mine = warp_sum_work(mine);
         if (lane == 0) sums[warp] = mine;
         __syncthreads();
         W = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) W += sums[i];
+        for (int i = 0; i < kWarps; ++i) W = add_work(W, sums[i]);
+        if (W == kNoLine) W = 0;
         T = max((W + workers - 1) / workers, static_cast<unsigned>(p.min_ticks));
         w0 = min(worker * T, W);
         w1 = min(w0 + T, W);

@@ -273,6 +273,17 @@ __device__ __forceinline__ unsigned warp_sum(unsigned v) {
     return v;
 }
 
+// Sums of ticks stay at kNoLine once they reach it. The host admits calls whose line is
+// shorter, so only offsets that are not in ascending order, whose sequences overlap, get
+// there: such a batch is left alone, as its sums past 32 bits would give shares nowhere.
+constexpr unsigned kNoLine = 0x7fffffffu;
+__device__ __forceinline__ unsigned add_work(unsigned a, unsigned b) { return min(a + b, kNoLine); }
+__device__ __forceinline__ unsigned warp_sum_work(unsigned v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = add_work(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
 // Ticks of one head group of sequence b (every thread of the warp calls it with its own
 // b; b >= B gives 0). Long sequences, with many token tiles, are summed by the whole
 // warp one after the other.
@@ -342,14 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- this CTA's share of the line of work: ticks w0 .. w1 - 1 of W. B sequences are
     // summed, and then searched for w0, one to a thread at a time.
     auto block_sum = [&](unsigned v) -> unsigned {
-        v = warp_sum(v);
+        v = warp_sum_work(v);
         __syncthreads();
         if (lane == 0) scan[warp] = v;
         __syncthreads();
         unsigned s = 0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) s += scan[i];
-        return s;
+        for (int i = 0; i < kThreads / 32; ++i) s = add_work(s, scan[i]);
+        return s == kNoLine ? 0 : s;
     };
     if (p.min_new > 0) {
         int longest = 0;
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const unsigned w = seq_work<kBN>(b0 + static_cast<int>(threadIdx.x), p) * p.spaces;
         if (b0 == 0) first = w;
-        mine += w;
+        mine = add_work(mine, w);
     }
     const unsigned W = block_sum(mine);
     const unsigned T = (W + gridDim.x - 1) / gridDim.x;
