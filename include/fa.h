@@ -444,7 +444,8 @@ typedef struct {
  * are stored, and queries copied, as they are. q, q_out: total_q x H x d, or both with
  * data = NULL (H is then ignored); k, v: total_q x H_kv x d; of all four the descriptor's
  * `head` and `token` strides are used. q_out may be q. Rows of q_out of tokens that belong
- * to no sequence are left as they are. Two sequences that write the same slot of a page
+ * to no sequence are left as they are. K and V of the cache share no element (the same
+ * pointer for both, fine to attend over, is refused). Two sequences that write the same slot of a page
  * leave either's row there. A sequence whose first new tokens would stand before position
  * 0 (more new tokens than keys) stores only the others. One kernel launch.
  */

@@ -225,6 +225,13 @@ def test_append_refusals(lib, kw):
     assert append(lib, **kw) == INVALID
 
 
+def test_append_needs_keys_and_values_apart(lib):
+    one = cache(v=0x200000000)
+    assert one.k == one.v
+    assert append(lib, c=one) == INVALID
+    assert past_checks(attend(lib, c=one))
+
+
 def test_no_tokens_need_no_pointers(lib):
     assert attend(lib, total=0, q=None, o=None, lse=None, ws=None) == fa.FA_OK
     none = FaRows(None, 0, 0, 0)

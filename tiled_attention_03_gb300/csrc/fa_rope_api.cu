@@ -420,6 +420,7 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     size_t cache_bytes = 0;
     fa_status s = fa_host::check_cache(*cache, &cache_bytes);
     if (s != FA_OK) return s;
+    if (cache->k == cache->v) return FA_ERR_INVALID_ARG;  // a key and a value for each place
     const int64_t d = cache->d, H_kv = cache->H_kv;
     const fa_norm_rope plain{nullptr, 0, FA_ROPE_INTERLEAVED, 1.f, nullptr, nullptr, 0.f};
     const fa_norm_rope &r = rope ? *rope : plain;
