@@ -480,3 +480,39 @@ def test_no_tokens_is_a_no_op():
     o, lse = run(q, cache, table, cu, lk, 0.1, "causal")
     fa.fa_paged_append(None, q[:, :1], q[:, :1], None, cache, table, cu, lk)
     assert o.shape[0] == 0 and fa.fa_launch_count() == n
+
+
+def test_a_strided_q_on_another_stream():
+    """The copy that makes q contiguous runs on the stream of the call."""
+    q, cache, table, cu, lens, _ = paged([(1, 300), (1, 40)], 8, 2, 64, torch.bfloat16, 16, seed=4)
+    strided = torch.full((q.shape[0], 8, 128), NAN, dtype=q.dtype, device=DEV)[:, :, :64]
+    strided.copy_(q)
+    want = fa.forward_paged(q, cache, table, cu, lens)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)  # the current stream is busy for about 0.1 s
+    got = fa.forward_paged(strided, cache, table, cu, lens, stream=s)
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_a_workspace_of_another_stream_is_not_the_current_streams():
+    """Memory that the current stream has freed but still reads is no workspace of a call on
+    another stream."""
+    q, cache, table, cu, lens, _ = paged([(1, 30000)], 8, 2, 64, torch.bfloat16, 16, seed=4)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    size = fa.fa_forward_paged_workspace_bytes(64)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.full((size,), 77, dtype=torch.uint8, device=DEV)
+    y = torch.empty_like(x)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)
+    y.copy_(x)
+    del x
+    fa.fa_forward_paged(q, o, lse, cache, table, cu, lens, 0.125, "causal", stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert bool((y == 77).all())

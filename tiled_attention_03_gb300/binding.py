@@ -8,6 +8,7 @@ calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -662,15 +663,23 @@ def _int32(t: torch.Tensor | None, numel: int, what: str):
     return t.data_ptr()
 
 
+def _on(stream):
+    """The context in which `stream` is the current one. What a call allocates or copies for
+    itself belongs there: memory that the current stream has just freed may still be in
+    use on it, and a copy on it is not ordered before the kernel."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
 def _workspace(workspace, need: int, like: torch.Tensor, stream, what: str):
     """(pointer, bytes) of a caller's workspace, or of one from PyTorch's caching
-    allocator, marked as used on `stream`."""
+    allocator that belongs to `stream`."""
     if workspace is None:
-        workspace = torch.empty(max(need, 32), dtype=torch.uint8, device=like.device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
-        elif stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=like.device))
+        with _on(stream):
+            workspace = torch.empty(max(need, 32), dtype=torch.uint8, device=like.device)
     elif not workspace.is_contiguous():
         raise FaError(FA_ERR_INVALID_ARG, what)
     return workspace.data_ptr(), workspace.nbytes, workspace
@@ -697,9 +706,10 @@ def fa_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope: NormRope,
                  positions: torch.Tensor | None = None, stream=None):
-    """Queries and keys normalised and rotated, as new contiguous tensors."""
-    q_out, k_out = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                    for t in (q, k))
+    """Queries and keys normalised and rotated, as new contiguous tensors (of `stream`)."""
+    with _on(stream):
+        q_out, k_out = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                        for t in (q, k))
     fa_qk_norm_rope(q, k, q_out, k_out, rope, positions, stream)
     return q_out, k_out
 
@@ -745,12 +755,14 @@ def fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
 def qk_norm_rope_backward(q, k, dq_out, dk_out, rope: NormRope,
                           positions: torch.Tensor | None = None, stream=None):
     """(dq, dk, dq_weight, dk_weight) of qk_norm_rope for the upstream gradients of its
-    outputs; a weight's gradient is None where `rope` has no such weight."""
-    dq, dk = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-              for t in (dq_out, dk_out))
-    dw = [None if g is None or w is None else
-          torch.empty(w.shape, dtype=torch.float32, device=w.device)
-          for g, w in ((dq, rope.q_weight), (dk, rope.k_weight))]
+    outputs; a weight's gradient is None where `rope` has no such weight. The results are
+    tensors of `stream`."""
+    with _on(stream):
+        dq, dk = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                  for t in (dq_out, dk_out))
+        dw = [None if g is None or w is None else
+              torch.empty(w.shape, dtype=torch.float32, device=w.device)
+              for g, w in ((dq, rope.q_weight), (dk, rope.k_weight))]
     fa_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dw[0], dw[1], rope, positions, None, stream)
     return dq, dk, dw[0], dw[1]
 
@@ -828,10 +840,12 @@ def fa_forward_paged(q: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, cache:
 def forward_paged(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
                   cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor, scale: float | None = None,
                   mask="causal", window=(0, 0), stream=None):
-    """Attention of the new tokens q (total_q, H, d) over a paged cache: returns (O, LSE)."""
-    q = q.contiguous()
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    """Attention of the new tokens q (total_q, H, d) over a paged cache: returns (O, LSE),
+    tensors of `stream`."""
+    with _on(stream):
+        q = q.contiguous()
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     fa_forward_paged(q, o, lse, cache, block_table, cu_seqlens_q, seqlens_k,
                      q.shape[-1] ** -0.5 if scale is None else scale, mask, window[0], window[1], None,
                      stream)
