@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import tiled_attention_03_gb300 as fa
+from tiled_attention_03_gb300 import binding
 from tiled_attention_03_gb300.binding import FaNormRope, FaPagedCache, load_library
 from tiled_attention_03_gb300.build import build_library
 
@@ -253,6 +254,15 @@ def test_binding_refuses_cpu_tensors():
         fa.PagedCache(x[None], x[None])
     with pytest.raises(fa.FaError):
         fa.NormRope(torch.zeros(4, dtype=torch.int64))
+
+
+def test_an_integer_handle_names_the_stream_it_belongs_to(monkeypatch):
+    """0 (and CUDA's other name for it, 1) is the default stream, not one of PyTorch's pool."""
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert binding._on(0) == "default" and binding._on(1) == "default"
+    assert binding._on(0x7F0000001000) == ("external", 0x7F0000001000)
 
 
 # ------------------------------------------------------------------------ rotary steps

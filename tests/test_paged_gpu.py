@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import tiled_attention_03_gb300 as fa
+from tiled_attention_03_gb300 import binding
 
 from rope_util import assert_within, attention_ref, norm_rope_ref
 
@@ -516,3 +517,40 @@ def test_a_workspace_of_another_stream_is_not_the_current_streams():
     s.synchronize()
     torch.cuda.synchronize()
     assert bool((y == 77).all())
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_streams_given_by_their_handles(own):
+    """An integer handle, the default stream's 0 among them: what the call copies and allocates
+    is ordered on that stream, with another one current."""
+    q, cache, table, cu, lens, _ = paged([(1, 300), (1, 40)], 8, 2, 64, torch.bfloat16, 16, seed=4)
+    want = fa.forward_paged(q, cache, table, cu, lens)
+    rope, _ = rope_handle(64, 64, "half", torch.bfloat16, True)
+    turned = fa.qk_norm_rope(q, None, rope)[0]
+    back = fa.qk_norm_rope_backward(q, None, q, None, rope)
+    strided = torch.zeros((q.shape[0], 8, 128), dtype=q.dtype, device=DEV)[:, :, :64]
+    s = torch.cuda.Stream() if own else torch.cuda.default_stream()
+    assert own or s.cuda_stream == 0
+    with binding._on(s.cuda_stream):
+        assert torch.cuda.current_stream().cuda_stream == s.cuda_stream
+
+    def step():
+        return [*fa.forward_paged(strided, cache, table, cu, lens, stream=s.cuda_stream),
+                fa.qk_norm_rope(strided, None, rope, stream=s.cuda_stream)[0],
+                *fa.qk_norm_rope_backward(strided, None, strided, None, rope, stream=s.cuda_stream)[::2]]
+
+    strided.copy_(q)
+    for _ in range(40):  # nothing below is a first use, which would wait for the busy stream
+        step()
+    strided.fill_(NAN)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s before q is there
+        strided.copy_(q)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = step()
+    with torch.cuda.stream(s):  # the results are tensors of s
+        got = [x.clone() for x in got]
+    torch.cuda.synchronize()
+    for a, b in zip(got, [*want, turned, back[0], back[2]]):
+        assert torch.equal(a, b)

@@ -670,7 +670,10 @@ def _on(stream):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # 0 and 1 are the default stream's handles; an ExternalStream of either would be some
+        # stream of PyTorch's pool
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 
