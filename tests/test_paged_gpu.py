@@ -2,6 +2,7 @@
 bits. Everything that the calls must not look at (slots past a sequence's end, pages that
 belong to nobody, table entries past a sequence) holds NaN or nonsense."""
 
+import ctypes
 import math
 import random
 
@@ -344,6 +345,26 @@ def test_append_without_queries_or_rope_copies():
     for b, pos, t in ((0, 17, 0), (0, 18, 1), (0, 19, 2), (1, 32, 3)):
         at = int(table[b, pos // 16]), pos % 16
         assert torch.equal(cache.k[at], kv[t, :2]) and torch.equal(cache.v[at], kv[t, 2:])
+
+
+@pytest.mark.parametrize("any_stride", [-8, 5, -2 ** 62])
+def test_append_of_one_head_and_one_token_by_any_strides(any_stride):
+    """Strides of dimensions of one entry, in the rows and in the cache, are not looked at."""
+    d, page = 64, 16
+    lib = binding.load_library()
+    x = torch.randn(3, 1, d, device=DEV).to(torch.bfloat16)
+    k, v = (torch.full((1, page, 1, d), NAN, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    c = binding.FaPagedCache(k.data_ptr(), v.data_ptr(), any_stride, d, any_stride, 1, page, 1, d, 1)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([7], dtype=torch.int32, device=DEV)
+    q = torch.full((1, 1, d), NAN, dtype=torch.bfloat16, device=DEV)
+    rows = lambda t: binding._pack_rows(t.data_ptr(), any_stride, any_stride, any_stride)  # noqa: E731
+    assert lib.fa_paged_append(rows(x[0]), rows(x[1]), rows(x[2]), rows(q), ctypes.addressof(c), table.data_ptr(), 1,
+                               cu.data_ptr(), lens.data_ptr(), 1, 1, 1, None, None) == fa.FA_OK
+    assert fa.fa_sync_status() == fa.FA_OK
+    assert torch.equal(q[0], x[0]) and torch.equal(k[0, 6], x[1]) and torch.equal(v[0, 6], x[2])
+    assert int(torch.isnan(k).sum()) == int(torch.isnan(v).sum()) == (page - 1) * d
 
 
 def test_append_skips_pages_outside_the_cache():

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import tiled_attention_03_gb300 as fa
+from tiled_attention_03_gb300 import binding
 
 from rope_util import assert_within, norm_rope_bwd_ref, norm_rope_ref, rotate
 
@@ -86,6 +87,35 @@ def test_in_place_and_into_a_fused_buffer():
     fa.fa_qk_norm_rope(x[:, :H], x[:, H:], wide[:, :H], wide[:, H + 1:2 * H + 1], rope)
     assert torch.equal(wide[:, :H], want[0]) and torch.equal(wide[:, H + 1:2 * H + 1], want[1])
     assert bool((wide[:, H] == -777.0).all()) and bool((wide[:, 2 * H + 1:] == -777.0).all())
+
+
+@pytest.mark.parametrize("any_stride", [-8, 5, -2 ** 62])
+@pytest.mark.parametrize("B,H,Hk,N", [(2, 1, 3, 37), (2, 3, 1, 37), (1, 1, 1, 1), (1, 5, 2, 40), (3, 4, 1, 1)])
+def test_strides_of_single_entries_do_not_matter(B, H, Hk, N, any_stride):
+    """Through the C ABI (PyTorch makes no such strides): the same bits as with strides of 0."""
+    dtype, d = torch.bfloat16, 128
+    rope, _ = handle(d, d, "half", dtype)
+    lib = binding.load_library()
+
+    def step(single):
+        x, g = ([make((B, h, N, d), dtype, 40 + 2 * i + j) for j, h in enumerate((H, Hk))] for i in range(2))
+        y, dx = ([torch.full_like(t, math.nan) for t in x] for _ in range(2))
+        dw = [torch.full((d,), math.nan, device=DEV) for _ in range(2)]
+        ws = torch.empty(fa.fa_qk_norm_rope_backward_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+
+        def rows(t):
+            s = [st if n > 1 else single for st, n in zip(t.stride()[:3], t.shape)]
+            return binding._pack_rows(t.data_ptr(), *s)
+
+        assert lib.fa_qk_norm_rope(*map(rows, x + y), rope.address, None, B, H, Hk, N, d, 1, None) == fa.FA_OK
+        assert lib.fa_qk_norm_rope_backward(
+            *map(rows, x + g + dx), dw[0].data_ptr(), dw[1].data_ptr(), rope.address, None, B, H, Hk, N, d, 1,
+            ws.data_ptr(), ws.numel(), None) == fa.FA_OK
+        assert fa.fa_sync_status() == fa.FA_OK
+        return y + dx + dw
+
+    for a, b in zip(step(any_stride), step(0)):
+        assert bool(torch.isfinite(b).all()) and torch.equal(a, b)
 
 
 def test_far_positions_keep_their_phase():

@@ -146,9 +146,12 @@ fa_status device_of(int *dev, fa_host::DeviceInfo *di) {
 
 bool absent_or_on(const void *p, int dev) { return p == nullptr || fa_host::on_device(p, dev); }
 
-Rows rows_of(const fa_rows *r) {
+// The stride of a dimension of one entry may be anything: 0 here, so that the kernels see
+// none below 0.
+Rows rows_of(const fa_rows *r, int64_t B, int64_t heads, int64_t N) {
     if (!there(r)) return Rows{nullptr, 0, 0, 0};
-    return Rows{static_cast<uint16_t *>(r->data), r->batch, r->head, r->token};
+    return Rows{static_cast<uint16_t *>(r->data), B > 1 ? r->batch : 0, heads > 1 ? r->head : 0,
+                N > 1 ? r->token : 0};
 }
 
 void set_rope(Params &p, const fa_norm_rope &r) {
@@ -299,10 +302,10 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
         return FA_ERR_INVALID_ARG;
     fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
     Params p{};
-    p.q = rows_of(q);
-    p.k = rows_of(k);
-    p.q_out = rows_of(q_out);
-    p.k_out = rows_of(k_out);
+    p.q = rows_of(q, B, H, N);
+    p.k = rows_of(k, B, H_kv, N);
+    p.q_out = rows_of(q_out, B, H, N);
+    p.k_out = rows_of(k_out, B, H_kv, N);
     p.H = static_cast<int>(H);
     p.H_kv = static_cast<int>(H_kv);
     p.N = static_cast<int>(N);
@@ -382,12 +385,12 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
         if (!absent_or_on(x.p, dev)) return FA_ERR_INVALID_ARG;
     fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
     Params p{};
-    p.q = rows_of(xq);
-    p.k = rows_of(xk);
-    p.q_out = rows_of(dq_out);
-    p.k_out = rows_of(dk_out);
-    p.dq = rows_of(dq);
-    p.dk = rows_of(dk);
+    p.q = rows_of(xq, B, H, N);
+    p.k = rows_of(xk, B, H_kv, N);
+    p.q_out = rows_of(dq_out, B, H, N);
+    p.k_out = rows_of(dk_out, B, H_kv, N);
+    p.dq = rows_of(dq, B, H, N);
+    p.dk = rows_of(dk, B, H_kv, N);
     p.H = static_cast<int>(H);
     p.H_kv = static_cast<int>(H_kv);
     p.N = static_cast<int>(N);
@@ -473,10 +476,10 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     if (!fa_host::on_device(cache->k, dev) || !fa_host::on_device(cache->v, dev)) return FA_ERR_INVALID_ARG;
     fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
     Params p{};
-    p.q = rows_of(q);
-    p.k = rows_of(k);
-    p.v = rows_of(v);
-    p.q_out = rows_of(q_out);
+    p.q = rows_of(q, 1, H, total_q);
+    p.k = rows_of(k, 1, H_kv, total_q);
+    p.v = rows_of(v, 1, H_kv, total_q);
+    p.q_out = rows_of(q_out, 1, H, total_q);
     p.H = static_cast<int>(H);
     p.H_kv = p.H_v = static_cast<int>(H_kv);
     p.N = static_cast<int>(total_q);

@@ -42,7 +42,7 @@ constexpr int kMaxPairs = 128;  // d / 2
 constexpr int kDepth = 4;       // stages of the ring (kDepth - 1 in flight)
 constexpr int kRows = 2;        // rows per group and stage, forward
 
-// A (batch, head, token, d) tensor of 16-bit elements; null: not there.
+// A (batch, head, token, d) tensor of 16-bit elements, strides >= 0; null: not there.
 struct Rows {
     uint16_t *p;
     long long batch, head, token;
