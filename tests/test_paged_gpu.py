@@ -347,6 +347,23 @@ def test_append_without_queries_or_rope_copies():
         assert torch.equal(cache.k[at], kv[t, :2]) and torch.equal(cache.v[at], kv[t, 2:])
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rope", [False, True])
+def test_append_without_norm_and_rotation_keeps_the_bits(rope, dtype):
+    """Every 16-bit pattern, the zero below 0 and each NaN among them, with rope = NULL and with
+    one that does nothing."""
+    d, n, page = 64, 2 ** 16 // 256, 16
+    x = torch.arange(-2 ** 15, 2 ** 15, device=DEV).to(torch.int16).view(n, 4, d).view(dtype)
+    k, v = (torch.zeros(n // page, page, 4, d, dtype=dtype, device=DEV) for _ in range(2))
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV)[None]
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    q = torch.zeros_like(x)
+    fa.fa_paged_append(x, x, x, q, fa.PagedCache(k, v), table, cu, cu[1:], fa.NormRope() if rope else None)
+    assert fa.fa_sync_status() == fa.FA_OK
+    for y in (q, k.view(n, 4, d), v.view(n, 4, d)):
+        assert torch.equal(y.view(torch.int16), x.view(torch.int16))
+
+
 @pytest.mark.parametrize("any_stride", [-8, 5, -2 ** 62])
 def test_append_of_one_head_and_one_token_by_any_strides(any_stride):
     """Strides of dimensions of one entry, in the rows and in the cache, are not looked at."""

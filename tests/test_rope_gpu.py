@@ -118,6 +118,22 @@ def test_strides_of_single_entries_do_not_matter(B, H, Hk, N, any_stride):
         assert bool(torch.isfinite(b).all()) and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("r", [0, 32])
+def test_elements_without_norm_and_rotation_stay(r, layout, dtype):
+    """Every 16-bit value, the zero below 0 among them; a NaN stays one."""
+    d = 64
+    x = torch.arange(-2 ** 15, 2 ** 15, device=DEV).flip(0).to(torch.int16).view(-1, 4, d).view(dtype)
+    assert bool((x[..., 32:].view(torch.int16) == -2 ** 15).any())
+    rope, _ = handle(d, r, layout, dtype, True, False)
+    for y in (*fa.qk_norm_rope(x, x, rope)[1:], fa.qk_norm_rope(None, x, rope)[1]):
+        x0, y0 = x[..., r:], y[..., r:]
+        nan = torch.isnan(x0)
+        assert bool(torch.isnan(y0[nan]).all())
+        assert torch.equal(y0.contiguous().view(torch.int16)[~nan], x0.contiguous().view(torch.int16)[~nan])
+
+
 def test_far_positions_keep_their_phase():
     """The whole range of int32 positions: a frequency of 1 wraps 340 million times."""
     d, dtype = 64, torch.float16

@@ -183,7 +183,8 @@ __device__ __forceinline__ void angles(float (&cs)[2][kMaxPairs], const Params &
 }
 
 // Coefficients of elements 8 l + e: C the cosine, S the sine of the partner (negative in
-// the first element of a pair); C = 1, S = 0 past the rotated ones.
+// the first element of a pair); C = 1, S = -0 past the rotated ones (0 x -0 added leaves
+// the sign of a zero as it is).
 template <int MODE>
 __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], int half_r, int l,
                                              f2 (&C)[4], f2 (&S)[4]) {
@@ -192,7 +193,7 @@ __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], in
         const int j = first ? 8 * l : 8 * l - half_r;
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(-0.f, -0.f, -0.f, -0.f);
             const float4 c = rotated ? *reinterpret_cast<const float4 *>(&cs[0][j + 2 * e]) : one;
             const float4 s = rotated ? *reinterpret_cast<const float4 *>(&cs[1][j + 2 * e]) : zero;
             const f2 sign = both(first ? -1.f : 1.f);
@@ -207,7 +208,7 @@ __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], in
             for (int x = 0; x < 2; ++x) {
                 const int i = 8 * l + 2 * e + x;
                 c[x] = 1.f;
-                t[x] = 0.f;
+                t[x] = -0.f;
                 if (i < 2 * half_r) {
                     const bool first = MODE == kBeside ? x == 0 : i < half_r;
                     const int j = MODE == kBeside ? i >> 1 : (first ? i : i - half_r);
@@ -475,8 +476,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
             const Run run = run_of<kStageHeads>(p, s, at.end);
             s += run.stages;
             const uint16_t *w = run.kind == 0 ? p.wq : p.wk;
+            // values, and rows neither normalised nor rotated, go through bit by bit (in the
+            // append alone: the dense forward of 16,384 x 64 rows took 88.5 us with it, 87.7 without)
+            const bool as_is = PAGED && (run.kind == 2 || (w == nullptr && p.half_r == 0));
             f2 A[4], Bc[4];
-            if (!PAGED || run.kind < 2) {
+            if (!as_is) {
                 f2 wt[4];
                 coefficients<MODE>(cs, p.half_r, l, A, Bc);
                 weights<BF16>(w, l, wt);
@@ -508,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
                 const uint4(&stage)[U][32] = ring[warp][slot];
                 slot = (slot + 1) % kDepth;
                 uint4 out[U];
-                if (PAGED && run.kind == 2) {
+                if (as_is) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) out[u] = stage[u][lane];
                 } else {
-f2 y[U][4], yp[U][4], r = both(1.f);
+                    f2 y[U][4], yp[U][4], r = both(1.f);
 #pragma unroll
                     for (int u = 0; u < U; ++u)
                         read_row<D, BF16, MODE>(&stage[u][lane], p.half_r, l, partner_l, y[u], yp[u]);
