@@ -470,8 +470,8 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
  * workspace: caller-owned device memory of at least
  * fa_forward_paged_workspace_bytes(d) bytes, 32-byte aligned, scratch: its contents on
  * entry do not matter. It does not depend on the batch. Calls that may overlap on the
- * GPU need a workspace each. Two kernel launches, or three. The results are the same every time
- * on one device. Alignment of Q, O, LSE and errors as fa_forward; the arrays of the
+ * GPU need a workspace each. Two kernel launches. The results are the same every time on
+ * one device. Alignment of Q, O, LSE and errors as fa_forward; the arrays of the
  * batch are 4-byte aligned. total_q = 0 returns FA_OK with nothing enqueued.
  */
 fa_status fa_forward_paged(const void *Q, void *O, float *LSE, const fa_paged_cache *cache,

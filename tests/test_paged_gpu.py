@@ -163,6 +163,22 @@ def test_few_tokens_per_sequence(d, kind, B):
     check(o, lse, b[5], 0.1, "causal", (0, 0), torch.bfloat16)
 
 
+@pytest.mark.parametrize("B", [40, 128, 200])
+@pytest.mark.parametrize("chunks", [1, 2])
+@pytest.mark.parametrize("d,H,Hk", [(32, 8, 2), (64, 4, 4), (128, 8, 1), (256, 4, 2)])
+def test_a_chunk_among_empty_sequences(d, H, Hk, chunks, B):
+    """No more tokens than sequences, and most sequences without any: a captured step of fixed
+    size. As many single tokens as sequences beside it."""
+    lens = [(0, n) for n in [0, 50] * (B // 2)]
+    lens[B // 3] = (B - chunks + 1, B + 1500)
+    if chunks == 2:
+        lens[-1] = (1, 700)
+    b = paged(lens, H, Hk, d, torch.bfloat16, 16, seed=B)
+    check(*run(*b[:5], 0.1, "causal"), b[5], 0.1, "causal", (0, 0), torch.bfloat16)
+    b = paged([(1, 1 + 7 * i % 500) for i in range(B)], H, Hk, d, torch.bfloat16, 16, seed=B)
+    check(*run(*b[:5], 0.1, "causal"), b[5], 0.1, "causal", (0, 0), torch.bfloat16)
+
+
 def test_a_workspace_passed_on():
     """One workspace, used by batches of all kinds in turn: what a call leaves there means
     nothing to the next (each is larger than the one before)."""

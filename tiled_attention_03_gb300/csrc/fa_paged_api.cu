@@ -28,15 +28,22 @@ struct Configured {
 };
 Configured g_configured[kMaxDevices];
 
+// Shared memory of the kernel that holds both bodies.
+template <int D>
+constexpr int kEitherSmem = fa::paged::Smem<D>::kAlloc > fa::paged::Small<D>::kBytes ? fa::paged::Smem<D>::kAlloc
+                                                                                     : fa::paged::Small<D>::kBytes;
+
 template <int D, bool BF16>
 cudaError_t opt_in() {
-    const cudaError_t e = cudaFuncSetAttribute(fa::paged::fa_paged_kernel<D, BF16>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               fa::paged::Smem<D>::kAlloc);
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(fa::paged::fa_paged_decode_kernel<D, BF16>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   fa::paged::Small<D>::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(fa::paged::fa_paged_kernel<D, BF16>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, fa::paged::Smem<D>::kAlloc);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa::paged::fa_paged_decode_kernel<D, BF16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, fa::paged::Small<D>::kBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fa::paged::fa_paged_either_kernel<D, BF16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kEitherSmem<D>);
+    return e;
 }
 
 bool configured(int dev) {
@@ -71,9 +78,12 @@ Layout layout_of(int64_t d, int64_t sms) {
     return l;
 }
 
-// What a call runs: one of the kernels, or both (see fa_paged_decode_kernel.cuh), and the merge.
+// What a call runs: decode, chunks, or whichever the device finds (see
+// fa_paged_decode_kernel.cuh); and the merge.
 struct Plan {
     bool decode, chunk;
+    int max_new;
+    unsigned merge_rows;  // blocks of the merge per decode unit
     fa::paged::SmallParams small;
     fa::paged::Params p;
     fa::paged::MergeParams merge;
@@ -83,24 +93,20 @@ struct Plan {
 
 template <int D, bool BF16>
 cudaError_t launch(const Plan &x, cudaStream_t st) {
-    using S = fa::paged::Small<D>;
-    if (x.decode) {
-        const cudaError_t e = fa::launch_after(fa::paged::fa_paged_decode_kernel<D, BF16>, dim3(x.sms),
-                                               S::kWarps * 32, S::kBytes, st, x.small);
-        if (e != cudaSuccess) return e;
-    }
-    if (x.chunk) {
-        fa::paged::Params p = x.p;
-        p.infos = S::kWarps;
-        const cudaError_t e = fa::launch_after(fa::paged::fa_paged_kernel<D, BF16>, dim3(x.sms),
-                                               fa::paged::kThreads, fa::paged::Smem<D>::kAlloc, st, x.q,
-                                               x.k, x.v, p);
-        if (e != cudaSuccess) return e;
-    }
+    using namespace fa::paged;
+    using S = Small<D>;
+    fa::paged::Params p = x.p;
+    p.infos = x.decode ? S::kWarps : 1;
+    const cudaError_t e =
+        !x.chunk ? fa::launch_after(fa_paged_decode_kernel<D, BF16>, dim3(x.sms), S::kWarps * 32, S::kBytes, st, x.small)
+        : !x.decode
+            ? fa::launch_after(fa_paged_kernel<D, BF16>, dim3(x.sms), kThreads, Smem<D>::kAlloc, st, x.q, x.k, x.v, p)
+            : fa::launch_after(fa_paged_either_kernel<D, BF16>, dim3(x.sms), kThreads, kEitherSmem<D>, st, x.q, x.k, x.v,
+                               x.small, p, x.max_new);
+    if (e != cudaSuccess) return e;
     // a block per worker; a unit of the chunk kernel has 128 rows to share among several
-    const dim3 grid(x.decode ? x.sms * S::kWarps : x.sms, !x.chunk ? 1 : x.decode ? 4 : 16);
-    return fa::launch_after(fa::paged::fa_paged_merge_kernel<D, BF16>, grid, fa::paged::kMergeWarps * 32, 0,
-                            st, x.merge);
+    const dim3 grid(x.decode ? x.sms * S::kWarps : x.sms, !x.chunk ? 1 : x.decode ? x.merge_rows : 16);
+    return fa::launch_after(fa_paged_merge_kernel<D, BF16>, grid, kMergeWarps * 32, 0, st, x.merge);
 }
 
 int sm_count_or_default() {
@@ -137,14 +143,14 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     int64_t pf = group;
     if (pf > fa::paged::kBM)
         for (pf = fa::paged::kBM; group % pf != 0;) --pf;
-    // Steps, of no more tokens than sequences (or too few for a long one): the decode
-    // kernel. A few tokens per sequence on average: whichever kernel suits the longest, as
-    // it turns out on the device; its units re-read a sequence's keys kMaxReads times at most.
+    // Few tokens: the decode kernel, whose units re-read a sequence's keys kMaxReads times at
+    // most. A few tokens per sequence on average: whichever kernel suits the longest, as it
+    // turns out on the device (with no more tokens than sequences, too: most may have none).
     constexpr int64_t kMaxReads = 2;
     const bool small = pf <= fa::paged::kSmallRows;
     const int64_t tpt_small = small ? fa::paged::kSmallRows / pf : 0, tpt = fa::paged::kBM / pf;
     const int64_t max_new = kMaxReads * tpt_small;
-    const bool steps_only = small && (total_q <= B || total_q <= max_new);
+    const bool steps_only = small && total_q <= max_new;
     const bool either = small && !steps_only && total_q <= B * tpt_small;
     const bool decode = steps_only || either, chunked = !steps_only;
     const int64_t spaces = H / pf;
@@ -215,6 +221,8 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     Plan x{};
     x.decode = decode;
     x.chunk = chunked;
+    x.max_new = static_cast<int>(max_new);
+    x.merge_rows = total_q <= B ? 1 : 4;
     x.sms = static_cast<unsigned>(di.sm_count);
     fa::paged::MergeInfo *info = reinterpret_cast<fa::paged::MergeInfo *>(ws);
     float *part_LSE = reinterpret_cast<float *>(ws + lay.lse), *part_O = reinterpret_cast<float *>(ws + lay.o);
@@ -225,6 +233,7 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
     x.merge.LSE = LSE;
     x.merge.H = static_cast<int>(H);
     x.merge.pf = static_cast<int>(pf);
+    x.merge.ctas = either ? di.sm_count : 0;
     const int fault = fa_host::take_fault_position();  // the decode kernel has no wait to run out
     // what both kernels' parameters have alike
     auto common = [&](auto &p) {
@@ -261,7 +270,6 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         p.head_stride = cache->head_stride;
         p.tpt = static_cast<int>(tpt_small);
         p.min_ticks = kMinTicks;
-        p.max_new = either ? static_cast<int>(max_new) : 0;
     }
     if (chunked) {
         fa::paged::Params &p = x.p;
@@ -283,7 +291,6 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         p.wait_budget_ns = fa_host::wait_budget();
         p.status = di.status;
         p.fault_skip_k = fault;
-        p.min_new = either ? static_cast<int>(max_new + 1) : 0;
     }
     cudaError_t e;
     switch (d) {
@@ -293,7 +300,7 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         default: e = bf16 ? launch<256, true>(x, st) : launch<256, false>(x, st); break;
     }
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    fa_host::count_launches(either ? 3 : 2);
+    fa_host::count_launches(2);
     return FA_OK;
 }
 

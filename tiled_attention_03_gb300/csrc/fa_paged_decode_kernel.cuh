@@ -14,11 +14,14 @@
 // tiles (its start and end cost that much), and worker w takes ticks w T .. w T + T - 1. A unit
 // that several workers share is joined by fa_paged_merge_kernel.
 //
-// Which of the two kernels a batch is for depends on its longest sequence, which only the
-// device knows: many rows of one sequence in units of 16 read its keys again and again. With
-// no more tokens than sequences the decode kernel takes the batch; with a few per
-// sequence on average both are launched and look for a sequence of more than max_new
-// tokens, and one of them returns at once.
+// Which of the two a batch is for depends on its longest sequence, which only the device
+// knows: many rows of one sequence in units of 16 read its keys again and again. A batch of
+// no more than max_new tokens goes to the decode kernel. With a few per sequence on average (or
+// one, or less: most sequences of a batch of fixed size may have none) one kernel holds both
+// bodies and takes the chunks' if a sequence has more than max_new new tokens. 256 tokens of one of
+// 256 sequences, on 30000 keys, take 120 us so, and 718 in units of 16 rows; 64 sequences of 100
+// keys with a token each 13.6 us, 13.2 with the decode kernel alone, and 15.1 with two
+// launches, one of which returns at once.
 //
 // Measured with the merge, in a graph: 8 x 32768 keys, 32 / 8 heads, d 128: 162 us (6.6 TB/s);
 // 128 ragged sequences, window 4096, 16 / 4 heads, d 64: 33.5 us (4.6 TB/s; the tcgen05 tile
@@ -115,10 +118,9 @@ struct SmallParams {
     int wl, wr;
     float scale_log2;
     int min_ticks;
-    int max_new;  // > 0: leave the batch to the chunk kernel if a sequence has more new tokens
 };
 
-// Ticks of one head group of sequence b: its units' tiles and kUnitTicks each.
+// K/V tiles of a unit (token tile qb of a sequence), from tile j0 on, and its keys lo .. hi.
 template <int kKeys>
 __device__ __forceinline__ int small_unit(const Seq &s, int qb, const SmallParams &p, int &lo, int &hi,
                                           int &j0) {
@@ -140,6 +142,7 @@ __device__ __forceinline__ Seq small_seq(int b, const SmallParams &p) {
 __device__ __forceinline__ int small_units(const Seq &s, const SmallParams &p) {
     return s.nq <= p.tpt ? min(s.nq, 1) : (s.nq + p.tpt - 1) / p.tpt;
 }
+// Ticks of one head group of a sequence: its units' tiles and kUnitTicks each.
 template <int kKeys>
 __device__ __forceinline__ unsigned small_work(const Seq &s, const SmallParams &p) {
     const int nqb = small_units(s, p);
@@ -151,11 +154,12 @@ __device__ __forceinline__ unsigned small_work(const Seq &s, const SmallParams &
     return w;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kernel(const SmallParams p) {
+// A CTA of the decode kernel: the shares of its first kWarps warps. EITHER: false, with nothing
+// done, if a sequence has more than max_new new tokens (for every warp of the block alike).
+template <int D, bool BF16, bool EITHER>
+__device__ __forceinline__ bool decode_cta(const SmallParams &p, uint8_t *small_smem, int max_new) {
     using L = Small<D>;
     constexpr int kKeys = L::kKeys, kWarps = L::kWarps, kThr = kWarps * 32;
-    extern __shared__ __align__(1024) uint8_t small_smem[];
     unsigned *pre = reinterpret_cast<unsigned *>(small_smem + L::kScan);
     unsigned *wrk = pre + 256;
     unsigned *sums = wrk + 256;
@@ -164,8 +168,6 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
     // neighbouring shares on different SMs: few shares still use all of them
     const unsigned worker = warp * gridDim.x + blockIdx.x;
     const unsigned workers = kWarps * gridDim.x;
-    after_previous();
-    let_next_start();
 
     // ---- this warp's share: ticks w0 .. w1 - 1 of W, and the sequence b that holds w0, `off`
     // ticks into it. Up to 128 sequences every warp finds its own, one to four to a lane,
@@ -183,17 +185,18 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
             q[i] = Seq{0, 0, 0};
             if (i < own && own * lane + i < p.B) q[i] = small_seq(own * lane + i, p);
         }
+        if constexpr (EITHER) {
+            int longest = q[0].nq;
+#pragma unroll
+            for (int i = 1; i < kOwn; ++i) longest = max(longest, q[i].nq);
+            if (__any_sync(0xffffffffu, longest > max_new)) return false;
+            if (warp >= kWarps) return true;
+        }
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
             w[i] = 0;
             if (i < own) w[i] = small_work<kKeys>(q[i], p);
             sum = add_work(sum, w[i] * p.spaces);
-        }
-        if (p.max_new > 0) {
-            int longest = q[0].nq;
-#pragma unroll
-            for (int i = 1; i < kOwn; ++i) longest = max(longest, q[i].nq);
-            if (__any_sync(0xffffffffu, longest > p.max_new)) return;
         }
         unsigned incl = sum;
 #pragma unroll
@@ -231,19 +234,26 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
         }
     } else {
         unsigned mine = 0, first = 0, carry = 0;
-        if (p.max_new > 0) {
-            int longest = 0;
-            for (int x = threadIdx.x; x < p.B; x += kThr) longest = max(longest, small_seq(x, p).nq);
-            if (__syncthreads_or(longest > p.max_new)) return;
-        }
-        for (int x = threadIdx.x; x < p.B; x += kThr) {
-            const unsigned w = small_work<kKeys>(small_seq(x, p), p) * p.spaces;
+        bool longer = false;
+        for (int x = threadIdx.x; x < p.B && (!EITHER || warp < kWarps); x += kThr) {
+            const Seq q = small_seq(x, p);
+            if (EITHER && q.nq > max_new) {
+                longer = true;
+                break;
+            }
+            const unsigned w = small_work<kKeys>(q, p) * p.spaces;
             if (x < kThr) first = w;
             mine = add_work(mine, w);
         }
+        __syncwarp();
         mine = warp_sum_work(mine);
-        if (lane == 0) sums[warp] = mine;
-        __syncthreads();
+        if (lane == 0 && warp < kWarps) sums[warp] = mine;
+        if constexpr (EITHER) {
+            if (__syncthreads_or(longer)) return false;
+            if (warp >= kWarps) return true;
+        } else {
+            __syncthreads();
+        }
         W = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) W = add_work(W, sums[i]);
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
     info.last_cta = -1;
     if (b < 0) {
         if (lane == 0) p.info[worker] = info;
-        return;
+        return true;
     }
 
     int nqb = small_units(s, p), qb = 0, sp;
@@ -575,6 +585,28 @@ __global__ void __launch_bounds__(Small<D>::kWarps * 32, 1) fa_paged_decode_kern
         }
     }
     if (lane == 0) p.info[worker] = info;
+    return true;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Small<D>::kWarps * 32, 1)
+    fa_paged_decode_kernel(const __grid_constant__ SmallParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    after_previous();
+    let_next_start();
+    decode_cta<D, BF16, false>(p, smem_raw, 0);
+}
+
+// Decode or chunks (see above), by the longest sequence.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_paged_either_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ SmallParams s,
+                           const __grid_constant__ Params p, int max_new) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    after_previous();
+    let_next_start();
+    if (!decode_cta<D, BF16, true>(s, smem_raw, max_new)) chunk_cta<D, BF16>(tmQ, tmK, tmV, p, smem_raw);
 }
 
 }  // namespace paged

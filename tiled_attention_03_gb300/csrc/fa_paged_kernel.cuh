@@ -130,10 +130,7 @@ struct Params {
     unsigned long long wait_budget_ns;
     unsigned int *status;
     int fault_skip_k;  // test hook: every CTA skips the K load at this ring position (-1: none)
-    // Where the decode kernel was launched before (min_new > 0): leave the batch to it
-    // unless a sequence has at least min_new new tokens. info then has `infos` entries
-    // per CTA, all to be written.
-    int min_new, infos;
+    int infos;  // entries of info per CTA, all to be written (more than one: what the decode body has)
 };
 
 // Tiles are stored as regions of min(D, 64) columns with the swizzle of that row width. Q: region
@@ -311,10 +308,10 @@ __device__ __forceinline__ unsigned seq_work(int b, const Params &p) {
     return w;
 }
 
+// A CTA of the kernel.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
-    fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const Params p) {
+__device__ __forceinline__ void chunk_cta(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                          const Params &p, uint8_t *smem_raw) {
     using L = Smem<D>;
     constexpr int kBN = bn(D);
     constexpr uint32_t kTmemO = tmem_o(D);
@@ -327,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       : kSB * kBN <= static_cast<int>(kTmemO),
                   "TMEM columns");
     static_assert(kTmemO + D <= kTmemCols, "TMEM columns");
-    extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -347,8 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint64_t budget = p.wait_budget_ns;
-    after_previous();
-    let_next_start();
 
     // ---- this CTA's share of the line of work: ticks w0 .. w1 - 1 of W. B sequences are
     // summed, and then searched for w0, one to a thread at a time.
@@ -362,13 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kThreads / 32; ++i) s = add_work(s, scan[i]);
         return s == kNoLine ? 0 : s;
     };
-    if (p.min_new > 0) {
-        int longest = 0;
-        for (int b = threadIdx.x; b < p.B; b += kThreads) longest = max(longest, load_seq(b, p).nq);
-        if (!__syncthreads_or(longest >= p.min_new)) return;
-        for (int i = 1 + threadIdx.x; i < p.infos; i += kThreads)
-            p.info[i * gridDim.x + blockIdx.x].last_cta = -1;
-    }
+    for (int i = 1 + threadIdx.x; i < p.infos; i += kThreads)
+        p.info[i * gridDim.x + blockIdx.x].last_cta = -1;
     unsigned mine = 0, first = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const unsigned w = seq_work<kBN>(b0 + static_cast<int>(threadIdx.x), p) * p.spaces;
@@ -1057,6 +1046,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    after_previous();
+    let_next_start();
+    chunk_cta<D, BF16>(tmQ, tmK, tmV, p, smem_raw);
+}
+
 // Joins the pieces of the cut units, block c the unit that starts in worker c's share: with O_s, LSE_s of piece s
 //     LSE = ln sum_s exp(LSE_s)          O = sum_s exp(LSE_s - LSE) O_s
 // around the largest LSE_s (blockIdx.y shares a unit's rows). A row is summed by one warp, or
@@ -1071,6 +1070,7 @@ struct MergeParams {
     void *O;
     float *LSE;
     int H, pf;
+    int ctas;  // > 0: either body's pieces, a block per decode worker; the chunk body had this many CTAs
 };
 
 constexpr int kMergeWarps = 8;
@@ -1084,16 +1084,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
     __shared__ float red_m[kMergeWarps], red_w[kMergeWarps];
     after_previous();
     let_next_start();
-    const int c = blockIdx.x;
-    const MergeInfo u = p.info[c];
+    int c = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
+    MergeInfo u = p.info[c];
+    if (p.ctas > 0) {
+        // a unit of the chunk body is shared by every p.ctas-th block
+        const MergeInfo chunk = p.info[c % p.ctas];
+        if (chunk.last_cta >= 0 && chunk.slot_rows == kBM) {
+            u = chunk;
+            part += c / p.ctas * parts;
+            parts *= gridDim.x / p.ctas;
+            c %= p.ctas;
+        }
+    }
     if (u.last_cta < 0) return;
     const int n = u.last_cta - c + 1;
     int ways = 1;  // warps per row
     while (ways < kMergeWarps && u.rows * ways * 2 <= kMergeWarps) ways *= 2;
     const int per = (n + ways - 1) / ways, run = warp % ways;
     const int s_lo = min(run * per, n), s_hi = min(s_lo + per, n);
-    for (int row0 = blockIdx.y * (kMergeWarps / ways); row0 < u.rows;
-         row0 += gridDim.y * (kMergeWarps / ways)) {
+    for (int row0 = part * (kMergeWarps / ways); row0 < u.rows; row0 += parts * (kMergeWarps / ways)) {
         const int row = row0 + warp / ways;
         const bool there = row < u.rows;
         auto prow = [&](int s) {
