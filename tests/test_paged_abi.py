@@ -198,6 +198,18 @@ def test_unsupported_caches(lib, kw):
     assert append(lib, c=cache(**kw)) == UNSUPPORTED
 
 
+def test_a_cache_of_too_many_steps_is_refused_by_every_call(lib):
+    """The page and head strides' greatest common divisor is 8: 257 steps a page, and 8 a head. The
+    limit does not depend on the kernel that a call would run."""
+    strides = dict(page_stride=16 * 2 * 64 + 8)
+    below, above = cache(num_pages=(2 ** 31 - 1 - 16) // 257, **strides), cache(num_pages=2 ** 31 // 257 + 1, **strides)
+    for total in (3, 500):
+        assert attend(lib, c=above, total=total) == UNSUPPORTED
+    assert append(lib, c=above) == UNSUPPORTED
+    if not torch.cuda.is_available():
+        assert attend(lib, c=below) == fa.FA_ERR_CUDA and append(lib, c=below) == fa.FA_ERR_CUDA
+
+
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(o=None), dict(lse=None), dict(table=None), dict(cu=None), dict(lens=None), dict(ws=None),
     dict(B=0), dict(H=0), dict(H=5), dict(total=-1), dict(pages=-1), dict(scale=0.0), dict(scale=math.nan),

@@ -277,8 +277,8 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_paged_cache *cache, c
         const int kbn = fa::paged::bn(static_cast<int>(d));
         const int64_t box = cache->page_size < kbn ? cache->page_size : kbn;
         fa_host::PageSteps steps;
-        if (!fa_host::page_steps(*cache, &steps)) return FA_ERR_UNSUPPORTED;
-        if (!fa_host::make_map_rows(&x.q, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf),
+        if (!fa_host::page_steps(*cache, &steps) ||
+            !fa_host::make_map_rows(&x.q, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf),
                                     static_cast<uint32_t>(tpt)) ||
             !fa_host::make_map_pages(&x.k, cache->k, *cache, steps, static_cast<uint32_t>(box)) ||
             !fa_host::make_map_pages(&x.v, cache->v, *cache, steps, static_cast<uint32_t>(box)))

@@ -55,7 +55,7 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
     for (int i = 0; i < 3; ++i)  // the stride of a single entry does not matter
         if (count[i] > 1 && (st[i] < 1 || st[i] % 8 != 0)) return FA_ERR_INVALID_ARG;
     if (c.d != 32 && c.d != 64 && c.d != 128 && c.d != 256) return FA_ERR_UNSUPPORTED;
-    if (c.page_size < 8 || c.page_size > (int64_t{1} << 20) || (c.page_size & (c.page_size - 1)) != 0)
+    if (c.page_size < kMinPage || c.page_size > (int64_t{1} << 20) || (c.page_size & (c.page_size - 1)) != 0)
         return FA_ERR_UNSUPPORTED;
     // what a tensor map and 64-bit extents hold
     if (c.num_pages >= (int64_t{1} << 31) || c.H_kv > (int64_t{1} << 20)) return FA_ERR_UNSUPPORTED;
@@ -84,6 +84,8 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
             span += (x.n - 1) * x.s;
         }
     *bytes = static_cast<size_t>(span) * 2;
+    PageSteps steps;  // the same caches for every call, whichever kernel it runs
+    if (!page_steps(c, &steps)) return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 

@@ -10,6 +10,7 @@
 
 namespace fa_host {
 
+constexpr int64_t kMinPage = 8;  // tokens per page at least: a swizzle atom of a K/V tile
 // Checks a cache descriptor (not its device); bytes: the extent of k (and of v) from
 // its first to its last element.
 fa_status check_cache(const fa_paged_cache &c, size_t *bytes);

@@ -96,7 +96,6 @@ __host__ __device__ constexpr bool two_issuers(int D) { return D >= 128; }
 // Warps that take the pieces: all but the scheduler (and an idle issuer); each arrives
 // once per piece.
 __host__ __device__ constexpr int unit_consumers(int D) { return two_issuers(D) ? 7 : 6; }
-constexpr int kMinPage = 8;        // tokens per page at least: a swizzle atom of a tile
 enum : int { kRoleSoftmax = 1, kRoleTma = 2, kRoleMma = 3 };
 
 // Written by every CTA for the merge: the unit whose first piece is this CTA's last
