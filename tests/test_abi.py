@@ -2,10 +2,12 @@
 include/*.h declares, and rejects invalid arguments before touching CUDA."""
 
 import ctypes
+import os
 
 import pytest
 
 import tiled_attention_03_gb300 as fa
+from tiled_attention_03_gb300 import build
 from tiled_attention_03_gb300.binding import declared_functions, load_library
 from tiled_attention_03_gb300.build import build_library
 
@@ -223,3 +225,12 @@ def test_splitkv_workspace_must_be_32_byte_aligned(lib):
 def test_release_build_has_no_debug_checks(lib):
     assert lib.fa_debug_flags() == 0
     lib.fa_test_arm_row_shift(0)  # accepted (and ignored) by release builds
+
+
+def test_every_source_file_makes_the_library_stale():
+    """Everything under csrc/ and include/ that a translation unit may include is looked at."""
+    looked_at = {os.path.abspath(f) for f in build._deps()}
+    for folder in (build.CSRC, build.INCLUDE):
+        for name in os.listdir(folder):
+            if name.endswith((".cu", ".cuh", ".h")):
+                assert os.path.join(folder, name) in looked_at, name
