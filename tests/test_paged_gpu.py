@@ -608,3 +608,30 @@ def test_streams_given_by_their_handles(own):
     torch.cuda.synchronize()
     for a, b in zip(got, [*want, turned, back[0], back[2]]):
         assert torch.equal(a, b)
+
+
+def test_append_of_long_prompts():
+    """Every warp's share goes around its ring and over several tokens and sequences."""
+    d, dtype, H, Hk, page = 64, torch.bfloat16, 25, 6, 32
+    lens = [(4001, 4100), (0, 9), (5000, 5000), (3333, 9000)]
+    _, cache, table, cu, lk, _ = paged(lens, 1, Hk, d, dtype, page, "head", seed=5)
+    total = int(cu[-1])
+    g = torch.Generator(device=DEV).manual_seed(12)
+    qkv = torch.randn(total, H + 2 * Hk, d, generator=g, device=DEV).to(dtype)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    rope, freq = rope_handle(d, 30, "half", dtype, True)
+    ek, ev = cache.k.clone(), cache.v.clone()
+    q_out = torch.full((total, H, d), NAN, dtype=dtype, device=DEV)
+    fa.fa_paged_append(q, k, v, q_out, cache, table, cu, lk, rope)
+    assert fa.fa_sync_status() == fa.FA_OK
+    for b, (n, keys) in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        pos = torch.arange(keys - n, keys, device=DEV)
+        want, bound = norm_rope_ref(q[rows], rope.q_weight, pos, freq, "half", 1.0, 1e-5, dtype)
+        assert_within(q_out[rows], want, bound, f"sequence {b}: q")
+        at = table[b].long()[pos // page], pos % page
+        want, bound = norm_rope_ref(k[rows], rope.k_weight, pos, freq, "half", 1.0, 1e-5, dtype)
+        assert_within(cache.k[at], want, bound, f"sequence {b}: k")
+        ek[at], ev[at] = cache.k[at], v[rows]  # the keys are checked; nothing else may differ
+    same = lambda a, b: torch.equal(a.nan_to_num(nan=1e4), b.nan_to_num(nan=1e4))  # noqa: E731
+    assert same(cache.k, ek) and same(cache.v, ev)

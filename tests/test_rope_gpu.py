@@ -324,3 +324,73 @@ def test_before_attention_and_back():
     for got, want in ((dq.transpose(1, 2), x[0].grad), (dk.transpose(1, 2), x[1].grad),
                       (dv.transpose(1, 2), x[2].grad), (dwq, x[3].grad), (dwk, x[4].grad)):
         assert (got.double() - want).norm() <= 8 * 2.0 ** -8 * want.norm()
+
+
+# How a launch is cut (the library's rule): tokens x stages of 256 / d heads (twice as many in
+# the forward) over 8 warps a block, of as many blocks as the GPU holds at once, or, forward,
+# more where each warp still gets 28 stages.
+RESIDENT, LONG = 2, 28
+
+
+def per_warp(tokens, H, Hk, d, rows):
+    per = rows * 256 // d
+    stages = tokens * (-(-H // per) + -(-Hk // per))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = RESIDENT * sms
+    if rows == 2:
+        blocks = max(blocks, stages // (8 * LONG))
+    return stages / (8 * blocks)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16])
+@pytest.mark.parametrize("layout,part", [("half", 1.0), ("half", 0.4), ("interleaved", 0.5)])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+def test_many_stages_per_warp(d, layout, part, dtype):
+    """Training sizes: a warp's share takes its ring around several times, runs on from queries to
+    keys, from token to token and from one batch entry into the next, and ends anywhere."""
+    B, N, H, Hk = 3, 4001, 33, 5
+    r = int(d * part) // 2 * 2
+    assert (layout == "interleaved") or (r % 16 == 0) == (part == 1.0)  # partners: beside, in a lane, anywhere
+    assert per_warp(B * N, H, Hk, d, 2) > 16 and per_warp(B * N, H, Hk, d, 1) > 28
+    rope, freq = handle(d, r, layout, dtype)
+    qkv = make((B, N, H + Hk, d), dtype, 50)
+    q, k = qkv[:, :, :H].transpose(1, 2), qkv[:, :, H:].transpose(1, 2)
+    y, z = fa.qk_norm_rope(q, k, rope)
+    assert fa.fa_sync_status() == fa.FA_OK
+    check_forward(q, y, rope.q_weight, freq, None, layout, 1.0, dtype, "q")
+    check_forward(k, z, rope.k_weight, freq, None, layout, 1.0, dtype, "k")
+    same = qkv.clone()
+    qs, ks = same[:, :, :H].transpose(1, 2), same[:, :, H:].transpose(1, 2)
+    fa.fa_qk_norm_rope(qs, ks, qs, ks, rope)
+    assert torch.equal(qs, y) and torch.equal(ks, z), "in place"
+
+    dqkv = make((B, N, H + Hk, d), dtype, 51)
+    dy, dz = dqkv[:, :, :H].transpose(1, 2), dqkv[:, :, H:].transpose(1, 2)
+    dq, dk, dwq, dwk = fa.qk_norm_rope_backward(q, k, dy, dz, rope)
+    assert fa.fa_sync_status() == fa.FA_OK
+    # dw: 2^-18 of each term; a lane's running sum, then 64 rows of a block, a tenth of the
+    # blocks and five halvings: that many steps of 2^-24 of the terms' sizes (sb is 2^-17 of them)
+    more = 0.5 + (per_warp(B * N, H, Hk, d, 1) + 80) / 128
+    pos = torch.arange(N, device=DEV)
+    for x, g, dx, w, dw in ((q, dy, dq, rope.q_weight, dwq), (k, dz, dk, rope.k_weight, dwk)):
+        sums, bounds = 0, 0
+        for xi, gi, di in zip(tok(x), tok(g), tok(dx)):
+            want, bound, s, sb = norm_rope_bwd_ref(xi, gi, w, pos, freq, layout, 1.0, EPS, dtype)
+            assert_within(di, want, bound, "dx")
+            sums, bounds = sums + s, bounds + more * sb
+        assert_within(dw, sums, bounds, "dw")
+    again = fa.qk_norm_rope_backward(q, k, dy, dz, rope)
+    assert all(torch.equal(a, b) for a, b in zip(again, (dq, dk, dwq, dwk))), "not the same twice"
+
+
+@pytest.mark.parametrize("more", [-1, 0, 1, 2000])
+def test_around_the_switch_to_more_blocks(more):
+    """The last sizes of resident blocks alone and the first of more."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    d, dtype = 128, torch.bfloat16
+    tokens = 8 * LONG * (RESIDENT * sms + 1) + more  # a stage each: 3 of its 4 heads there
+    assert (per_warp(tokens, 3, 0, d, 2) * 8 * RESIDENT * sms >= tokens) == (more < 0)
+    rope, freq = handle(d, d, "half", dtype)
+    x = make((tokens, 3, d), dtype, 52)
+    y, _ = fa.qk_norm_rope(x, None, rope)
+    check_forward(x, y, rope.q_weight, freq, None, "half", 1.0, dtype, "q")
