@@ -467,6 +467,11 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
  * NaN or infinity in a value row that one query of a sequence sees may reach the
  * outputs of its other new tokens processed in the same tile.
  *
+ * Scores, softmax statistics and sums are float32. The weights exp(score - maximum) are rounded
+ * to the cache's dtype for their product with V, as in fa_forward; where a batch has few new
+ * tokens (at most 16 rows, tokens x query heads of a K/V head, per sequence on average, and 32 of
+ * one sequence) they keep twice as many bits.
+ *
  * workspace: caller-owned device memory of at least
  * fa_forward_paged_workspace_bytes(d) bytes, 32-byte aligned, scratch: its contents on
  * entry do not matter. It does not depend on the batch. Calls that may overlap on the

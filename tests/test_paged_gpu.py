@@ -635,3 +635,29 @@ def test_append_of_long_prompts():
         ek[at], ev[at] = cache.k[at], v[rows]  # the keys are checked; nothing else may differ
     same = lambda a, b: torch.equal(a.nan_to_num(nan=1e4), b.nan_to_num(nan=1e4))  # noqa: E731
     assert same(cache.k, ek) and same(cache.v, ev)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("new,H,Hk", [(1, 4, 4), (1, 16, 2), (1, 18, 2), (3, 8, 2)])
+def test_steps_round_their_outputs_alone(new, H, Hk, d, dtype):
+    """Units of 1, 8, 9 and 12 rows: the weights of the keys go into their product with V in two
+    16-bit parts. What the second leaves is half a step of half a step of each (or 2^-25 where
+    fp16 goes below its normal range), so that O is off by its own rounding, by that, and by the
+    scores' products in 32 bits."""
+    lens = [(new, 700), (new, 90), (1, 5000)]
+    q, cache, table, cu, lk, seqs = paged(lens, H, Hk, d, dtype, 16, seed=d + H)
+    o, _ = run(q, cache, table, cu, lk, d ** -0.5, "causal")
+    half = torch.finfo(dtype).eps / 2
+    t = 0
+    for b, (qq, k, v) in enumerate(seqs):
+        n = qq.shape[0]
+        want = attention_ref(qq, k, v, d ** -0.5, "causal", (0, 0), dtype)[0]
+        size = attention_ref(qq, k, v.abs(), d ** -0.5, "causal", (0, 0), dtype)[0]  # sums of p |v|
+        scores = d ** -0.5 * d * float(qq.abs().max()) * float(k.abs().max())
+        step = d * 2.0 ** -24 * scores + 2.0 ** -19
+        bound = half * (1 + 2.0 ** -7) * want.abs() + (half ** 2 + 2 * step) * size
+        if dtype == torch.float16:
+            bound += 2.0 ** -25 * (1 + float(v.double().abs().sum(0).max()))
+        assert_within(o[t:t + n], want, bound, f"sequence {b}: O")
+        t += n

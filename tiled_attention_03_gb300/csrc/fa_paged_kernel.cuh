@@ -931,8 +931,11 @@ __device__ __forceinline__ void chunk_cta(const CUtensorMap &tmQ, const CUtensor
                     fadd2(s0, s1, x[c], x[c + 1]);
                     fadd2(s2, s3, x[c + 2], x[c + 3]);
                 }
-                // P(j) as 16-bit pairs over the first kBN / 2 columns of the buffer (the
-                // operand type of the product; l keeps the fp32 values)
+                // P(j) as 16-bit pairs over the first kBN / 2 columns of the buffer: the operand
+                // type of the product, as in the library's other forwards; l keeps the fp32
+                // values. The rounding puts O's error at 0.0024 where its own is 0.0017 (bf16,
+                // relative, root mean square). A second part beside it, what the rounding left,
+                // gave 0.0017 and took 988 us for 727 (2048 tokens on 32048 keys, d = 128).
 #pragma unroll
                 for (int h = 0; h < kBN; h += 64) {
                     uint32_t pk[32];
