@@ -328,7 +328,7 @@ def test_before_attention_and_back():
 
 # How a launch is cut (the library's rule): tokens x stages of 256 / d heads (twice as many in
 # the forward) over 8 warps a block, of as many blocks as the GPU holds at once, or, forward,
-# more where each warp still gets 28 stages.
+# more, a multiple of those, where each warp still gets 28 stages.
 RESIDENT, LONG = 2, 28
 
 
@@ -338,7 +338,7 @@ def per_warp(tokens, H, Hk, d, rows):
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     blocks = RESIDENT * sms
     if rows == 2:
-        blocks = max(blocks, stages // (8 * LONG))
+        blocks *= max(1, stages // (8 * LONG * blocks))
     return stages / (8 * blocks)
 
 
@@ -388,7 +388,7 @@ def test_around_the_switch_to_more_blocks(more):
     """The last sizes of resident blocks alone and the first of more."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     d, dtype = 128, torch.bfloat16
-    tokens = 8 * LONG * (RESIDENT * sms + 1) + more  # a stage each: 3 of its 4 heads there
+    tokens = 8 * LONG * 2 * RESIDENT * sms + more  # a stage each: 3 of its 4 heads there
     assert (per_warp(tokens, 3, 0, d, 2) * 8 * RESIDENT * sms >= tokens) == (more < 0)
     rope, freq = handle(d, d, "half", dtype)
     x = make((tokens, 3, d), dtype, 52)

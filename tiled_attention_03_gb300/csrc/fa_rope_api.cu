@@ -170,10 +170,14 @@ int mode_of(const fa_norm_rope &r) {
 
 // The stages of a token, `rows` rows per group each, and the blocks of a launch. Up to
 // `resident` blocks (what the SMs hold at once) every warp takes a stage at least; more,
-// up to `most`, only where their warps still have kLongShare stages each: blocks that
-// start as others end even out what the SMs get (forward, B4 N4096 H32+32 d128: 97 us with
-// resident blocks alone, 88 us with shares of 28 stages, 91 us with 14), but a short share is
-// mostly its start (24 prompts appended at d 64: 25.6 us with shares of 28, 29.5 us with 14).
+// up to `most`, in whole waves of them, only where their warps still have kLongShare stages each:
+// blocks that start as others end even out what the SMs get, but a share that is shorter is
+// mostly its start (24 prompts appended at d 64: 25.6 us with shares of 28, 29.5 us with 14),
+// and blocks of equal length past the last whole wave run by themselves (forward, 32 + 8 heads,
+// d 128: 69,000 stages in a little over a wave took 36.8 us, in one 24.7). Against resident blocks
+// alone, forward at d 128: 32 + 32 heads 260,000 stages 85.6 and 96.2 us, 137,000 47.3 and 48.1;
+// 32 + 8 heads 300,000 stages 97.0 and 105.2; tokens of few stages pay for the more starts (16 +
+// 2 heads, 5 stages a token, 300,000 in all: 112.3 and 109.2).
 // The backward keeps to resident blocks: its longer start and end and the sums of more
 // blocks cost more than they even out (92 us, 97 to 104 us with more).
 constexpr int kLongShare = 28;
@@ -185,8 +189,8 @@ unsigned set_stages(Params &p, int64_t d, int rows, long long resident, long lon
     p.s_v = stages(p.H_v);
     p.stages = static_cast<long long>(p.tokens) * (p.s_q + p.s_k + p.s_v);
     const long long each = (p.stages + fa::rope::kWarps - 1) / fa::rope::kWarps;
-    const long long longer = p.stages / (fa::rope::kWarps * kLongShare);
-    const long long blocks = longer > resident ? longer : each < resident ? each : resident;
+    const long long waves = p.stages / (fa::rope::kWarps * kLongShare * resident);
+    const long long blocks = waves > 1 ? waves * resident : each < resident ? each : resident;
     return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
