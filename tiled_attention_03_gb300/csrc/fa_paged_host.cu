@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <utility>
 
 #include "fa_host.h"
 
@@ -46,6 +47,32 @@ bool encode(CUtensorMap *map, const void *base, bool bf16, int rank, const cuuin
 
 namespace fa_host {
 
+int sm_count_or_default() {
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    else
+        cudaGetLastError();
+    return sms;
+}
+
+int64_t span_apart(const int64_t (&count)[3], const int64_t (&stride)[3], int64_t d) {
+    int64_t n[3] = {count[0], count[1], count[2]}, s[3] = {stride[0], stride[1], stride[2]};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (s[j] > s[j + 1]) {
+                std::swap(s[j], s[j + 1]);
+                std::swap(n[j], n[j + 1]);
+            }
+    int64_t span = d;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1) {
+            if (s[i] < span) return 0;
+            span += (n[i] - 1) * s[i];
+        }
+    return span;
+}
+
 fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
     if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return FA_ERR_INVALID_ARG;
     if (c.dtype != FA_DTYPE_FP16 && c.dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
@@ -65,24 +92,8 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
     for (int i = 0; i < 3; ++i)
         if (count[i] > 1) extent += static_cast<double>(count[i] - 1) * static_cast<double>(st[i]);
     if (extent > 1e18) return FA_ERR_UNSUPPORTED;
-    // every element at a place of its own: with the (extent > 1) dimensions sorted by
-    // stride, each steps over all that the smaller ones span
-    struct Dim {
-        int64_t n, s;
-    } dim[3] = {{c.num_pages, st[0]}, {c.page_size, st[1]}, {c.H_kv, st[2]}};
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2 - i; ++j)
-            if (dim[j].s > dim[j + 1].s) {
-                const Dim t = dim[j];
-                dim[j] = dim[j + 1];
-                dim[j + 1] = t;
-            }
-    int64_t span = c.d;
-    for (const Dim &x : dim)
-        if (x.n > 1) {
-            if (x.s < span) return FA_ERR_INVALID_ARG;
-            span += (x.n - 1) * x.s;
-        }
+    const int64_t span = span_apart(count, st, c.d);
+    if (span == 0) return FA_ERR_INVALID_ARG;
     *bytes = static_cast<size_t>(span) * 2;
     PageSteps steps;  // the same caches for every call, whichever kernel it runs
     if (!page_steps(c, &steps)) return FA_ERR_UNSUPPORTED;

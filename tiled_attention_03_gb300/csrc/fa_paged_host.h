@@ -10,6 +10,12 @@
 
 namespace fa_host {
 
+// SMs of the current device (152 without one).
+int sm_count_or_default();
+// Elements from the first to the last of a tensor of three dimensions over rows of d, if no two of
+// its elements share a place, else 0: with the dimensions of more than one entry sorted by
+// stride, each has to step over what the smaller ones span.
+int64_t span_apart(const int64_t (&count)[3], const int64_t (&stride)[3], int64_t d);
 constexpr int64_t kMinPage = 8;  // tokens per page at least: a swizzle atom of a K/V tile
 // Checks a cache descriptor (not its device); bytes: the extent of k (and of v) from
 // its first to its last element.

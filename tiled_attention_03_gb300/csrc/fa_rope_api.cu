@@ -42,27 +42,10 @@ int64_t extent(const Tensor &t, int64_t d) {
     return sum;
 }
 
-// Whether no two elements of a written tensor share a place: with the dimensions that
-// have more than one entry sorted by stride, each steps over what the smaller ones span.
+// Whether no two elements of a written tensor share a place.
 bool injective(const Tensor &t, int64_t d) {
-    int64_t n[3] = {t.B, t.heads, t.N}, s[3] = {t.r->batch, t.r->head, t.r->token};
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2 - i; ++j)
-            if (s[j] > s[j + 1]) {
-                int64_t x = s[j];
-                s[j] = s[j + 1];
-                s[j + 1] = x;
-                x = n[j];
-                n[j] = n[j + 1];
-                n[j + 1] = x;
-            }
-    int64_t span = d;
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1) {
-            if (s[i] < span) return false;
-            span += (n[i] - 1) * s[i];
-        }
-    return true;
+    const int64_t n[3] = {t.B, t.heads, t.N}, st[3] = {t.r->batch, t.r->head, t.r->token};
+    return fa_host::span_apart(n, st, d) > 0;
 }
 
 // Slices of one fused buffer: equal strides of tokens and batch entries (those there are
@@ -233,15 +216,6 @@ constexpr int kBlocksPerSm = 2;
 // Blocks of a backward launch at most: each leaves 2 d partial sums.
 constexpr int kBackwardBlocksPerSm = 2;
 
-int sm_count_or_default() {
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    else
-        cudaGetLastError();
-    return sms;
-}
-
 // What the two dense calls check alike: sizes, and which of q and k are there.
 fa_status check_sizes(int64_t B, int64_t *H, int64_t *H_kv, int64_t N, int64_t d, fa_dtype dtype,
                       const fa_rows *q, const fa_rows *k) {
@@ -327,7 +301,7 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
 
 size_t fa_qk_norm_rope_backward_workspace_bytes(int64_t d) {
     if (!known(d)) return 0;
-    return static_cast<size_t>(sm_count_or_default()) * kBackwardBlocksPerSm * 2 * static_cast<size_t>(d) * sizeof(float);
+    return static_cast<size_t>(fa_host::sm_count_or_default()) * kBackwardBlocksPerSm * 2 * static_cast<size_t>(d) * sizeof(float);
 }
 
 fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_rows *dq_out,

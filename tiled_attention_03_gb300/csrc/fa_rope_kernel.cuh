@@ -30,6 +30,7 @@
 #include <cstdint>
 
 #include "fa.h"
+#include "fa_copy.cuh"
 #include "fa_pdl.cuh"
 #include "ptx.cuh"
 
@@ -137,16 +138,6 @@ __device__ __forceinline__ float load1(const uint16_t *p) {
     float lo, hi;
     unpack2<BF16>(*p, lo, hi);
     return lo;
-}
-
-// 16-byte asynchronous copy global -> shared (past L1), and its groups.
-__device__ __forceinline__ void copy16(uint4 *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // How the partner of a rotated element is found: beside it (interleaved), in another
@@ -460,10 +451,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (in.h + u * G::kGroups < in.heads)
-                    copy16(&ring[warp][slot][u][lane], in.src[0] + u * G::kGroups * in.head[0]);
+                    copy16(smem_u32(&ring[warp][slot][u][lane]), in.src[0] + u * G::kGroups * in.head[0]);
             in.next(p, g, l, which);
         }
-        copy_commit();
+        copies_commit();
     };
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) issue(i);
@@ -506,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
                 dst = row_at(t, at, h) + 8 * l;
             }
             for (int j = 0; j < run.stages; ++j) {
-                copy_wait<kDepth - 2>();
+                copies_wait<kDepth - 2>();
                 __syncwarp();  // the stage is there, and the one before has been read
                 issue((slot + kDepth - 1) % kDepth);
                 const uint4(&stage)[U][32] = ring[warp][slot];
@@ -546,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
             }
         }
     }
-    copy_wait<0>();
+    copies_wait<0>();
 }
 
 // Backward: dx of every row, and per block the sums of u z over its rows. The split of
@@ -580,12 +571,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
     auto issue = [&](int slot) {
         if (in.stages > 0) {
             if (in.h < in.heads) {
-                copy16(&ring[warp][slot][0][lane], in.src[0]);
-                if (in.head[1] >= 0) copy16(&ring[warp][slot][1][lane], in.src[1]);
+                copy16(smem_u32(&ring[warp][slot][0][lane]), in.src[0]);
+                if (in.head[1] >= 0) copy16(smem_u32(&ring[warp][slot][1][lane]), in.src[1]);
             }
             in.next(p, g, l, which);
         }
-        copy_commit();
+        copies_commit();
     };
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) issue(i);
@@ -609,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
 #pragma unroll
             for (int e = 0; e < 4; ++e) dw[e] = 0;
             for (int j = 0; j < run.stages; ++j) {
-                copy_wait<kDepth - 2>();
+                copies_wait<kDepth - 2>();
                 __syncwarp();
                 issue((slot + kDepth - 1) % kDepth);
                 const uint4(&stage)[2][32] = ring[warp][slot];
@@ -646,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
             }
         }
     }
-    copy_wait<0>();
+    copies_wait<0>();
     if (p.part == nullptr) return;
     // the groups' sums, column by column, in one order
     float *red = reinterpret_cast<float *>(&ring[0][0][0][0]);
