@@ -24,8 +24,8 @@
 // launches, one of which returns at once.
 //
 // Measured with the merge, in a graph: 8 x 32768 keys, 32 / 8 heads, d 128: 162 us (6.6 TB/s);
-// 128 ragged sequences, window 4096, 16 / 4 heads, d 64: 33.5 us (4.6 TB/s; the tcgen05 tile
-// took 84 us); 4 sequences of 60-1000 keys, d 128: 11.7 us.
+// 128 ragged sequences, window 4096, 16 / 4 heads, d 64: 34 us (4.6 TB/s; the tcgen05 tile
+// took 84 us); 4 sequences of 60-1000 keys, d 128: 12.2 us.
 //
 // Keys that no row of the unit sees are not read: their rows are filled with zeros in
 // shared memory, whatever the pages hold.

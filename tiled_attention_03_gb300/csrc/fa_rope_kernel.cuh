@@ -21,7 +21,7 @@
 //
 // Bound by memory, 4 bytes per element forward and 6 backward, and beside it by its own
 // instructions (61 and 67 % of issue slots). B4 N4096 d128 bf16, replayed in a graph:
-// forward of 32+32 heads 88 us (6.1 TB/s), backward of 32+8 heads 92 us (5.5 TB/s). Without
+// forward of 32+32 heads 87 us (6.2 TB/s), backward of 32+8 heads 92 us (5.5 TB/s). Without
 // norm and rotation the forward took as long, without its stores or its loads 69 us. A
 // block per few tokens with an angle barrier took 161 and 152 us, a warp per whole token 99
 // and 133 us.
