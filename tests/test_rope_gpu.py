@@ -127,7 +127,8 @@ def test_elements_without_norm_and_rotation_stay(r, layout, dtype):
     x = torch.arange(-2 ** 15, 2 ** 15, device=DEV).flip(0).to(torch.int16).view(-1, 4, d).view(dtype)
     assert bool((x[..., 32:].view(torch.int16) == -2 ** 15).any())
     rope, _ = handle(d, r, layout, dtype, True, False)
-    for y in (*fa.qk_norm_rope(x, x, rope)[1:], fa.qk_norm_rope(None, x, rope)[1]):
+    for y in (*fa.qk_norm_rope(x, x, rope)[1:], fa.qk_norm_rope(None, x, rope)[1],
+              fa.qk_norm_rope_backward(None, None, None, x, rope)[1]):
         x0, y0 = x[..., r:], y[..., r:]
         nan = torch.isnan(x0)
         assert bool(torch.isnan(y0[nan]).all())

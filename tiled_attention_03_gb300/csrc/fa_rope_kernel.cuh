@@ -174,9 +174,9 @@ __device__ __forceinline__ void angles(float (&cs)[2][kMaxPairs], const Params &
 }
 
 // Coefficients of elements 8 l + e: C the cosine, S the sine of the partner (negative in
-// the first element of a pair); C = 1, S = -0 past the rotated ones (0 x -0 added leaves
-// the sign of a zero as it is).
-template <int MODE>
+// the first element of a pair; TRANSPOSED: in the second); C = 1, S = -0 past the rotated ones
+// (0 x -0 added leaves the sign of a zero as it is).
+template <int MODE, bool TRANSPOSED>
 __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], int half_r, int l,
                                              f2 (&C)[4], f2 (&S)[4]) {
     if constexpr (MODE == kLane) {
@@ -187,7 +187,7 @@ __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], in
             const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(-0.f, -0.f, -0.f, -0.f);
             const float4 c = rotated ? *reinterpret_cast<const float4 *>(&cs[0][j + 2 * e]) : one;
             const float4 s = rotated ? *reinterpret_cast<const float4 *>(&cs[1][j + 2 * e]) : zero;
-            const f2 sign = both(first ? -1.f : 1.f);
+            const f2 sign = both(rotated && first != TRANSPOSED ? -1.f : 1.f);
             C[e] = f2_pack(c.x, c.y), C[e + 1] = f2_pack(c.z, c.w);
             S[e] = mul2(f2_pack(s.x, s.y), sign), S[e + 1] = mul2(f2_pack(s.z, s.w), sign);
         }
@@ -204,7 +204,7 @@ __device__ __forceinline__ void coefficients(const float (&cs)[2][kMaxPairs], in
                     const bool first = MODE == kBeside ? x == 0 : i < half_r;
                     const int j = MODE == kBeside ? i >> 1 : (first ? i : i - half_r);
                     c[x] = cs[0][j];
-                    t[x] = first ? -cs[1][j] : cs[1][j];
+                    t[x] = first != TRANSPOSED ? -cs[1][j] : cs[1][j];
                 }
             }
             C[e] = f2_pack(c[0], c[1]);
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_kernel(const Params 
             f2 A[4], Bc[4];
             if (!as_is) {
                 f2 wt[4];
-                coefficients<MODE>(cs, p.half_r, l, A, Bc);
+                coefficients<MODE, false>(cs, p.half_r, l, A, Bc);
                 weights<BF16>(w, l, wt);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) A[e] = mul2(A[e], wt[e]);
@@ -585,9 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_norm_rope_bwd_kernel(const Par
     for (; at.left > 0; at.next(p, at.end - at.s)) {
         angles(cs, p, place<false>(p, at.m, at.n).pos);
         f2 C[4], S[4];
-        coefficients<MODE>(cs, p.half_r, l, C, S);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[e] = mul2(S[e], both(-1.f));  // the transposed rotation
+        coefficients<MODE, true>(cs, p.half_r, l, C, S);
         for (int s = at.s; s < at.end;) {
             const Run run = run_of<kStageHeads>(p, s, at.end);
             s += run.stages;
