@@ -494,6 +494,33 @@ def test_capture_follows_the_lengths():
     assert fa.fa_sync_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("d", [64, 256])
+def test_capture_follows_the_tokens(d):
+    """A captured step of 64 sequences and 64 tokens, replayed as the tokens move from single steps
+    to a chunk of one sequence, to a few for each of some, and back."""
+    B, H, Hk, page = 64, 8, 2, 16
+    q, cache, table, cu, lk, _ = paged([(1, 400)] * B, H, Hk, d, torch.bfloat16, page, seed=d)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    ws = torch.empty(fa.fa_forward_paged_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+    step = lambda: fa.fa_forward_paged(q, o, lse, cache, table, cu, lk, 0.1, "causal", 0, 0, ws)  # noqa: E731
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rows = [torch.stack([x[table[b, j // page], j % page] for j in range(400)])
+            for x in (cache.k, cache.v) for b in range(B)]
+    for new in ([1] * B, [0] * 40 + [64] + [0] * 23, [4] * 16 + [0] * 48, [0] * 10 + [30, 34] + [0] * 52, [1] * B):
+        cu.copy_(torch.tensor([sum(new[:b]) for b in range(B + 1)]))
+        o.fill_(NAN)
+        torch.cuda.synchronize()
+        graph.replay()
+        assert fa.fa_sync_status() == fa.FA_OK
+        at = [sum(new[:b]) for b in range(B)]
+        seqs = [(q[at[b]:at[b] + new[b]], rows[b], rows[B + b]) for b in range(B)]
+        check(o, lse, seqs, 0.1, "causal", (0, 0), torch.bfloat16)
+
+
 @pytest.mark.parametrize("new", [1, 60])
 def test_two_streams_at_once(new):
     """Two calls that may overlap, without a workspace of the caller's, on streams of their
