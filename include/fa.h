@@ -489,6 +489,73 @@ fa_status fa_forward_paged(const void *Q, void *O, float *LSE, const fa_paged_ca
 /* Workspace bytes fa_forward_paged needs on the current device (0: invalid d). */
 size_t fa_forward_paged_workspace_bytes(int64_t d);
 
+/*
+ * A paged cache of one latent row per token: num_pages pages of page_size rows of
+ * d_latent latent elements and d_rope rotary ones behind them, element (page, token, i) at
+ * data + page * page_stride + token * token_stride + i. All heads read the same row: it is the
+ * key of each, and its latent part the value. Strides, page_size and num_pages as for
+ * fa_paged_cache (H_kv = 1). data: device memory, 16-byte aligned. d_latent: 128, 256 or
+ * 512; d_rope: 64.
+ */
+typedef struct {
+    void *data;
+    int64_t page_stride, token_stride;
+    int64_t num_pages, page_size, d_latent, d_rope;
+    fa_dtype dtype;
+} fa_latent_cache;
+
+/*
+ * fa_latent_append -- write the new tokens' latent rows into their pages: the latent c,
+ * normalised over its d_latent elements by rope->k_weight (d_latent elements; NULL: as it is),
+ * and the key's rotary part k_rope, rotated; and, when q_rope is given, q_out from the
+ * rotary parts of the queries, rotated alike. A token's rotary position is its key
+ * position. The batch, its arrays and what happens to tokens without a place are as for
+ * fa_paged_append. c: total_q rows of d_latent, k_rope: total_q rows of d_rope (their `token`
+ * strides are used: the two halves of one projection are fine); q_rope, q_out:
+ * total_q x H x d_rope by `head` and `token`, or both with data = NULL (H is then
+ * ignored): slices of wider buffers are fine, such as the last d_rope columns of the
+ * absorbed queries that fa_forward_latent takes. q_out may be q_rope. rope->rotary_dim is
+ * at most d_rope, rope->q_weight must be NULL. rope = NULL: rows are stored, and rotary parts of
+ * queries copied, as they are. One kernel launch. Errors as fa_forward.
+ */
+fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_rows *k_rope,
+                           const fa_rows *q_out, const fa_latent_cache *cache,
+                           const int32_t *block_table, int64_t max_pages, const int32_t *cu_seqlens_q,
+                           const int32_t *seqlens_k, int64_t B, int64_t H, int64_t total_q,
+                           const fa_norm_rope *rope, void *stream);
+
+/*
+ * fa_forward_latent -- attention of the new tokens over their sequences' latent rows
+ * (fa_latent_append first: a token sees its own row), in the absorbed form: for each
+ * (token, head) pair with query q of d_latent + d_rope elements
+ *     s_j = scale q . row_j + mask,  O = sum_j softmax(s)_j row_j[0 .. d_latent),
+ *     LSE = ln sum_j exp(s_j).
+ * The caller multiplies its queries with the up-projection of the keys before, and O with that
+ * of the values after; with c the stored latent, that is attention with keys (W_k c, k_rope)
+ * and values W_v c per head. Q: total_q x H x (d_latent + d_rope), O: total_q x H x d_latent,
+ * both contiguous and of the cache's dtype; LSE: total_q x H float32; any H >= 1. scale is that
+ * of the heads as the model defines them. Positions, masks, tokens without keys or sequences,
+ * what is not looked at, and NaN in rows that are: as for fa_forward_paged.
+ *
+ * Scores, softmax statistics and sums are float32; the weights exp(score - reference) are
+ * rounded to the cache's dtype for their product with the rows.
+ *
+ * workspace: caller-owned device memory of at least
+ * fa_forward_latent_workspace_bytes(d_latent) bytes, 32-byte aligned, scratch: its contents on
+ * entry do not matter. It does not depend on the batch. Calls that may overlap on the GPU
+ * need a workspace each. Two kernel launches. The results are the same every time on one
+ * device. total_q * H is at most 2^30. Everything else as fa_forward_paged.
+ */
+fa_status fa_forward_latent(const void *Q, void *O, float *LSE, const fa_latent_cache *cache,
+                            const int32_t *block_table, int64_t max_pages,
+                            const int32_t *cu_seqlens_q, const int32_t *seqlens_k, int64_t B,
+                            int64_t H, int64_t total_q, float scale, fa_mask_mode mask_mode,
+                            int64_t window_left, int64_t window_right, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Workspace bytes fa_forward_latent needs on the current device (0: invalid d_latent). */
+size_t fa_forward_latent_workspace_bytes(int64_t d_latent);
+
 /* Static, NUL-terminated description of a status code. Never NULL. */
 const char *fa_status_string(fa_status status);
 

@@ -18,3 +18,5 @@ from .binding import (NormRope, PagedCache, fa_forward_paged,  # noqa: F401
                       fa_qk_norm_rope_backward, fa_qk_norm_rope_backward_workspace_bytes,
                       fa_rope_steps, forward_paged, qk_norm_rope, qk_norm_rope_backward,
                       rope_frequencies, rope_steps)
+from .binding import (LatentCache, fa_forward_latent, fa_forward_latent_workspace_bytes,  # noqa: F401
+                      fa_latent_append, forward_latent)

@@ -51,6 +51,14 @@ class FaPagedCache(ctypes.Structure):
                 ("H_kv", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
+class FaLatentCache(ctypes.Structure):
+    """fa_latent_cache of include/fa.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("d_latent", ctypes.c_int64),
+                ("d_rope", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -140,6 +148,12 @@ def load_library_at(path: str) -> ctypes.CDLL:
                                ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.fa_forward_paged_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_forward_paged_workspace_bytes.argtypes = [ctypes.c_int64]
+    lib.fa_latent_append.restype = ctypes.c_int
+    lib.fa_latent_append.argtypes = lib.fa_paged_append.argtypes
+    lib.fa_forward_latent.restype = ctypes.c_int
+    lib.fa_forward_latent.argtypes = lib.fa_forward_paged.argtypes
+    lib.fa_forward_latent_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_forward_latent_workspace_bytes.argtypes = [ctypes.c_int64]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_status_string.argtypes = [ctypes.c_int]
     lib.fa_sync_status.restype = ctypes.c_int
@@ -605,6 +619,23 @@ class PagedCache:
         self.address = ctypes.addressof(self.c)
 
 
+class LatentCache:
+    """fa_latent_cache over a tensor (num_pages, page_size, d_latent + d_rope), rows contiguous:
+    the latent elements of a token first, its rotary ones behind them."""
+
+    def __init__(self, data: torch.Tensor, d_latent: int):
+        if not data.is_cuda or data.dim() != 3 or data.dtype not in _DTYPES or \
+                data.stride(2) != 1 or not 0 < d_latent < data.shape[2]:
+            raise FaError(FA_ERR_INVALID_ARG, "LatentCache")
+        self.data, self.dtype = data, data.dtype
+        self.num_pages, self.page_size, self.d = data.shape
+        self.d_latent, self.d_rope = int(d_latent), self.d - int(d_latent)
+        ps, ts = data.stride()[:2]
+        self.c = FaLatentCache(data.data_ptr(), ps, ts, self.num_pages, self.page_size, self.d_latent,
+                               self.d_rope, _DTYPES[data.dtype])
+        self.address = ctypes.addressof(self.c)
+
+
 _FA_ROWS = struct.Struct("@Pqqq")  # fa_rows of include/fa.h: data and three strides
 _pack_rows = _FA_ROWS.pack
 _NO_ROWS = _pack_rows(0, 0, 0, 0)
@@ -621,6 +652,13 @@ def _rows(t: torch.Tensor | None, dtype, what: str) -> bytes:
     if len(s) == 4:
         return _pack_rows(t.data_ptr(), s[0], s[1], s[2])
     return _pack_rows(t.data_ptr(), 0, s[1], s[0])
+
+
+def _token_rows(t: torch.Tensor, dtype, what: str) -> bytes:
+    """The descriptor of a (tokens, d) tensor: rows of one head."""
+    if t.dtype is not dtype or t.stride(-1) != 1:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    return _pack_rows(t.data_ptr(), 0, 0, t.stride(0))
 
 
 def _qk_sizes(q, k, what: str):
@@ -852,4 +890,81 @@ def forward_paged(q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
     fa_forward_paged(q, o, lse, cache, block_table, cu_seqlens_q, seqlens_k,
                      q.shape[-1] ** -0.5 if scale is None else scale, mask, window[0], window[1], None,
                      stream)
+    return o, lse
+
+
+def fa_latent_append(q_rope: torch.Tensor | None, c: torch.Tensor, k_rope: torch.Tensor,
+                     q_out: torch.Tensor | None, cache: LatentCache, block_table: torch.Tensor,
+                     cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor,
+                     rope: NormRope | None = None, stream=None) -> None:
+    """Enqueue fa_latent_append: c (total_q, d_latent), normalised by `rope`'s k_weight, and
+    k_rope (total_q, d_rope), rotated, go to the rows of block_table (B, max_pages) int32 at each
+    sequence's last positions; q_rope (total_q, H, d_rope) is rotated to q_out, which may be
+    the last columns of the absorbed queries (both may be None). cu_seqlens_q (B + 1,) and
+    seqlens_k (B,) int32; seqlens_k counts the new tokens."""
+    what = "fa_latent_append"
+    dtype, total = cache.dtype, c.shape[0]
+    if c.shape != (total, cache.d_latent) or k_rope.shape != (total, cache.d_rope):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    _same_shape(q_rope, q_out, what)
+    if q_rope is not None and (q_rope.dim() != 3 or q_rope.shape[0] != total or
+                               q_rope.shape[2] != cache.d_rope):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    if rope is not None:
+        rope.check(dtype, cache.d_latent, what)
+    table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
+    rc = (_lib or load_library()).fa_latent_append(
+        _rows(q_rope, dtype, what), _token_rows(c, dtype, what), _token_rows(k_rope, dtype, what),
+        _rows(q_out, dtype, what), cache.address, table, pages, cu, lens, B,
+        0 if q_rope is None else q_rope.shape[1], total, None if rope is None else rope.address,
+        _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def fa_forward_latent_workspace_bytes(d_latent: int) -> int:
+    return load_library().fa_forward_latent_workspace_bytes(d_latent)
+
+
+def fa_forward_latent(q: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, cache: LatentCache,
+                      block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                      seqlens_k: torch.Tensor, scale: float, mask_mode=FA_MASK_CAUSAL,
+                      window_left: int = 0, window_right: int = 0,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Enqueue fa_forward_latent: q (total_q, H, d_latent + d_rope), o (total_q, H, d_latent) and
+    lse (total_q, H) float32, contiguous; block_table (B, max_pages), cu_seqlens_q (B + 1,),
+    seqlens_k (B,) int32. Without a workspace tensor one is taken from PyTorch's caching
+    allocator."""
+    what = "fa_forward_latent"
+    lib = _lib or load_library()
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.d or o.shape != (*shape[:2], cache.d_latent) or \
+            lse.shape != shape[:2] or q.dtype != cache.dtype or o.dtype != q.dtype or \
+            lse.dtype != torch.float32:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    if not (q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
+    ws, n, keep = _workspace(
+        workspace, lib.fa_forward_latent_workspace_bytes(cache.d_latent) if workspace is None else 0, q,
+        stream, what)
+    rc = lib.fa_forward_latent(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache.address, table, pages,
+                               cu, lens, B, shape[1], shape[0], float(scale), _MASKS[mask_mode],
+                               int(window_left), int(window_right), ws, n, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def forward_latent(q: torch.Tensor, cache: LatentCache, block_table: torch.Tensor,
+                   cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor, scale: float,
+                   mask="causal", window=(0, 0), stream=None):
+    """Attention of the new tokens' absorbed queries q (total_q, H, d_latent + d_rope) over a
+    cache of latent rows: returns (O, LSE), O (total_q, H, d_latent), tensors of `stream`. scale
+    has no default: it is that of the heads before the absorption."""
+    with _on(stream):
+        q = q.contiguous()
+        o = torch.empty(*q.shape[:2], cache.d_latent, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    fa_forward_latent(q, o, lse, cache, block_table, cu_seqlens_q, seqlens_k, scale, mask, window[0],
+                      window[1], None, stream)
     return o, lse

@@ -73,7 +73,9 @@ int64_t span_apart(const int64_t (&count)[3], const int64_t (&stride)[3], int64_
     return span;
 }
 
-fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
+namespace {
+// Everything about a cache but the head dimensions that the kernels know.
+fa_status check_pages(const fa_paged_cache &c, bool known, size_t *bytes) {
     if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return FA_ERR_INVALID_ARG;
     if (c.dtype != FA_DTYPE_FP16 && c.dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
     if (c.num_pages < 1 || c.H_kv < 1 || c.page_size < 1 || c.d < 1) return FA_ERR_INVALID_ARG;
@@ -81,7 +83,7 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
     const int64_t count[3] = {c.num_pages, c.page_size, c.H_kv};
     for (int i = 0; i < 3; ++i)  // the stride of a single entry does not matter
         if (count[i] > 1 && (st[i] < 1 || st[i] % 8 != 0)) return FA_ERR_INVALID_ARG;
-    if (c.d != 32 && c.d != 64 && c.d != 128 && c.d != 256) return FA_ERR_UNSUPPORTED;
+    if (!known) return FA_ERR_UNSUPPORTED;
     if (c.page_size < kMinPage || c.page_size > (int64_t{1} << 20) || (c.page_size & (c.page_size - 1)) != 0)
         return FA_ERR_UNSUPPORTED;
     // what a tensor map and 64-bit extents hold
@@ -98,6 +100,19 @@ fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
     PageSteps steps;  // the same caches for every call, whichever kernel it runs
     if (!page_steps(c, &steps)) return FA_ERR_UNSUPPORTED;
     return FA_OK;
+}
+}  // namespace
+
+fa_status check_cache(const fa_paged_cache &c, size_t *bytes) {
+    return check_pages(c, c.d == 32 || c.d == 64 || c.d == 128 || c.d == 256, bytes);
+}
+
+fa_status check_latent(const fa_latent_cache &c, fa_paged_cache *rows, size_t *bytes) {
+    if (c.d_latent < 1 || c.d_rope < 1) return FA_ERR_INVALID_ARG;
+    const bool known = (c.d_latent == 128 || c.d_latent == 256 || c.d_latent == 512) && c.d_rope == 64;
+    *rows = fa_paged_cache{c.data, c.data, c.page_stride, c.token_stride, 0, c.num_pages, c.page_size, 1,
+                           known ? c.d_latent + c.d_rope : 1, c.dtype};
+    return check_pages(*rows, known, bytes);
 }
 
 bool make_map_rows(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t heads,
@@ -129,7 +144,7 @@ bool page_steps(const fa_paged_cache &c, PageSteps *s) {
 }
 
 bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c, const PageSteps &s,
-                    uint32_t box_tokens) {
+                    uint32_t box_tokens, uint32_t box_regions) {
     const int64_t cols = c.d < 64 ? c.d : 64;
     const cuuint64_t dims[5] = {
         static_cast<cuuint64_t>(cols), 8, static_cast<cuuint64_t>(c.d / cols),
@@ -137,8 +152,8 @@ bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c,
     const cuuint64_t strides[4] = {
         static_cast<cuuint64_t>(c.token_stride * 2), static_cast<cuuint64_t>(cols * 2),
         static_cast<cuuint64_t>(c.token_stride * 16), static_cast<cuuint64_t>(s.stride * 2)};
-    const cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), 8, static_cast<cuuint32_t>(c.d / cols),
-                               box_tokens / 8, 1};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), 8,
+                               box_regions ? box_regions : static_cast<cuuint32_t>(c.d / cols), box_tokens / 8, 1};
     return encode(map, base, c.dtype == FA_DTYPE_BF16, 5, dims, strides, box, c.d);
 }
 

@@ -20,6 +20,9 @@ constexpr int64_t kMinPage = 8;  // tokens per page at least: a swizzle atom of 
 // Checks a cache descriptor (not its device); bytes: the extent of k (and of v) from
 // its first to its last element.
 fa_status check_cache(const fa_paged_cache &c, size_t *bytes);
+// A cache of latent rows as a cache of one head of d_latent + d_rope elements, k = v = data: what
+// the functions here that do not look at d's value take. Checks the descriptor like check_cache.
+fa_status check_latent(const fa_latent_cache &c, fa_paged_cache *rows, size_t *bytes);
 // 3-D TMA map over a contiguous tokens x heads x d 16-bit tensor, ordered (d, heads,
 // tokens): box of min(d, 64) columns x box_heads x box_tokens.
 bool make_map_rows(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t heads,
@@ -33,8 +36,8 @@ struct PageSteps {
 bool page_steps(const fa_paged_cache &c, PageSteps *s);
 // 5-D TMA map over one tensor of a paged cache, ordered (column in a region of min(d, 64),
 // token in a group of 8, region, group of 8 tokens of a page, page and head as above): box
-// of all columns of box_tokens tokens of one head of one page.
+// of box_regions regions (0: all columns) of box_tokens tokens of one head of one page.
 bool make_map_pages(CUtensorMap *map, const void *base, const fa_paged_cache &c, const PageSteps &s,
-                    uint32_t box_tokens);
+                    uint32_t box_tokens, uint32_t box_regions = 0);
 
 }  // namespace fa_host

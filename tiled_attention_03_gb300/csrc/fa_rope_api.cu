@@ -1,5 +1,6 @@
-// fa_rope_api.cu -- fa_rope_steps, fa_qk_norm_rope, fa_qk_norm_rope_backward and
-// fa_paged_append: argument checks and launches of the kernels of fa_rope_kernel.cuh.
+// fa_rope_api.cu -- fa_rope_steps, fa_qk_norm_rope, fa_qk_norm_rope_backward, fa_paged_append
+// and fa_latent_append: argument checks and launches of the kernels of fa_rope_kernel.cuh and
+// fa_latent_append_kernel.cuh.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -7,6 +8,7 @@
 
 #include "fa.h"
 #include "fa_host.h"
+#include "fa_latent_append_kernel.cuh"
 #include "fa_paged_host.h"
 #include "fa_pdl.cuh"
 #include "fa_rope_kernel.cuh"
@@ -215,6 +217,16 @@ cudaError_t backward(const Params &p, int64_t d, bool bf16, int mode, unsigned g
 constexpr int kBlocksPerSm = 2;
 // Blocks of a backward launch at most: each leaves 2 d partial sums.
 constexpr int kBackwardBlocksPerSm = 2;
+
+template <int DL, bool BF16>
+cudaError_t latent_mode(const fa::latent::AppendParams &p, int mode, unsigned g, cudaStream_t st) {
+    using namespace fa::rope;
+    using fa::latent::fa_latent_append_kernel;
+    auto *k = mode == kBeside ? fa_latent_append_kernel<DL, BF16, kBeside>
+              : mode == kLane ? fa_latent_append_kernel<DL, BF16, kLane>
+                              : fa_latent_append_kernel<DL, BF16, kAnywhere>;
+    return fa::launch_after(k, g, fa::latent::kAppendThreads, 0, st, p);
+}
 
 // What the two dense calls check alike: sizes, and which of q and k are there.
 fa_status check_sizes(int64_t B, int64_t *H, int64_t *H_kv, int64_t N, int64_t d, fa_dtype dtype,
@@ -480,6 +492,109 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     if (forward<true>(p, d, cache->dtype == FA_DTYPE_BF16, mode_of(r), blocks,
                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return FA_ERR_CUDA;
+    fa_host::count_launches(1);
+    return FA_OK;
+}
+
+fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_rows *k_rope,
+                           const fa_rows *q_out, const fa_latent_cache *cache,
+                           const int32_t *block_table, int64_t max_pages, const int32_t *cu_seqlens_q,
+                           const int32_t *seqlens_k, int64_t B, int64_t H, int64_t total_q,
+                           const fa_norm_rope *rope, void *stream) {
+    if (cache == nullptr || B < 1 || total_q < 0 || max_pages < 0 || there(q_rope) != there(q_out))
+        return FA_ERR_INVALID_ARG;
+    size_t cache_bytes = 0;
+    fa_paged_cache rows{};
+    fa_status s = fa_host::check_latent(*cache, &rows, &cache_bytes);
+    if (s != FA_OK) return s;
+    const int64_t dl = cache->d_latent, dr = cache->d_rope;
+    const fa_norm_rope plain{nullptr, 0, FA_ROPE_INTERLEAVED, 1.f, nullptr, nullptr, 0.f};
+    const fa_norm_rope &r = rope ? *rope : plain;
+    s = check_rope(r, dr);
+    if (s != FA_OK) return s;
+    if (r.q_weight != nullptr) return FA_ERR_INVALID_ARG;
+    if (!there(q_rope)) H = 0;
+    if (there(q_rope) && H < 1) return FA_ERR_INVALID_ARG;
+    if (total_q == 0) return FA_OK;  // no new tokens: nothing to do
+    if (!there(c) || !there(k_rope) || !cu_seqlens_q || !seqlens_k || (!block_table && max_pages > 0))
+        return FA_ERR_INVALID_ARG;
+    if (!fa_host::aligned4(block_table) || !fa_host::aligned4(cu_seqlens_q) || !fa_host::aligned4(seqlens_k))
+        return FA_ERR_INVALID_ARG;
+    if (total_q > kLimit || B > kLimit || H > (1 << 20) || max_pages > kLimit ||
+        max_pages * cache->page_size > (int64_t{1} << 31))
+        return FA_ERR_UNSUPPORTED;
+    const Tensor t[] = {{q_rope, 1, H, total_q, false, -1}, {k_rope, 1, 1, total_q, false, -1},
+                        {q_out, 1, H, total_q, true, 0}};
+    s = check_tensors(t, 3, dr);
+    if (s != FA_OK) return s;
+    const Tensor latents[] = {{c, 1, 1, total_q, false, -1}};
+    s = check_tensors(latents, 1, dl);
+    if (s != FA_OK) return s;
+    const struct {
+        const void *p;
+        size_t n;
+    } small[] = {{r.rotary_dim > 0 ? r.steps : nullptr, static_cast<size_t>(r.rotary_dim) * 4},
+                 {r.k_weight, static_cast<size_t>(dl) * 2},
+                 {max_pages > 0 ? block_table : nullptr, static_cast<size_t>(B * max_pages) * 4},
+                 {cu_seqlens_q, static_cast<size_t>(B + 1) * 4},
+                 {seqlens_k, static_cast<size_t>(B) * 4},
+                 {c->data, static_cast<size_t>(extent(latents[0], dl)) * 2}};
+    for (const auto &x : small) {
+        if (hits_written(x.p, x.n, t, 3, dr)) return FA_ERR_INVALID_ARG;
+        if (x.p != nullptr && fa_host::overlaps(cache->data, cache_bytes, x.p, x.n)) return FA_ERR_INVALID_ARG;
+    }
+    for (const Tensor &x : t)
+        if (there(x.r) &&
+            fa_host::overlaps(cache->data, cache_bytes, x.r->data, static_cast<size_t>(extent(x, dr)) * 2))
+            return FA_ERR_INVALID_ARG;
+    int dev = 0;
+    fa_host::DeviceInfo di;
+    s = device_of(&dev, &di);
+    if (s != FA_OK) return s;
+    for (const Tensor &x : t)
+        if (there(x.r) && !fa_host::on_device(x.r->data, dev)) return FA_ERR_INVALID_ARG;
+    for (const auto &x : small)
+        if (!absent_or_on(x.p, dev)) return FA_ERR_INVALID_ARG;
+    if (!fa_host::on_device(cache->data, dev)) return FA_ERR_INVALID_ARG;
+    fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
+    fa::latent::AppendParams a{};
+    Params &p = a.r;
+    p.q = rows_of(q_rope, 1, H, total_q);
+    p.q_out = rows_of(q_out, 1, H, total_q);
+    p.H = static_cast<int>(H);
+    p.N = p.tokens = static_cast<int>(total_q);
+    set_rope(p, r);
+    p.page_stride = rows.page_stride;
+    p.token_stride = rows.token_stride;
+    p.cu_q = cu_seqlens_q;
+    p.seq_k = seqlens_k;
+    p.table = block_table;
+    p.B = static_cast<int>(B);
+    p.max_pages = static_cast<int>(max_pages);
+    while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
+    p.num_pages = static_cast<int>(cache->num_pages);
+    const Rows cr = rows_of(c, 1, 1, total_q), kr = rows_of(k_rope, 1, 1, total_q);
+    a.c = cr.p;
+    a.k = kr.p;
+    a.c_token = cr.token;
+    a.k_token = kr.token;
+    a.data = static_cast<uint16_t *>(cache->data);
+    a.parts = static_cast<int>(1 + (H + fa::latent::kHeads - 1) / fa::latent::kHeads);
+    a.items = total_q * a.parts;
+    // a warp per item up to what the SMs hold at once
+    const long long each = (a.items + fa::latent::kAppendWarps - 1) / fa::latent::kAppendWarps;
+    const long long most = static_cast<long long>(di.sm_count) * 4;
+    const unsigned blocks = static_cast<unsigned>(each < most ? each : most);
+    const int mode = mode_of(r);
+    const bool bf16 = cache->dtype == FA_DTYPE_BF16;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    switch (dl) {
+        case 128: e = bf16 ? latent_mode<128, true>(a, mode, blocks, st) : latent_mode<128, false>(a, mode, blocks, st); break;
+        case 256: e = bf16 ? latent_mode<256, true>(a, mode, blocks, st) : latent_mode<256, false>(a, mode, blocks, st); break;
+        default: e = bf16 ? latent_mode<512, true>(a, mode, blocks, st) : latent_mode<512, false>(a, mode, blocks, st); break;
+    }
+    if (e != cudaSuccess) return FA_ERR_CUDA;
     fa_host::count_launches(1);
     return FA_OK;
 }
