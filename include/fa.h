@@ -556,6 +556,27 @@ fa_status fa_forward_latent(const void *Q, void *O, float *LSE, const fa_latent_
 /* Workspace bytes fa_forward_latent needs on the current device (0: invalid d_latent). */
 size_t fa_forward_latent_workspace_bytes(int64_t d_latent);
 
+/*
+ * fa_paged_weights -- the attention weight that a batch's new tokens give to each key, gathered
+ * over calls. For key j of sequence b and each K/V head, over the new tokens i that see it and
+ * the query heads h of that K/V head,
+ *     a_j = sum_{i, h} exp(scale q_{i,h} . k_j - LSE_{i,h})
+ * and then weights_j += a_j for a key that was there before the call's tokens, weights_j = a_j for
+ * the call's own (the last L_q positions), whose slots need no clearing. Q, cache, batch, scale
+ * and mask are those of the fa_forward_paged call that wrote LSE (only the keys of the cache
+ * are read). A row whose LSE is -infinity adds nothing. weights: device memory, num_pages x
+ * H_kv x page_size float32, contiguous: entry (page, head, token). Entries of keys that no new
+ * token sees, and of slots past a sequence's end, are left as they are. A page that several
+ * sequences of the batch share gets each one's a_j, added in any order; otherwise the
+ * results are the same every time. weights overlaps no other buffer. One kernel launch, no
+ * workspace. Everything else as fa_forward_paged.
+ */
+fa_status fa_paged_weights(const void *Q, const float *LSE, float *weights, const fa_paged_cache *cache,
+                           const int32_t *block_table, int64_t max_pages, const int32_t *cu_seqlens_q,
+                           const int32_t *seqlens_k, int64_t B, int64_t H, int64_t total_q, float scale,
+                           fa_mask_mode mask_mode, int64_t window_left, int64_t window_right,
+                           void *stream);
+
 /* Static, NUL-terminated description of a status code. Never NULL. */
 const char *fa_status_string(fa_status status);
 

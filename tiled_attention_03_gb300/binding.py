@@ -154,6 +154,11 @@ def load_library_at(path: str) -> ctypes.CDLL:
     lib.fa_forward_latent.argtypes = lib.fa_forward_paged.argtypes
     lib.fa_forward_latent_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_forward_latent_workspace_bytes.argtypes = [ctypes.c_int64]
+    lib.fa_paged_weights.restype = ctypes.c_int
+    lib.fa_paged_weights.argtypes = [ctypes.c_void_p] * 3 + [
+        cache, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p] + [
+        ctypes.c_int64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                               ctypes.c_void_p]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_status_string.argtypes = [ctypes.c_int]
     lib.fa_sync_status.restype = ctypes.c_int
@@ -968,3 +973,32 @@ def forward_latent(q: torch.Tensor, cache: LatentCache, block_table: torch.Tenso
     fa_forward_latent(q, o, lse, cache, block_table, cu_seqlens_q, seqlens_k, scale, mask, window[0],
                       window[1], None, stream)
     return o, lse
+
+
+def _check_weights(weights: torch.Tensor, cache: PagedCache, what: str) -> None:
+    if weights.dtype != torch.float32 or not weights.is_contiguous() or \
+            weights.shape != (cache.num_pages, cache.H_kv, cache.page_size):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+
+
+def fa_paged_weights(q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, cache: PagedCache,
+                     block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                     seqlens_k: torch.Tensor, scale: float, mask_mode=FA_MASK_CAUSAL,
+                     window_left: int = 0, window_right: int = 0, stream=None) -> None:
+    """Enqueue fa_paged_weights: q (total_q, H, d) and lse (total_q, H) float32 as fa_forward_paged
+    took and wrote them, contiguous; weights (num_pages, H_kv, page_size) float32, the attention
+    weight gathered by each key so far; block_table (B, max_pages), cu_seqlens_q (B + 1,),
+    seqlens_k (B,) int32."""
+    what = "fa_paged_weights"
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.d or lse.shape != shape[:2] or q.dtype != cache.dtype or \
+            lse.dtype != torch.float32 or not (q.is_contiguous() and lse.is_contiguous()):
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    _check_weights(weights, cache, what)
+    table, pages, cu, lens, B = _batch(block_table, cu_seqlens_q, seqlens_k, what)
+    rc = (_lib or load_library()).fa_paged_weights(
+        q.data_ptr(), lse.data_ptr(), weights.data_ptr(), cache.address, table, pages, cu, lens, B,
+        shape[1], shape[0], float(scale), _MASKS[mask_mode], int(window_left), int(window_right),
+        _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)

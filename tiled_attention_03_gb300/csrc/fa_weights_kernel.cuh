@@ -1,0 +1,550 @@
+// fa_weights_kernel.cuh -- the attention weight that the new tokens of a batch give to each key of
+// a paged cache, for head dimensions 32, 64, 128 and 256 on sm_103a.
+//
+// For key j of a K/V head, over the new tokens i of its sequence that see it and the query
+// heads h of the group,
+//     a_j = sum_{i, h} exp(scale q_{i,h} . k_j - LSE_{i,h}),
+// with the LSE that the attention of the same tokens left. No row maximum and no normalisation
+// are needed: LSE is both. A key that was there before gets a_j added, one of the call's
+// own tokens is set to it, so a slot's former content does not matter.
+//
+// The scores are taken transposed, S^T = K Q^T (128 keys x R rows): keys stand in the lanes of
+// tensor memory, so that the sum over rows is a sum over one thread's registers, and a tile of
+// keys, the M operand, is read once for all rows of its sequence and K/V head. A unit is one tile
+// of 128 keys of one K/V head with all tiles of R rows that see it; CTA c takes every gridDim-th
+// unit from c on. That shares them evenly (units of one sequence grow lighter along the keys under
+// a causal mask, and neighbours go to different CTAs), needs no counters, and gives every
+// key to one thread: one addition per key and call, so the result is the same every time (keys
+// of pages that several sequences share get one addition each, in any order).
+//
+// What bounds it: single steps read K once, by HBM. Chunks take one exponential per key and
+// row: 128 x 128 of them occupy the SM's exponential unit for 1,024 cycles, where the
+// products (d = 128) take 512.
+//
+// Warps (352 threads): 0-3 and 4-7 sum alternate tiles of rows (of units with one: alternate
+// units), 8 finds units and loads keys, 9 issues the products, 10 loads queries and their LSE.
+// Every wait is bounded; on expiry the CTA records the failure, drains its copies and
+// products, frees its tensor memory and returns.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "fa_paged_kernel.cuh"
+#include "fa_pdl.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace weights {
+
+constexpr int kBK = 128;  // keys per tile
+constexpr int kThreads = 352;
+constexpr int kPlanWarp = 8, kIssueWarp = 9, kQWarp = 10;
+constexpr int kUnitSlots = 4;
+constexpr int kUnitConsumers = 10;
+constexpr int kMaxStages = 8;
+constexpr int kBufs = 4;  // of scores and of their rows' LSE
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmem = 0;  // all columns are allocated: they start at 0
+constexpr unsigned kStatusTimeout = 4;
+constexpr unsigned kStatusLayout = 2;  // shared memory base not 1024-aligned
+enum : int { kRoleSum = 1, kRoleTma = 2, kRoleMma = 3 };
+
+struct Params {
+    float *weights;    // page x H_kv x page_size
+    const float *LSE;
+    const int *cu_q, *seq_k, *table;
+    int B, H, H_kv, pf, subs, tpt;  // heads and tokens of a tile of rows; tiles of heads per group
+    int total_q, max_pages, page_log2, num_pages, max_keys;
+    int chunk;         // tokens per TMA box: min(page size, kBK)
+    int page_step, head_step, page_none;  // the map's last coordinate; past its end
+    int wl, wr;        // key j visible to the query at position i iff i - wl <= j <= i + wr
+    float scale_log2;
+    unsigned long long wait_budget_ns;
+    unsigned int *status;
+    int fault_skip_k;  // test hook: every CTA skips the load at this ring position (-1: none)
+};
+
+template <int D, int R>
+struct Smem {
+    using P = paged::Smem<D>;  // the layout of key tiles: groups of 8 rows, their regions side by side
+    static constexpr int kTile = kBK / 8 * P::kGroup;
+    static constexpr int kQRegion = R * P::kRowBytes;
+    static constexpr int kQBytes = P::kRegions * kQRegion;
+    static constexpr int kSmall = 4096;
+    static constexpr int kMost = 227 * 1024 - kSmall;
+    // as many tiles of queries as leave four of keys (two where a tile of keys is 64 KB)
+    static constexpr int kQFit = (kMost - (D == 256 ? 2 : 4) * kTile) / kQBytes;
+    static constexpr int kQStages = kQFit < 4 ? kQFit : 4;
+    static constexpr int kKFit = (kMost - kQStages * kQBytes) / kTile;
+    static constexpr int kKStages = kKFit < kMaxStages ? kKFit : kMaxStages;
+    static_assert(kQStages >= 2 && kKStages >= 2, "shared memory");
+    static constexpr int kK = 0;
+    static constexpr int kQ = kK + kKStages * kTile;
+    static constexpr int kBar = kQ + kQStages * kQBytes;
+    static constexpr int kMisc = kBar + 64 * 8;              // TMEM address, abort flag
+    static constexpr int kRing = kMisc + 16;                 // kUnitSlots units
+    static constexpr int kLse = kRing + kUnitSlots * 64;     // kBufs x R, times log2 e
+    static constexpr int kSums = kLse + kBufs * R * 4;       // two units' sums of the second four warps
+    static constexpr int kBytes = kSums + 2 * kBK * 4;
+    static_assert(kLse % 16 == 0 && kBytes - kBar <= kSmall, "layout");
+    static constexpr int kAlloc = kBytes > 120 * 1024 ? kBytes : 120 * 1024;  // one CTA per SM
+};
+
+enum : int {
+    kBarKFull = 0,                         // + stage
+    kBarKEmpty = kBarKFull + kMaxStages,   // + stage
+    kBarQFull = kBarKEmpty + kMaxStages,   // + stage (4)
+    kBarQEmpty = kBarQFull + 4,            // + stage (4)
+    kBarSFull = kBarQEmpty + 4,            // + buffer
+    kBarSEmpty = kBarSFull + kBufs,        // + buffer: scores and LSE read
+    kBarLFull = kBarSEmpty + kBufs,        // + buffer
+    kBarSumFull = kBarLFull + kBufs,       // + slot (2)
+    kBarSumEmpty = kBarSumFull + 2,        // + slot (2)
+    kBarUnitFull = kBarSumEmpty + 2,            // + slot
+    kBarUnitEmpty = kBarUnitFull + kUnitSlots,  // + slot
+    kBarDrain = kBarUnitEmpty + kUnitSlots,
+    kNumBars = kBarDrain + 1,
+};
+static_assert(kNumBars <= 64, "barrier slots");
+
+// A tile of keys of K/V head h of sequence b, and its n tiles of rows from the first-th on
+// (tile r: tokens from r / subs * tpt on, heads from r mod subs * pf on).
+struct Unit {
+    int b, h, j;
+    int first, n;
+    int q0, nq, nk, q_off;  // token i of the sequence stands at key position i + q_off
+};
+static_assert(sizeof(Unit) <= 64, "ring slot");
+
+struct Seq {
+    int q0, nq, nk;
+};
+__device__ __forceinline__ Seq load_seq(int b, const Params &p) {
+    Seq s{0, 0, 0};
+    if (b >= p.B) return s;
+    s.q0 = min(max(p.cu_q[b], 0), p.total_q);
+    s.nq = min(max(p.cu_q[b + 1], s.q0), p.total_q) - s.q0;
+    s.nk = min(max(p.seq_k[b], 0), p.max_keys);
+    return s;
+}
+// The first tile of keys that a token of the sequence sees, and how many follow.
+__device__ __forceinline__ int first_tile(const Seq &s, const Params &p) {
+    return max(0, s.nk - s.nq - p.wl) / kBK;
+}
+__device__ __forceinline__ int key_tiles(const Seq &s, const Params &p) {
+    return s.nq == 0 || s.nk == 0 ? 0 : max(0, (s.nk - 1) / kBK - first_tile(s, p) + 1);
+}
+// Tokens lo .. hi (hi < lo: none) see a key of keys k0 .. k1.
+__device__ __forceinline__ void tokens_of(const Unit &u, int k0, int k1, const Params &p, int &lo, int &hi) {
+    lo = max(0, k0 - u.q_off - p.wr);
+    hi = min(u.nq - 1, k1 - u.q_off + p.wl);
+}
+
+__device__ __forceinline__ void record_timeout(const Params &p, volatile int *abort_flag, int role, int unit) {
+    *abort_flag = 1;
+    if (atomicCAS(p.status, 0u, kStatusTimeout) == 0u) {
+        p.status[1] = static_cast<unsigned>(role);
+        p.status[2] = static_cast<unsigned>(unit);
+        p.status[3] = blockIdx.x;
+        __threadfence();
+    }
+}
+
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
+    tmem_ld32(taddr, r);
+    tmem_ld_wait(r);
+}
+
+template <int D, int R, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ Params p) {
+    using L = Smem<D, R>;
+    using P = typename L::P;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *const smem = smem_raw;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::kBar;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+    auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    auto sK = [sbase](int t) { return sbase + L::kK + (t % L::kKStages) * L::kTile; };
+    auto sQ = [sbase](int t) { return sbase + L::kQ + (t % L::kQStages) * L::kQBytes; };
+    float *const lse_ring = reinterpret_cast<float *>(smem + L::kLse);
+    // (from one lane: the compiler then knows that the roles' branches are the warp's)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const uint64_t budget = p.wait_budget_ns;
+
+    if ((sbase & 1023u) != 0) {
+        after_previous();
+        if (threadIdx.x == 0) atomicCAS(p.status, 0u, kStatusLayout);
+        return;
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == kPlanWarp * 32) {
+        for (int s = 0; s < L::kKStages; ++s) {
+            mbar_init(bar(kBarKFull + s), 1);
+            mbar_init(bar(kBarKEmpty + s), 1);
+        }
+        for (int s = 0; s < L::kQStages; ++s) {
+            mbar_init(bar(kBarQFull + s), 1);
+            mbar_init(bar(kBarQEmpty + s), 1);
+        }
+        for (int s = 0; s < kBufs; ++s) {
+            mbar_init(bar(kBarSFull + s), 1);
+            mbar_init(bar(kBarSEmpty + s), 128);
+            mbar_init(bar(kBarLFull + s), 32);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(kBarSumFull + s), 128);
+            mbar_init(bar(kBarSumEmpty + s), 128);
+        }
+        for (int k = 0; k < kUnitSlots; ++k) {
+            mbar_init(bar(kBarUnitFull + k), 1);
+            mbar_init(bar(kBarUnitEmpty + k), kUnitConsumers);
+        }
+        mbar_init(bar(kBarDrain), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    after_previous();
+    let_next_start();
+    const bool idle = *tmem_slot != kTmem;
+    if (idle && threadIdx.x == 0) atomicCAS(p.status, 0u, kStatusLayout);
+
+    auto slot_of = [smem](int k) { return reinterpret_cast<Unit *>(smem + L::kRing + (k % kUnitSlots) * 64); };
+    auto wait = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag, budget)) != 0;
+    };
+    auto one = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    // The k-th unit of this CTA (every role walks the same ones). b < 0: no more.
+    auto take = [&](int k, bool &ok) -> Unit {
+        Unit u{};
+        u.b = -1;
+        const int slot = k % kUnitSlots;
+        ok = wait(kBarUnitFull + slot, (k / kUnitSlots) & 1);
+        if (!ok) return u;
+        u = *slot_of(k);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarUnitEmpty + slot));
+        u.b = one(u.b);
+        u.n = one(u.n);
+        return u;
+    };
+
+    if (idle) {
+        // (frees its tensor memory below)
+    } else if (warp == kPlanWarp) {
+        // ================================================================ units and key tiles
+        // Units are numbered sequence by sequence, head by head, tile by tile. Each lane holds
+        // one sequence of the 32 from b0 on: its units, and those before them from `base` on.
+        long long base = 0, unit = blockIdx.x;
+        int b0 = 0;
+        Seq s = load_seq(lane, p);
+        int tiles = key_tiles(s, p);
+        long long incl = static_cast<long long>(tiles) * p.H_kv;
+        auto scan = [&] {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+        };
+        scan();
+        int t = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            // ---- find it
+            Unit u{};
+            u.b = -1;
+            while (true) {
+                const unsigned hit = __ballot_sync(0xffffffffu, unit - base < incl);
+                if (hit != 0) {
+                    const int at = __ffs(hit) - 1;
+                    u.b = b0 + at;
+                    u.q0 = __shfl_sync(0xffffffffu, s.q0, at);
+                    u.nq = __shfl_sync(0xffffffffu, s.nq, at);
+                    u.nk = __shfl_sync(0xffffffffu, s.nk, at);
+                    const int n = __shfl_sync(0xffffffffu, tiles, at);
+                    const int x = static_cast<int>(unit - base - (__shfl_sync(0xffffffffu, incl, at) -
+                                                                  static_cast<long long>(n) * p.H_kv));
+                    u.h = x / n;
+                    u.q_off = u.nk - u.nq;
+                    u.j = x - u.h * n + first_tile(Seq{0, u.nq, u.nk}, p);
+                    int lo, hi;
+                    tokens_of(u, u.j * kBK, min(u.j * kBK + kBK, u.nk) - 1, p, lo, hi);
+                    u.first = lo / p.tpt * p.subs;
+                    u.n = hi < lo ? 0 : (hi / p.tpt + 1) * p.subs - u.first;
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
+                b0 += 32;
+                if (b0 >= p.B) break;
+                s = load_seq(b0 + lane, p);
+                tiles = key_tiles(s, p);
+                incl = static_cast<long long>(tiles) * p.H_kv;
+                scan();
+            }
+            unit += gridDim.x;
+            const int slot = k % kUnitSlots;
+            ok = wait(kBarUnitEmpty + slot, ((k / kUnitSlots) & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) {
+                *slot_of(k) = u;
+                mbar_arrive(bar(kBarUnitFull + slot));
+            }
+            __syncwarp();
+            if (u.b < 0) break;
+            if (u.n == 0) continue;
+            // ---- its keys: chunk `lane` of the tile
+            const int k0 = u.j * kBK + lane * p.chunk;
+            const bool need = lane * p.chunk < kBK && k0 < u.nk;
+            int page = 0;
+            if (need) {
+                page = p.table[static_cast<size_t>(u.b) * p.max_pages + (k0 >> p.page_log2)];
+                // a page number outside the cache reads as zeros
+                page = page >= 0 && page < p.num_pages ? page * p.page_step + u.h * p.head_step : p.page_none;
+            }
+            const unsigned all = __ballot_sync(0xffffffffu, need);
+            const int st = t % L::kKStages;
+            ok = wait(kBarKEmpty + st, ((t / L::kKStages) & 1) ^ 1);
+            if (!ok) break;
+            if (t != p.fault_skip_k) {
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar(kBarKFull + st),
+                                          static_cast<uint32_t>(__popc(all)) * p.chunk * (P::kGroup / 8));
+                __syncwarp();
+                if (need)
+                    paged::tma_load_5d(sK(t) + lane * p.chunk * (P::kGroup / 8), &tmK, bar(kBarKFull + st), 0, 0, 0,
+                                       (k0 & ((1 << p.page_log2) - 1)) >> 3, page);
+                __syncwarp();
+            }
+            ++t;
+        }
+        if (lane == 0) {
+            if (!ok) record_timeout(p, abort_flag, kRoleTma, -1);
+            for (int s2 = 0; s2 < L::kKStages; ++s2)
+                if (t > s2) {
+                    const int last = t - 1 - ((t - 1 - s2) % L::kKStages);
+                    mbar_wait_bounded(bar(kBarKFull + s2), (last / L::kKStages) & 1, nullptr, budget);
+                }
+        }
+    } else if (warp == kQWarp) {
+        // ================================================================ queries and their LSE
+        int i = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Unit u = take(k, ok);
+            if (!ok || u.b < 0) break;
+            for (int x = 0; x < u.n; ++x, ++i) {
+                const int r = u.first + x, t0 = r / p.subs * p.tpt;
+                const int h0 = u.h * p.pf * p.subs + r % p.subs * p.pf;
+                const int st = i % L::kQStages, buf = i % kBufs;
+                ok = wait(kBarQEmpty + st, ((i / L::kQStages) & 1) ^ 1);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(kBarQFull + st), static_cast<uint32_t>(p.pf * p.tpt) *
+                                                                              P::kRowBytes * P::kRegions);
+                __syncwarp();
+                if (lane < P::kRegions)
+                    tma_load_3d(sQ(i) + lane * L::kQRegion, &tmQ, bar(kBarQFull + st), P::kCols * lane, h0, u.q0 + t0);
+                __syncwarp();
+                // row c: token c / pf, head c mod pf; tokens that saw nothing get +infinity, which
+                // makes every weight 0
+                float v[(R + 31) / 32];
+#pragma unroll
+                for (int y = 0; y < (R + 31) / 32; ++y) {
+                    const int c = lane + 32 * y, tok = c / p.pf;
+                    v[y] = INFINITY;
+                    if (tok < p.tpt && t0 + tok < u.nq) {
+                        v[y] = p.LSE[(static_cast<size_t>(u.q0) + t0 + tok) * p.H + h0 + (c - tok * p.pf)] *
+                               1.4426950408889634f;
+                        if (v[y] == -INFINITY) v[y] = INFINITY;
+                    }
+                }
+                ok = wait(kBarSEmpty + buf, ((i / kBufs) & 1) ^ 1);
+                if (!ok) break;
+#pragma unroll
+                for (int y = 0; y < (R + 31) / 32; ++y)
+                    if (lane + 32 * y < R) lse_ring[buf * R + lane + 32 * y] = v[y];
+                mbar_arrive(bar(kBarLFull + buf));
+            }
+        }
+        if (lane == 0) {
+            if (!ok) record_timeout(p, abort_flag, kRoleTma, -2);
+            for (int s = 0; s < L::kQStages; ++s)
+                if (i > s) {
+                    const int last = i - 1 - ((i - 1 - s) % L::kQStages);
+                    mbar_wait_bounded(bar(kBarQFull + s), (last / L::kQStages) & 1, nullptr, budget);
+                }
+        }
+    } else if (warp == kIssueWarp) {
+        // ================================================================ S^T = K Q^T
+        constexpr uint32_t idesc = idesc_f16_ab(BF16, kBK, R, false, false);
+        constexpr int kSteps = P::kCols / 16;  // K-steps of 16 columns per region
+        int t = 0, i = 0, k = 0;
+        bool ok = true;
+        for (; ok; ++k) {
+            const Unit u = take(k, ok);
+            if (!ok || u.b < 0) break;
+            if (u.n == 0) continue;
+            ok = wait(kBarKFull + t % L::kKStages, (t / L::kKStages) & 1);
+            const uint64_t dk = paged::tile_desc<P::kRowBytes>(sK(t), 16, P::kGroup);
+            for (int x = 0; ok && x < u.n; ++x, ++i) {
+                ok = wait(kBarQFull + i % L::kQStages, (i / L::kQStages) & 1);
+                if (ok) ok = wait(kBarSEmpty + i % kBufs, ((i / kBufs) & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dq = paged::tile_desc<P::kRowBytes>(sQ(i), 16, P::kAtom);
+                const uint32_t d = kTmem + (i % kBufs) * R;
+                if (elect_one()) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)
+                        umma_f16_ss(d, dk + (c / kSteps) * (P::kAtom >> 4) + (c % kSteps) * 2,
+                                    dq + (c / kSteps) * (L::kQRegion >> 4) + (c % kSteps) * 2, idesc, c > 0 ? 1u : 0u);
+                    umma_commit(bar(kBarSFull + i % kBufs));
+                    umma_commit(bar(kBarQEmpty + i % L::kQStages));
+                }
+                __syncwarp();
+            }
+            if (ok) {
+                if (elect_one()) umma_commit(bar(kBarKEmpty + t % L::kKStages));
+                __syncwarp();
+                ++t;
+            }
+        }
+        if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleMma, k);
+        if (elect_one()) umma_commit(bar(kBarDrain));
+        __syncwarp();
+        if (lane == 0) mbar_wait_bounded(bar(kBarDrain), 0, nullptr, budget);
+        __syncwarp();
+    } else {
+        // ================================================================ sums over rows
+        const int half = warp >> 2;  // which four warps
+        const int own = threadIdx.x & 127;
+        const uint32_t tl = kTmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const float sl2 = p.scale_log2;
+        float *const sums = reinterpret_cast<float *>(smem + L::kSums);
+        int i = 0, k = 0, joined = 0;  // tiles of rows; units; those that both halves shared
+        bool ok = true;
+        for (; ok; ++k) {
+            const Unit u = take(k, ok);
+            if (!ok || u.b < 0) break;
+            if (u.n == 0) continue;
+            if (u.n == 1 && (k & 1) != half) {  // the others' unit
+                ++i;
+                continue;
+            }
+            const int key = u.j * kBK + own;
+            const bool there = key < u.nk;
+            int page = -1;
+            if (there && (u.n == 1 || half == 0))
+                page = p.table[static_cast<size_t>(u.b) * p.max_pages + (key >> p.page_log2)];
+            // tokens that see this key, and those that see every key of the tile
+            int lo, hi, all_lo, all_hi, x1, x2;
+            tokens_of(u, key, key, p, lo, hi);
+            tokens_of(u, u.j * kBK + kBK - 1, u.j * kBK + kBK - 1, p, all_lo, x1);
+            tokens_of(u, u.j * kBK, u.j * kBK, p, x2, all_hi);
+            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+            const int start = u.n == 1 ? 0 : half, step = u.n == 1 ? 1 : 2;
+            for (int x = start; ok && x < u.n; x += step) {
+                const int at = i + x, buf = at % kBufs, t0 = (u.first + x) / p.subs * p.tpt;
+                ok = wait(kBarLFull + buf, (at / kBufs) & 1);
+                if (ok) ok = wait(kBarSFull + buf, (at / kBufs) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                // rows that see this key, and whether that is every row of the tile for all keys (rows
+                // behind the sequence's last token may hold anything: they are not looked at)
+                const int c_lo = (lo - t0) * p.pf, c_hi = min(hi - t0 + 1, p.tpt) * p.pf;
+                const bool whole = t0 >= all_lo && t0 + p.tpt - 1 <= all_hi && p.tpt * p.pf == R;
+                const float *lse = lse_ring + buf * R;
+                constexpr int kCols = R < 32 ? R : 32;
+#pragma unroll
+                for (int h = 0; h < R; h += kCols) {
+                    uint32_t r[kCols];
+                    ld_cols(tl + buf * R + h, r);
+                    float y[kCols];
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(lse + h + c);
+                        y[c] = __uint_as_float(r[c]), y[c + 1] = __uint_as_float(r[c + 1]);
+                        y[c + 2] = __uint_as_float(r[c + 2]), y[c + 3] = __uint_as_float(r[c + 3]);
+                        ffma2(y[c], y[c + 1], sl2, sl2, -v.x, -v.y);
+                        ffma2(y[c + 2], y[c + 3], sl2, sl2, -v.z, -v.w);
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c)
+                            if (h + c < c_lo || h + c >= c_hi) y[c] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) y[c] = ex2_approx(y[c]);
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 4) {
+                        fadd2(a0, a1, y[c], y[c + 1]);
+                        fadd2(a2, a3, y[c + 2], y[c + 3]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kBarSEmpty + buf));
+            }
+            i += u.n;
+            if (!ok) break;
+            float sum = (a0 + a1) + (a2 + a3);
+            if (u.n > 1) {
+                // the second four warps hand their sums to the first
+                const int slot = joined % 2;
+                if (half == 1) {
+                    ok = wait(kBarSumEmpty + slot, ((joined / 2) & 1) ^ 1);
+                    if (!ok) break;
+                    sums[slot * kBK + own] = sum;
+                    mbar_arrive(bar(kBarSumFull + slot));
+                } else {
+                    ok = wait(kBarSumFull + slot, (joined / 2) & 1);
+                    if (!ok) break;
+                    sum += sums[slot * kBK + own];
+                    mbar_arrive(bar(kBarSumEmpty + slot));
+                }
+                ++joined;
+            }
+            if (there && page >= 0 && page < p.num_pages) {
+                float *w = p.weights + ((static_cast<size_t>(page) * p.H_kv + u.h) << p.page_log2) +
+                           (key & ((1 << p.page_log2) - 1));
+                if (key >= u.q_off)
+                    *w = sum;
+                else
+                    atomicAdd(w, sum);
+            }
+        }
+        if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleSum, k);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(*tmem_slot, kTmemCols);
+    }
+}
+
+}  // namespace weights
+}  // namespace fa
