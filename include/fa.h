@@ -577,6 +577,28 @@ fa_status fa_paged_weights(const void *Q, const float *LSE, float *weights, cons
                            fa_mask_mode mask_mode, int64_t window_left, int64_t window_right,
                            void *stream);
 
+/*
+ * fa_paged_evict -- cut the sequences of a paged cache back to `budget` keys by the weight
+ * that each key has gathered. For sequence b of n = seqlens_k[b] keys, n > budget, every K/V
+ * head keeps its first `first` keys, its last `recent` ones, and of those between the
+ * budget - first - recent with the largest weights (of equal ones those at lower positions;
+ * NaN counts as -infinity). What is kept moves, in its order, to positions 0 .. budget - 1 of
+ * the sequence's pages: keys, values and weights alike, each head its own. Shorter sequences, and
+ * what the slots behind position budget - 1 hold, are left as they are. seqlens_out[b] =
+ * min(n, budget); it must not overlap seqlens_k.
+ *
+ * Stored keys keep the rotary positions they were stored with, so later tokens' positions are
+ * no longer their places in the cache: rotate those with fa_qk_norm_rope and explicit positions,
+ * and append with rope = NULL. Masks of later calls count places (causal stays what it is).
+ * A page that two sequences of the batch share ends with either's rows. weights as
+ * fa_paged_weights leaves it; K and V of the cache share no element. 0 <= first, recent,
+ * first + recent <= budget. One kernel launch, no workspace. Everything else as
+ * fa_paged_append.
+ */
+fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights, const int32_t *block_table,
+                         int64_t max_pages, const int32_t *seqlens_k, int32_t *seqlens_out, int64_t B,
+                         int64_t budget, int64_t first, int64_t recent, void *stream);
+
 /* Static, NUL-terminated description of a status code. Never NULL. */
 const char *fa_status_string(fa_status status);
 

@@ -20,4 +20,4 @@ from .binding import (NormRope, PagedCache, fa_forward_paged,  # noqa: F401
                       rope_frequencies, rope_steps)
 from .binding import (LatentCache, fa_forward_latent, fa_forward_latent_workspace_bytes,  # noqa: F401
                       fa_latent_append, forward_latent)
-from .binding import fa_paged_weights  # noqa: F401
+from .binding import fa_paged_evict, fa_paged_weights  # noqa: F401

@@ -159,6 +159,9 @@ def load_library_at(path: str) -> ctypes.CDLL:
         cache, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p] + [
         ctypes.c_int64] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                ctypes.c_void_p]
+    lib.fa_paged_evict.restype = ctypes.c_int
+    lib.fa_paged_evict.argtypes = [cache, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64] + [
+        ctypes.c_void_p] * 2 + [ctypes.c_int64] * 4 + [ctypes.c_void_p]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_status_string.argtypes = [ctypes.c_int]
     lib.fa_sync_status.restype = ctypes.c_int
@@ -1000,5 +1003,25 @@ def fa_paged_weights(q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, 
         q.data_ptr(), lse.data_ptr(), weights.data_ptr(), cache.address, table, pages, cu, lens, B,
         shape[1], shape[0], float(scale), _MASKS[mask_mode], int(window_left), int(window_right),
         _stream_handle(stream))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def fa_paged_evict(cache: PagedCache, weights: torch.Tensor, block_table: torch.Tensor,
+                   seqlens_k: torch.Tensor, seqlens_out: torch.Tensor, budget: int, first: int = 0,
+                   recent: int = 0, stream=None) -> None:
+    """Enqueue fa_paged_evict: cut every sequence of seqlens_k (B,) int32 that has more than
+    `budget` keys back to them, in place in the pages of block_table (B, max_pages) int32; each
+    K/V head keeps its first `first` and last `recent` keys and the largest of weights
+    (num_pages, H_kv, page_size) float32 between. seqlens_out (B,) int32 gets the lengths."""
+    what = "fa_paged_evict"
+    _check_weights(weights, cache, what)
+    shape, B = block_table.shape, seqlens_k.numel()
+    if len(shape) != 2 or shape[0] != B or B < 1:
+        raise FaError(FA_ERR_INVALID_ARG, what)
+    rc = (_lib or load_library()).fa_paged_evict(
+        cache.address, weights.data_ptr(), _int32(block_table, B * shape[1], what), shape[1],
+        _int32(seqlens_k, B, what), _int32(seqlens_out, B, what), B, int(budget), int(first),
+        int(recent), _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, what)
