@@ -93,11 +93,11 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
     p.budget = static_cast<int>(budget < most ? budget : most);
     p.first = static_cast<int>(first < most ? first : most);
     p.recent = static_cast<int>(recent < most ? recent : most);
-    // CTAs per sequence and head: what fills the SMs twice over, while a round of theirs is not
-    // longer than the cache
+    // CTAs per sequence and head: what the SMs hold at once (one CTA each), while a round of theirs
+    // is not longer than the cache
     int ctas = 1;
     const int64_t units = B * cache->H_kv;
-    while (ctas < kMaxCluster && units * ctas < 2 * di.sm_count && static_cast<int64_t>(ctas) * p.slots < max_keys)
+    while (ctas < kMaxCluster && units * ctas * 2 <= di.sm_count && static_cast<int64_t>(ctas) * p.slots < max_keys)
         ctas *= 2;
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,8 +15,9 @@
 // The next round's rows are loaded (asynchronous copies to shared memory) before the
 // barrier: they lie behind everything that this round writes.
 //
-// Bound by memory: rows are read and written once, weights read once (their ordered form stays in
-// shared memory as far as it fits).
+// Bound by memory: rows are read and written once, weights read once. Weights and page numbers
+// stay in shared memory as far as they fit, so that nothing but the rows is waited for between
+// rounds, and rounds are as large as what is left allows.
 #pragma once
 
 #include <cstdint>
@@ -31,8 +32,9 @@ namespace evict {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBufBytes = 48 * 1024;  // rows of a round (two rounds are in flight)
-constexpr int kKept = 8192;           // ordered weights that stay in shared memory
+constexpr int kBufBytes = 64 * 1024;  // rows of a round (two rounds are in flight)
+constexpr int kKept = 16384;          // weights of this CTA that stay in shared memory
+constexpr int kPages = 2048;          // page numbers that do
 
 struct Params {
     uint16_t *k, *v;
@@ -46,7 +48,8 @@ struct Params {
 };
 
 struct Shared {
-    uint32_t keys[kKept];
+    float w_all[kKept];
+    int pages[kPages];
     unsigned hist[2][256];          // of this CTA, read by the cluster
     unsigned part[kWarps / 4][256];
     int counts[2][kMaxCluster];     // kept rows of each CTA in a round, written by each
@@ -109,8 +112,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
     const int *table = p.table + static_cast<size_t>(b) * p.max_pages;
     const int page_mask = (1 << p.page_log2) - 1;
     // page of slot j, or -1 when its number lies outside the cache
+    for (int i = tid; i < kPages && i <= (n - 1) >> p.page_log2; i += kThreads) sh.pages[i] = table[i];
+    __syncthreads();
     auto page_of = [&](int j) {
-        const int x = table[j >> p.page_log2];
+        const int i = j >> p.page_log2, x = i < kPages ? sh.pages[i] : table[i];
         return x >= 0 && x < p.num_pages ? x : -1;
     };
     auto weight_at = [&](int page, int j) {
@@ -129,12 +134,22 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
     int want = p.budget - p.first - p.recent;
     uint32_t T = 0xffffffffu;  // kept: above T, or equal and at J or before
     int J = -1;
-    if (want > 0) {
-        for (int x = tid; x < own && x < kKept; x += kThreads) {
-            const int j = slot(x);
-            sh.keys[x] = j >= mid0 && j < mid1 ? ordered(weight_of(j)) : 0;
+    // weights of this CTA's slots, several loads of a thread at a time
+    constexpr int kBatch = 8;
+    for (int x0 = 0; x0 < own && x0 < kKept; x0 += kBatch * kThreads) {
+        float w[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int x = x0 + i * kThreads + tid, j = slot(x);
+            w[i] = x < own && x < kKept && j < n ? weight_of(j) : 0.f;
         }
-        auto key_of = [&](int x, int j) { return x < kKept ? sh.keys[x] : ordered(weight_of(j)); };
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (x0 + i * kThreads + tid < kKept) sh.w_all[x0 + i * kThreads + tid] = w[i];
+    }
+    __syncthreads();
+    auto own_weight = [&](int x, int j) { return x < kKept ? sh.w_all[x] : weight_of(j); };
+    if (want > 0) {
         T = 0;
         J = 0x7fffffff;
         int top = 24;  // of the index
@@ -149,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
             for (int x = tid; x < own; x += kThreads) {
                 const int j = slot(x);
                 if (j < mid0 || j >= mid1) continue;
-                const uint32_t m = key_of(x, j);
+                const uint32_t m = ordered(own_weight(x, j));
                 const uint32_t v = by_index ? static_cast<uint32_t>(j) : m;
                 const uint32_t known = by_index ? static_cast<uint32_t>(J0) : T;
                 if ((by_index && m != T) || (shift < 24 && v >> (shift + 8) != known >> (shift + 8))) continue;
@@ -161,7 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
                 for (int i = 0; i < kWarps / 4; ++i) c += sh.part[i][tid];
                 sh.hist[pass & 1][tid] = c;
             }
-            cluster_sync();
+            if (ctas > 1)
+                cluster_sync();
+            else
+                __syncthreads();
             // digit 255 - tid of a weight (the largest first), tid of an index
             const int digit = by_index ? tid : 255 - tid;
             unsigned c = 0;
@@ -208,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
         int page = -1;
         if (tid < S && j < n) {
             page = page_of(j);
-            w = page < 0 ? 0.f : p.weights[weight_at(page, j)];
+            w = own_weight(x, j);
             kept = j < mid0 || j >= mid1;
             if (!kept) {
-                const uint32_t m = x < kKept && p.budget > p.first + p.recent ? sh.keys[x] : ordered(w);
+                const uint32_t m = ordered(w);
                 kept = m > T || (m == T && j <= J);
             }
         }
@@ -249,8 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
         } else {
             copies_wait<0>();
         }
-        __syncthreads();
-        cluster_sync();  // this round has been read by all
+        // this round has been read by all
+        if (ctas > 1)
+            cluster_sync();
+        else
+            __syncthreads();
         int dest = before;
         for (int r = 0; r < ctas; ++r) {
             const int c = sh.counts[t & 1][r];
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
         __syncthreads();
         count = next;
     }
-    cluster_sync();  // nobody leaves while its shared memory may be read or written
+    if (ctas > 1) cluster_sync();  // nobody leaves while its shared memory may be read or written
 }
 
 }  // namespace evict

@@ -171,7 +171,7 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_latent_cache *cache, 
     p.B = static_cast<int>(B);
     p.H = static_cast<int>(H);
     p.group = group;
-    p.by_H = fa::latent::divisor(H);
+    p.by_H = fa::divisor(H);
     while ((1 << p.rb_log2) < r * group) ++p.rb_log2;
     p.total_q = static_cast<int>(total_q);
     p.max_pages = static_cast<int>(max_pages);

@@ -45,6 +45,7 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "fa_divisor.cuh"
 #include "fa_paged_kernel.cuh"
 #include "fa_pdl.cuh"
 #include "ptx.cuh"
@@ -69,20 +70,6 @@ constexpr unsigned kStatusLayout = 2;  // shared memory base not 1024-aligned
 constexpr uint32_t kTmem = 0;  // all columns of tensor memory are allocated: they start at 0
 
 enum : int { kRoleSoftmax = 1, kRoleTma = 2, kRoleMma = 3 };
-
-// Division of 0 <= n < 2^31 by d as a product: mul = ceil(2^s / d), s = 31 + ceil(log2 d).
-struct Divisor {
-    uint32_t mul;
-    int shift;
-    __device__ __forceinline__ int of(int n) const {
-        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
-    }
-};
-inline Divisor divisor(int64_t d) {
-    int l = 0;
-    while ((int64_t{1} << l) < d) ++l;
-    return Divisor{static_cast<uint32_t>(((uint64_t{1} << (31 + l)) + d - 1) / d), 31 + l};
-}
 
 struct Params {
     void *O;

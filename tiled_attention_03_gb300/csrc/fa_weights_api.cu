@@ -145,6 +145,9 @@ extern "C" fa_status fa_paged_weights(const void *Q, const float *LSE, float *we
     p.pf = static_cast<int>(pf);
     p.subs = static_cast<int>(group / pf);
     p.tpt = static_cast<int>(tpt);
+    p.by_heads = fa::divisor(H_kv);
+    p.by_tpt = fa::divisor(tpt);
+    p.by_subs = fa::divisor(group / pf);
     p.total_q = static_cast<int>(total_q);
     p.max_pages = static_cast<int>(max_pages);
     while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;

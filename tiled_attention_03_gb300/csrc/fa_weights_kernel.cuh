@@ -21,8 +21,9 @@
 // row: 128 x 128 of them occupy the SM's exponential unit for 1,024 cycles, where the
 // products (d = 128) take 512.
 //
-// Warps (352 threads): 0-3 and 4-7 sum alternate tiles of rows (of units with one: alternate
-// units), 8 finds units and loads keys, 9 issues the products, 10 loads queries and their LSE.
+// Warps (384 threads): 0-3 and 4-7 sum alternate tiles of rows (of units with one: alternate
+// units), 8 finds units, 9 issues the products, 10 loads queries and their LSE, 11 loads keys;
+// the loaders ask for the next page numbers and LSEs before they wait for the present ones.
 // Every wait is bounded; on expiry the CTA records the failure, drains its copies and
 // products, frees its tensor memory and returns.
 #pragma once
@@ -30,6 +31,7 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "fa_divisor.cuh"
 #include "fa_paged_kernel.cuh"
 #include "fa_pdl.cuh"
 #include "ptx.cuh"
@@ -38,12 +40,13 @@ namespace fa {
 namespace weights {
 
 constexpr int kBK = 128;  // keys per tile
-constexpr int kThreads = 352;
-constexpr int kPlanWarp = 8, kIssueWarp = 9, kQWarp = 10;
-constexpr int kUnitSlots = 4;
-constexpr int kUnitConsumers = 10;
+constexpr int kThreads = 384;
+constexpr int kPlanWarp = 8, kIssueWarp = 9, kQWarp = 10, kKWarp = 11;
+constexpr int kUnitSlots = 8;
+constexpr int kUnitConsumers = 11;  // warps that take the units: all but the one that finds them
 constexpr int kMaxStages = 8;
 constexpr int kBufs = 4;  // of scores and of their rows' LSE
+constexpr int kByHand = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmem = 0;  // all columns are allocated: they start at 0
 constexpr unsigned kStatusTimeout = 4;
@@ -58,6 +61,7 @@ struct Params {
     int total_q, max_pages, page_log2, num_pages, max_keys;
     int chunk;         // tokens per TMA box: min(page size, kBK)
     int page_step, head_step, page_none;  // the map's last coordinate; past its end
+    Divisor by_heads, by_tpt, by_subs;  // by H_kv, tpt and subs
     int wl, wr;        // key j visible to the query at position i iff i - wl <= j <= i + wr
     float scale_log2;
     unsigned long long wait_budget_ns;
@@ -71,7 +75,7 @@ struct Smem {
     static constexpr int kTile = kBK / 8 * P::kGroup;
     static constexpr int kQRegion = R * P::kRowBytes;
     static constexpr int kQBytes = P::kRegions * kQRegion;
-    static constexpr int kSmall = 4096;
+    static constexpr int kSmall = 4608;
     static constexpr int kMost = 227 * 1024 - kSmall;
     // as many tiles of queries as leave four of keys (two where a tile of keys is 64 KB)
     static constexpr int kQFit = (kMost - (D == 256 ? 2 : 4) * kTile) / kQBytes;
@@ -82,7 +86,7 @@ struct Smem {
     static constexpr int kK = 0;
     static constexpr int kQ = kK + kKStages * kTile;
     static constexpr int kBar = kQ + kQStages * kQBytes;
-    static constexpr int kMisc = kBar + 64 * 8;              // TMEM address, abort flag
+    static constexpr int kMisc = kBar + 72 * 8;              // TMEM address, abort flag
     static constexpr int kRing = kMisc + 16;                 // kUnitSlots units
     static constexpr int kLse = kRing + kUnitSlots * 64;     // kBufs x R, times log2 e
     static constexpr int kSums = kLse + kBufs * R * 4;       // two units' sums of the second four warps
@@ -106,7 +110,7 @@ enum : int {
     kBarDrain = kBarUnitEmpty + kUnitSlots,
     kNumBars = kBarDrain + 1,
 };
-static_assert(kNumBars <= 64, "barrier slots");
+static_assert(kNumBars <= 72, "barrier slots");
 
 // A tile of keys of K/V head h of sequence b, and its n tiles of rows from the first-th on
 // (tile r: tokens from r / subs * tpt on, heads from r mod subs * pf on).
@@ -149,6 +153,35 @@ __device__ __forceinline__ void record_timeout(const Params &p, volatile int *ab
         p.status[3] = blockIdx.x;
         __threadfence();
     }
+}
+
+// (a, b) <- (2^a, 2^b) by multiply-adds: 2^x = 2^i 2^f with i the nearest integer and 2^f on
+// [-1/2, 1/2] by the polynomial of degree 5 of least relative error (7.5e-8, found by exchange). x
+// is cut to [-126, 128]: below, 2^-126 adds nothing to a sum that is not as small; above, the
+// result is infinite as it should be. NaN stays NaN.
+__device__ __forceinline__ void exp2_pair(float &a, float &b) {
+    constexpr float kShift = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-126.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-126.f));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(128.f));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(128.f));
+    float ta = a, tb = b;
+    fadd2(ta, tb, kShift, kShift);
+    float fa = ta, fb = tb;
+    fadd2(fa, fb, -kShift, -kShift);
+    ffma2(fa, fb, -1.f, -1.f, a, b);  // x - i
+    float ya = 0.00132764725f, yb = 0.00132764725f;
+    ffma2(ya, yb, fa, fb, 0.00967554096f, 0.00967554096f);
+    ffma2(ya, yb, fa, fb, 0.0555071309f, 0.0555071309f);
+    ffma2(ya, yb, fa, fb, 0.240221202f, 0.240221202f);
+    ffma2(ya, yb, fa, fb, 0.693146944f, 0.693146944f);
+    ffma2(ya, yb, fa, fb, 1.00000012f, 1.00000012f);
+    // the integer's low bits, as an exponent
+    const float sa = __int_as_float((__float_as_int(ta) << 23) + 0x3f800000);
+    const float sb = __int_as_float((__float_as_int(tb) << 23) + 0x3f800000);
+    fmul2(ya, yb, sa, sb);
+    a = ya;
+    b = yb;
 }
 
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
@@ -255,9 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (idle) {
         // (frees its tensor memory below)
     } else if (warp == kPlanWarp) {
-        // ================================================================ units and key tiles
-        // Units are numbered sequence by sequence, head by head, tile by tile. Each lane holds
-        // one sequence of the 32 from b0 on: its units, and those before them from `base` on.
+        // ================================================================ units
+        // Units are numbered sequence by sequence, tile by tile, head by head (the heads of a tile lie
+        // beside each other, and CTAs side by side read them at the same time). Each lane holds one
+        // sequence of the 32 from b0 on: its units, and those before them from `base` on.
         long long base = 0, unit = blockIdx.x;
         int b0 = 0;
         Seq s = load_seq(lane, p);
@@ -271,10 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         scan();
-        int t = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            // ---- find it
             Unit u{};
             u.b = -1;
             while (true) {
@@ -288,13 +320,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = __shfl_sync(0xffffffffu, tiles, at);
                     const int x = static_cast<int>(unit - base - (__shfl_sync(0xffffffffu, incl, at) -
                                                                   static_cast<long long>(n) * p.H_kv));
-                    u.h = x / n;
+                    const int y = p.by_heads.of(x);
+                    u.h = x - y * p.H_kv;
                     u.q_off = u.nk - u.nq;
-                    u.j = x - u.h * n + first_tile(Seq{0, u.nq, u.nk}, p);
+                    u.j = y + first_tile(Seq{0, u.nq, u.nk}, p);
                     int lo, hi;
                     tokens_of(u, u.j * kBK, min(u.j * kBK + kBK, u.nk) - 1, p, lo, hi);
-                    u.first = lo / p.tpt * p.subs;
-                    u.n = hi < lo ? 0 : (hi / p.tpt + 1) * p.subs - u.first;
+                    u.first = p.by_tpt.of(lo) * p.subs;
+                    u.n = hi < lo ? 0 : (p.by_tpt.of(hi) + 1) * p.subs - u.first;
                     break;
                 }
                 base += __shfl_sync(0xffffffffu, incl, 31);
@@ -315,17 +348,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (u.b < 0) break;
-            if (u.n == 0) continue;
-            // ---- its keys: chunk `lane` of the tile
-            const int k0 = u.j * kBK + lane * p.chunk;
-            const bool need = lane * p.chunk < kBK && k0 < u.nk;
-            int page = 0;
-            if (need) {
-                page = p.table[static_cast<size_t>(u.b) * p.max_pages + (k0 >> p.page_log2)];
-                // a page number outside the cache reads as zeros
-                page = page >= 0 && page < p.num_pages ? page * p.page_step + u.h * p.head_step : p.page_none;
+        }
+        if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleTma, -3);
+    } else if (warp == kKWarp) {
+        // ================================================================ key tiles
+        bool ok = true;
+        int k = 0, t = 0;
+        // The next unit with rows: its chunk `lane` of the tile, and that chunk's page.
+        struct Tile {
+            int b, h, k0, page;
+            bool need;
+        };
+        auto next = [&]() -> Tile {
+            Tile n{-1, 0, 0, 0, false};
+            while (true) {
+                const Unit u = take(k, ok);
+                ++k;
+                if (!ok || u.b < 0) return n;
+                if (u.n == 0) continue;
+                n.b = u.b;
+                n.h = u.h;
+                n.k0 = u.j * kBK + lane * p.chunk;
+                n.need = lane * p.chunk < kBK && n.k0 < u.nk;
+                if (n.need) n.page = p.table[static_cast<size_t>(u.b) * p.max_pages + (n.k0 >> p.page_log2)];
+                return n;
             }
-            const unsigned all = __ballot_sync(0xffffffffu, need);
+        };
+        Tile now = next();
+        while (ok && now.b >= 0) {
+            const Tile after = next();
+            if (!ok) break;
+            // a page number outside the cache reads as zeros
+            const int page = now.page >= 0 && now.page < p.num_pages ? now.page * p.page_step + now.h * p.head_step
+                                                                     : p.page_none;
+            const unsigned all = __ballot_sync(0xffffffffu, now.need);
             const int st = t % L::kKStages;
             ok = wait(kBarKEmpty + st, ((t / L::kKStages) & 1) ^ 1);
             if (!ok) break;
@@ -334,12 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(bar(kBarKFull + st),
                                           static_cast<uint32_t>(__popc(all)) * p.chunk * (P::kGroup / 8));
                 __syncwarp();
-                if (need)
+                if (now.need)
                     paged::tma_load_5d(sK(t) + lane * p.chunk * (P::kGroup / 8), &tmK, bar(kBarKFull + st), 0, 0, 0,
-                                       (k0 & ((1 << p.page_log2) - 1)) >> 3, page);
+                                       (now.k0 & ((1 << p.page_log2) - 1)) >> 3, page);
                 __syncwarp();
             }
             ++t;
+            now = after;
         }
         if (lane == 0) {
             if (!ok) record_timeout(p, abort_flag, kRoleTma, -1);
@@ -351,43 +408,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kQWarp) {
         // ================================================================ queries and their LSE
-        int i = 0;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            const Unit u = take(k, ok);
-            if (!ok || u.b < 0) break;
-            for (int x = 0; x < u.n; ++x, ++i) {
-                const int r = u.first + x, t0 = r / p.subs * p.tpt;
-                const int h0 = u.h * p.pf * p.subs + r % p.subs * p.pf;
-                const int st = i % L::kQStages, buf = i % kBufs;
-                ok = wait(kBarQEmpty + st, ((i / L::kQStages) & 1) ^ 1);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(kBarQFull + st), static_cast<uint32_t>(p.pf * p.tpt) *
-                                                                              P::kRowBytes * P::kRegions);
-                __syncwarp();
-                if (lane < P::kRegions)
-                    tma_load_3d(sQ(i) + lane * L::kQRegion, &tmQ, bar(kBarQFull + st), P::kCols * lane, h0, u.q0 + t0);
-                __syncwarp();
-                // row c: token c / pf, head c mod pf; tokens that saw nothing get +infinity, which
-                // makes every weight 0
-                float v[(R + 31) / 32];
+        int k = 0, i = 0;
+        constexpr int kOwn = (R + 31) / 32;
+        // this lane's rows of a tile: token and head
+        int tok[kOwn], head[kOwn];
 #pragma unroll
-                for (int y = 0; y < (R + 31) / 32; ++y) {
-                    const int c = lane + 32 * y, tok = c / p.pf;
-                    v[y] = INFINITY;
-                    if (tok < p.tpt && t0 + tok < u.nq) {
-                        v[y] = p.LSE[(static_cast<size_t>(u.q0) + t0 + tok) * p.H + h0 + (c - tok * p.pf)] *
-                               1.4426950408889634f;
-                        if (v[y] == -INFINITY) v[y] = INFINITY;
-                    }
-                }
-                ok = wait(kBarSEmpty + buf, ((i / kBufs) & 1) ^ 1);
-                if (!ok) break;
-#pragma unroll
-                for (int y = 0; y < (R + 31) / 32; ++y)
-                    if (lane + 32 * y < R) lse_ring[buf * R + lane + 32 * y] = v[y];
-                mbar_arrive(bar(kBarLFull + buf));
+        for (int y = 0; y < kOwn; ++y) {
+            tok[y] = (lane + 32 * y) / p.pf;
+            head[y] = lane + 32 * y - tok[y] * p.pf;
+        }
+        Unit u{};
+        int x = 0, t0 = -1, h0 = 0, row0 = 0;  // the next tile of rows: t0 < 0: none
+        float v[kOwn];                         // its LSEs
+        auto next = [&] {
+            t0 = -1;
+            while (x >= u.n) {
+                u = take(k, ok);
+                ++k;
+                x = 0;
+                if (!ok || u.b < 0) return;
             }
+            const int r = u.first + x++;
+            const int ts = p.by_subs.of(r);
+            t0 = ts * p.tpt;
+            h0 = (u.h * p.subs + r - ts * p.subs) * p.pf;
+            row0 = u.q0 + t0;
+#pragma unroll
+            for (int y = 0; y < kOwn; ++y) {
+                v[y] = INFINITY;
+                if (tok[y] < p.tpt && t0 + tok[y] < u.nq)
+                    v[y] = p.LSE[(static_cast<size_t>(row0) + tok[y]) * p.H + h0 + head[y]];
+            }
+        };
+        next();
+        while (ok && t0 >= 0) {
+            const int st = i % L::kQStages, buf = i % kBufs;
+            ok = wait(kBarQEmpty + st, ((i / L::kQStages) & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar(kBarQFull + st),
+                                      static_cast<uint32_t>(p.pf * p.tpt) * P::kRowBytes * P::kRegions);
+            __syncwarp();
+            if (lane < P::kRegions)
+                tma_load_3d(sQ(i) + lane * L::kQRegion, &tmQ, bar(kBarQFull + st), P::kCols * lane, h0, row0);
+            __syncwarp();
+            ++i;
+            float w[kOwn];
+#pragma unroll
+            for (int y = 0; y < kOwn; ++y) w[y] = v[y];
+            next();
+            if (!ok) break;
+            ok = wait(kBarSEmpty + buf, (((i - 1) / kBufs) & 1) ^ 1);
+            if (!ok) break;
+            // row c: token c / pf, head c mod pf; tokens that saw nothing get +infinity, which
+            // makes every weight 0
+#pragma unroll
+            for (int y = 0; y < kOwn; ++y)
+                if (lane + 32 * y < R)
+                    lse_ring[buf * R + lane + 32 * y] = w[y] == -INFINITY ? INFINITY : w[y] * 1.4426950408889634f;
+            mbar_arrive(bar(kBarLFull + buf));
         }
         if (lane == 0) {
             if (!ok) record_timeout(p, abort_flag, kRoleTma, -2);
@@ -467,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
             const int start = u.n == 1 ? 0 : half, step = u.n == 1 ? 1 : 2;
             for (int x = start; ok && x < u.n; x += step) {
-                const int at = i + x, buf = at % kBufs, t0 = (u.first + x) / p.subs * p.tpt;
+                const int at = i + x, buf = at % kBufs, t0 = p.by_subs.of(u.first + x) * p.tpt;
                 ok = wait(kBarLFull + buf, (at / kBufs) & 1);
                 if (ok) ok = wait(kBarSFull + buf, (at / kBufs) & 1);
                 if (!ok) break;
@@ -496,8 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < kCols; ++c)
                             if (h + c < c_lo || h + c >= c_hi) y[c] = -INFINITY;
                     }
+                    // of 32 exponentials kByHand are computed by multiply-adds, beside the others
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) y[c] = ex2_approx(y[c]);
+                    for (int c = 0; c < kCols; c += 2) {
+                        if (R >= 64 && c % 32 < kByHand) {
+                            exp2_pair(y[c], y[c + 1]);
+                        } else {
+                            y[c] = ex2_approx(y[c]);
+                            y[c + 1] = ex2_approx(y[c + 1]);
+                        }
+                    }
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
                         fadd2(a0, a1, y[c], y[c + 1]);
