@@ -12,6 +12,7 @@
 
 namespace {
 constexpr int kMaxDevices = 64;
+constexpr int kMostShared = 227 * 1024;
 std::once_flag g_once[kMaxDevices];
 cudaError_t g_opted[kMaxDevices];
 }  // namespace
@@ -66,7 +67,7 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
         if (x.n > 0 && !fa_host::on_device(x.p, dev)) return FA_ERR_INVALID_ARG;
     using namespace fa::evict;
     std::call_once(g_once[dev], [dev] {
-        g_opted[dev] = cudaFuncSetAttribute(fa_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
+        g_opted[dev] = cudaFuncSetAttribute(fa_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     });
     if (g_opted[dev] != cudaSuccess) return FA_ERR_CUDA;
     fa_host::take_fault_position();  // nothing here waits: an armed test hook is spent
@@ -84,7 +85,6 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
     p.seq_out = seqlens_out;
     p.H_kv = static_cast<int>(cache->H_kv);
     p.d = static_cast<int>(cache->d);
-    p.slots = kBufBytes / (4 * p.d) < kThreads ? kBufBytes / (4 * p.d) : kThreads;
     p.max_pages = static_cast<int>(max_pages);
     while ((int64_t{1} << p.page_log2) < cache->page_size) ++p.page_log2;
     p.num_pages = static_cast<int>(cache->num_pages);
@@ -93,12 +93,21 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
     p.budget = static_cast<int>(budget < most ? budget : most);
     p.first = static_cast<int>(first < most ? first : most);
     p.recent = static_cast<int>(recent < most ? recent : most);
-    // CTAs per sequence and head: what the SMs hold at once (one CTA each), while a round of theirs
-    // is not longer than the cache
-    int ctas = 1;
+    // CTAs per sequence and head: one for every 128 bytes of a row (a key and its value), twice as many
+    // where that leaves SMs without one; but at least 16 KB to move for each.
+    const int row_bytes = p.d * 4;
     const int64_t units = B * cache->H_kv;
-    while (ctas < kMaxCluster && units * ctas * 2 <= di.sm_count && static_cast<int64_t>(ctas) * p.slots < max_keys)
-        ctas *= 2;
+    int ctas = row_bytes / 128 < kMaxCluster ? row_bytes / 128 : kMaxCluster;
+    if (units * ctas < di.sm_count && ctas * 2 <= kMaxCluster) ctas *= 2;
+    while (ctas > 1 && static_cast<int64_t>(p.budget) * row_bytes < ctas * 16384) ctas /= 2;
+    const int columns = row_bytes / ctas;
+    while ((16 << p.piece_log2) < columns) ++p.piece_log2;
+    // shared memory: two CTAs to an SM; all of it where there are no two
+    const int shared = units * ctas <= di.sm_count ? kMostShared : kMostShared / 2 / 1024 * 1024;
+    const int room = (shared - kSharedBytes) / 128 * 128;
+    const int rows = room / (kDepth * columns + kLists * 20);
+    p.rows = rows < kThreads ? rows : kThreads;
+    p.keys = room / 4;
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -108,7 +117,7 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(units * ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSharedBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(shared);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 2;

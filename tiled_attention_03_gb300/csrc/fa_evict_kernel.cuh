@@ -3,21 +3,22 @@
 // those between the ones of the largest weight) move together, in their order, to the front of the
 // sequence's pages, with their values and weights.
 //
-// A cluster of 1 .. 8 CTAs takes a sequence and head. It first selects: weights as ordered 32-bit
-// numbers, histograms of 8 bits at a time summed over the cluster through distributed
-// shared memory, from the top digit down until the kept ones are exactly told apart; where equal
-// weights remain, 8 bits of the index at a time, lowest first. What is kept is then a
-// comparison with two numbers, which every thread can make for its own slot.
+// A cluster of 1 .. 8 CTAs takes a sequence and head. It first selects, each CTA on its part of the
+// slots: weights as ordered 32-bit numbers, histograms of 8 bits at a time summed over the
+// cluster through distributed shared memory, from the top digit down until the kept ones are
+// exactly told apart; where equal weights remain, 8 bits of the index at a time, lowest first. What
+// is kept is then a comparison with two numbers; one bit per slot of it goes to every CTA.
 //
-// Then it moves, in place. Slot j's row goes to a slot <= j, so rounds of consecutive slots are
-// taken in order, and a row may be written once the round it was read in, and so all before, has
-// been read by the whole cluster: one cluster barrier per round, which also carries the CTAs' counts.
-// The next round's rows are loaded (asynchronous copies to shared memory) before the
-// barrier: they lie behind everything that this round writes.
+// Then it moves, in place, each CTA its own columns of all rows (of 64 or 128 bytes where rows are
+// that wide), so that none waits for another. Row r of what is kept comes from a slot >= r: rounds of
+// consecutive rows are taken in order, and a round is written once it, and so all before, has
+// been read. The next rounds' rows are on their way meanwhile (asynchronous copies to shared memory):
+// they lie behind everything that this round writes. One block barrier a round orders all of that. (With
+// whole rows per CTA and slots shared among the cluster a round was small and took a cluster barrier
+// and 1.5 to 2 us: 16 sequences of 5000 to 20000 keys cut to 8192 took 295 us; rounds of
+// consecutive slots instead of rows, fewer bytes in flight where few are kept, 174.)
 //
-// Bound by memory: rows are read and written once, weights read once. Weights and page numbers
-// stay in shared memory as far as they fit, so that nothing but the rows is waited for between
-// rounds, and rounds are as large as what is left allows.
+// Bound by memory: rows and weights are read and written once.
 #pragma once
 
 #include <cstdint>
@@ -32,9 +33,10 @@ namespace evict {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBufBytes = 64 * 1024;  // rows of a round (two rounds are in flight)
-constexpr int kKept = 16384;          // weights of this CTA that stay in shared memory
-constexpr int kPages = 2048;          // page numbers that do
+constexpr int kDepth = 3;             // rounds of rows in shared memory
+constexpr int kPages = 2048;          // page numbers that stay there
+constexpr int kWords = 2048;          // 32 slots each: a window of slots whose bits are known
+constexpr int kWindow = kWords * 32;
 
 struct Params {
     uint16_t *k, *v;
@@ -42,24 +44,28 @@ struct Params {
     long long page_stride, token_stride, head_stride;
     const int *seq_k, *table;
     int *seq_out;
-    int H_kv, d, slots;  // slots: of a CTA in a round
+    int H_kv, d;
+    int rows;        // of a round (at most kThreads)
+    int piece_log2;  // 16-byte pieces of a CTA's columns: 2^piece_log2
+    int keys;        // weights of a CTA that stay in shared memory (a multiple of 4)
     int max_pages, page_log2, num_pages, max_keys;
     int budget, first, recent;
 };
 
 struct Shared {
-    float w_all[kKept];
-    int pages[kPages];
     unsigned hist[2][256];          // of this CTA, read by the cluster
     unsigned part[kWarps / 4][256];
-    int counts[2][kMaxCluster];     // kept rows of each CTA in a round, written by each
+    int pages[kPages];
+    unsigned bits[kWords];          // of the window: 1 = kept (written by the cluster)
+    int before[kWords + 1];         // kept slots of the window before each word
     int warp_sum[kWarps];
     int found[3];                   // digit, still to take, its count
-    long long src[2][kThreads];     // kept rows of a round: first element, -1: not in the cache
-    long long dst[kThreads];
-    float w[2][kThreads];
 };
-constexpr int kSharedBytes = (static_cast<int>(sizeof(Shared)) + 127) / 128 * 128 + 2 * kBufBytes;
+constexpr int kSharedBytes = (static_cast<int>(sizeof(Shared)) + 127) / 128 * 128;
+// behind it: the weights' ordered forms, and later, in their place, the rows of kDepth rounds and
+// their lists (one more: it is made while the round before is still read): a kept row's first elements
+// before and after, -1 where its page is not in the cache, and its weight
+constexpr int kLists = kDepth + 1;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -95,10 +101,11 @@ __device__ __forceinline__ uint32_t ordered(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) fa_evict_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
-    uint8_t *const bufs = smem_raw + kSharedBytes - 2 * kBufBytes;
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(smem_raw + kSharedBytes);
+    const uint32_t bufs = smem_u32(smem_raw) + kSharedBytes;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_size());
     const int unit = blockIdx.x / ctas, b = unit / p.H_kv, h = unit - b * p.H_kv;
@@ -108,7 +115,6 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
     if (h == 0 && rank == 0 && tid == 0) p.seq_out[b] = min(n, p.budget);
     if (n <= p.budget) return;
 
-    const int S = p.slots, round = S * ctas, rounds = (n + round - 1) / round;
     const int *table = p.table + static_cast<size_t>(b) * p.max_pages;
     const int page_mask = (1 << p.page_log2) - 1;
     // page of slot j, or -1 when its number lies outside the cache
@@ -125,30 +131,31 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
         const int page = page_of(j);
         return page < 0 ? 0.f : p.weights[weight_at(page, j)];
     };
-    // this CTA's x-th slot
-    auto slot = [&](int x) { return x / S * round + rank * S + x % S; };
-    const int own = rounds * S;
+    // this CTA's part of the slots, from `begin` on: whole words of bits
+    const int part_slots = ((n + ctas - 1) / ctas + 31) & ~31, begin = rank * part_slots;
+    const int own = max(0, min(part_slots, n - begin));
 
     // ---- select `want` of the slots between the first and the recent ones
     const int mid0 = p.first, mid1 = n - p.recent;
     int want = p.budget - p.first - p.recent;
     uint32_t T = 0xffffffffu;  // kept: above T, or equal and at J or before
     int J = -1;
-    // weights of this CTA's slots, several loads of a thread at a time
+    // ordered weights of this CTA's slots between (0, which no weight gives: not between), several
+    // loads of a thread at a time
     constexpr int kBatch = 8;
-    for (int x0 = 0; x0 < own && x0 < kKept; x0 += kBatch * kThreads) {
-        float w[kBatch];
+    const int cached = min((own + 3) & ~3, p.keys);
+    auto key_of = [&](int j) { return j >= mid0 && j < mid1 ? ordered(weight_of(j)) : 0u; };
+    for (int x0 = 0; x0 < cached; x0 += kBatch * kThreads) {
+        uint32_t m[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int x = x0 + i * kThreads + tid, j = slot(x);
-            w[i] = x < own && x < kKept && j < n ? weight_of(j) : 0.f;
+            const int x = x0 + i * kThreads + tid;
+            m[i] = x < min(own, cached) ? key_of(begin + x) : 0u;
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            if (x0 + i * kThreads + tid < kKept) sh.w_all[x0 + i * kThreads + tid] = w[i];
+            if (x0 + i * kThreads + tid < cached) keys[x0 + i * kThreads + tid] = m[i];
     }
-    __syncthreads();
-    auto own_weight = [&](int x, int j) { return x < kKept ? sh.w_all[x] : weight_of(j); };
     if (want > 0) {
         T = 0;
         J = 0x7fffffff;
@@ -161,14 +168,26 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
             if (pass == 4) shift = top;
             for (int i = tid; i < kWarps / 4 * 256; i += kThreads) (&sh.part[0][0])[i] = 0;
             __syncthreads();
-            for (int x = tid; x < own; x += kThreads) {
-                const int j = slot(x);
-                if (j < mid0 || j >= mid1) continue;
-                const uint32_t m = ordered(own_weight(x, j));
-                const uint32_t v = by_index ? static_cast<uint32_t>(j) : m;
-                const uint32_t known = by_index ? static_cast<uint32_t>(J0) : T;
-                if ((by_index && m != T) || (shift < 24 && v >> (shift + 8) != known >> (shift + 8))) continue;
-                atomicAdd(&sh.part[warp / 4][(v >> shift) & 255u], 1u);
+            unsigned *const part = sh.part[warp / 4];
+            if (by_index) {
+                auto count = [&](uint32_t m, int j) {
+                    if (m == T && (shift == 24 || j >> (shift + 8) == J0 >> (shift + 8))) atomicAdd(&part[(j >> shift) & 255], 1u);
+                };
+                for (int x = tid; x < cached; x += kThreads)
+                    if (keys[x] == T) count(T, begin + x);
+                for (int x = cached + tid; x < own; x += kThreads) count(key_of(begin + x), begin + x);
+            } else {
+                const int known = shift < 24 ? shift + 8 : 31;  // (nothing is known before the first digit)
+                const uint32_t prefix = shift < 24 ? T >> known : 0u;
+                auto count = [&](uint32_t m) {
+                    if (m != 0 && (shift == 24 || m >> known == prefix)) atomicAdd(&part[(m >> shift) & 255u], 1u);
+                };
+#pragma unroll 2
+                for (int x = tid * 4; x < cached; x += 4 * kThreads) {
+                    const uint4 m = *reinterpret_cast<const uint4 *>(keys + x);
+                    count(m.x), count(m.y), count(m.z), count(m.w);
+                }
+                for (int x = cached + tid; x < own; x += kThreads) count(key_of(begin + x));
             }
             __syncthreads();
             if (tid < 256) {
@@ -216,85 +235,140 @@ __global__ void __launch_bounds__(kThreads, 1) fa_evict_kernel(const Params p) {
         }
     }
 
-    // ---- move
-    const int row_bytes = p.d * 2, pieces = row_bytes / 16;  // of a key, and of a value
-    // Finds the kept ones of round t's slots and starts their copies. Returns their number.
-    auto load = [&](int t) -> int {
-        const int x = t * S + tid, j = t * round + rank * S + tid, buf = t & 1;
-        bool kept = false;
-        float w = 0.f;
-        int page = -1;
-        if (tid < S && j < n) {
-            page = page_of(j);
-            w = own_weight(x, j);
-            kept = j < mid0 || j >= mid1;
-            if (!kept) {
-                const uint32_t m = ordered(w);
-                kept = m > T || (m == T && j <= J);
+    // ---- move. A thread copies the same 16-byte piece of every kThreads / 2^piece_log2-th row.
+    const int log2 = p.piece_log2, S = p.rows;
+    const int piece = (rank << log2) + (tid & ((1 << log2) - 1)), per_row = p.d / 8;  // of a key
+    uint16_t *const mine = (piece < per_row ? p.k + piece * 8 : p.v + (piece - per_row) * 8) + h * p.head_stride;
+    const int row0 = tid >> log2, row_step = kThreads >> log2;
+    const uint32_t buf_bytes = static_cast<uint32_t>(S) << (log2 + 4);
+    longlong2 *const list_at = reinterpret_cast<longlong2 *>(smem_raw + kSharedBytes + kDepth * buf_bytes);
+    float *const list_w = reinterpret_cast<float *>(list_at + kLists * S);
+    auto element = [&](int page, int j) { return page * p.page_stride + (j & page_mask) * p.token_stride; };
+    int done = 0;  // kept rows of earlier windows
+    for (int window = 0; window < n; window += kWindow) {
+        const int end = min(n, window + kWindow), words = (end - window + 31) / 32;
+        // ---- its bits: of the first window each CTA's part, whose weights may be in shared memory;
+        // of others (whose weights nothing has been written over) a warp's words in turn
+        const int w_first = window == 0 ? begin / 32 + warp : rank * kWarps + warp;
+        const int w_end = window == 0 ? min((begin + own + 31) / 32, words) : words;
+        const int w_step = window == 0 ? kWarps : kWarps * ctas;
+        for (int i = w_first; i < w_end; i += w_step) {
+            const int j = window + i * 32 + lane;
+            bool kept = false;
+            if (j < end) {
+                kept = j < mid0 || j >= mid1;
+                if (!kept) {
+                    const uint32_t m = window == 0 && j - begin < cached ? keys[j - begin] : ordered(weight_of(j));
+                    kept = m > T || (m == T && j <= J);
+                }
             }
+            const unsigned word = __ballot_sync(0xffffffffu, kept);
+            if (lane < ctas) st_cluster(at_rank(smem_u32(&sh.bits[i]), lane), static_cast<int>(word));
         }
-        const unsigned mask = __ballot_sync(0xffffffffu, kept);
-        if (lane == 0) sh.warp_sum[warp] = __popc(mask);
-        __syncthreads();
-        int at = __popc(mask & ((1u << lane) - 1)), count = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) at += sh.warp_sum[i];
-            count += sh.warp_sum[i];
-        }
-        if (kept) {
-            sh.src[buf][at] = page < 0 ? -1 : page * p.page_stride + (j & page_mask) * p.token_stride + h * p.head_stride;
-            sh.w[buf][at] = w;
-        }
-        if (tid < ctas) st_cluster(at_rank(smem_u32(&sh.counts[buf][rank]), tid), count);
-        __syncthreads();
-        const uint32_t base = smem_u32(bufs) + buf * kBufBytes;
-        for (int c = tid; c < count * pieces * 2; c += kThreads) {
-            const int row = c / (2 * pieces), y = c - row * 2 * pieces;
-            const long long src = sh.src[buf][row];
-            const uint16_t *from = (y < pieces ? p.k : p.v) + (src < 0 ? 0 : src) + (y < pieces ? y : y - pieces) * 8;
-            copy16_or_zero(base + c * 16, from, src >= 0);
-        }
-        copies_commit();
-        return count;
-    };
-    int before = 0;  // kept rows of earlier rounds
-    int count = load(0);
-    for (int t = 0; t < rounds; ++t) {
-        int next = 0;
-        if (t + 1 < rounds) {
-            next = load(t + 1);
-            copies_wait<1>();
-        } else {
-            copies_wait<0>();
-        }
-        // this round has been read by all
         if (ctas > 1)
             cluster_sync();
         else
             __syncthreads();
-        int dest = before;
-        for (int r = 0; r < ctas; ++r) {
-            const int c = sh.counts[t & 1][r];
-            if (r < rank) dest += c;
-            before += c;
+        // ---- kept slots before each word
+        constexpr int kOwn = kWords / kThreads;
+        int c[kOwn], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            c[i] = sum;
+            sum += tid * kOwn + i < words ? __popc(sh.bits[tid * kOwn + i]) : 0;
         }
-        if (tid < count) {
-            const int j = dest + tid, page = page_of(j);
-            sh.dst[tid] = page < 0 ? -1 : page * p.page_stride + (j & page_mask) * p.token_stride + h * p.head_stride;
-            if (page >= 0) p.weights[weight_at(page, j)] = sh.w[t & 1][tid];
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
         }
+        if (lane == 31) sh.warp_sum[warp] = incl;
         __syncthreads();
-        const uint4 *rows = reinterpret_cast<const uint4 *>(bufs + (t & 1) * kBufBytes);
-        for (int c = tid; c < count * pieces * 2; c += kThreads) {
-            const int row = c / (2 * pieces), y = c - row * 2 * pieces;
-            const long long dst = sh.dst[row];
-            if (dst >= 0)
-                *reinterpret_cast<uint4 *>((y < pieces ? p.k : p.v) + dst + (y < pieces ? y : y - pieces) * 8) = rows[c];
-        }
+        for (int i = 0; i < warp; ++i) incl += sh.warp_sum[i];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) sh.before[tid * kOwn + i] = incl - sum + c[i];
+        if (tid == kThreads - 1) sh.before[kWords] = incl;
         __syncthreads();
-        count = next;
+
+        const int rows = sh.before[kWords], rounds = (rows + S - 1) / S;
+        float w_next = 0.f;  // the weight of this thread's row of the round listed last
+        int w_at = -1;
+        // the places of round t's rows before and after
+        auto list = [&](int t) {
+            if (w_at >= 0) list_w[w_at] = w_next;
+            w_at = -1;
+            const int row = t * S + tid;
+            if (tid >= S || row >= rows) return;
+            // the last word with no more than `row` kept slots before it, and its bit of that rank
+            int word = 0;
+#pragma unroll
+            for (int step = kWords / 2; step > 0; step >>= 1)
+                if (sh.before[word + step] <= row) word += step;
+            int rank_in = row - sh.before[word], bit = 0;
+            const unsigned bits = sh.bits[word];
+#pragma unroll
+            for (int step = 16; step > 0; step >>= 1) {
+                const int below = __popc((bits >> bit) & ((1u << step) - 1));
+                if (rank_in >= below) bit += step, rank_in -= below;
+            }
+            const int at = t % kLists * S + tid, from = window + word * 32 + bit, to = done + row;
+            const int page = page_of(from), page_to = page_of(to);
+            list_at[at] = make_longlong2(page < 0 ? -1 : element(page, from), page_to < 0 ? -1 : element(page_to, to));
+            if (rank == 0) {
+                w_at = at;
+                w_next = page < 0 ? 0.f : p.weights[weight_at(page, from)];
+            }
+        };
+        auto load = [&](int t) {
+            const int count = min(S, rows - t * S);
+            const longlong2 *list = list_at + t % kLists * S;
+            uint32_t to = bufs + t % kDepth * buf_bytes + tid * 16;
+#pragma unroll 4
+            for (int row = row0; row < count; row += row_step, to += kThreads * 16) {
+                const long long from = list[row].x;
+                copy16_or_zero(to, mine + max(from, 0ll), from >= 0);
+            }
+            copies_commit();
+        };
+#pragma unroll
+        for (int t = 0; t + 1 < kDepth; ++t) {
+            list(t);
+            __syncthreads();
+            if (t < rounds)
+                load(t);
+            else
+                copies_commit();
+        }
+        for (int t = 0; t < rounds; ++t) {
+            const int ahead = t + kDepth - 1;
+            copies_wait<kDepth - 2>();  // round t is there
+            list(ahead);
+            __syncthreads();  // for all threads; and the round before has left its buffer
+            if (ahead < rounds)
+                load(ahead);
+            else
+                copies_commit();
+            const int dest = t * S, count = min(S, rows - dest);
+            const longlong2 *at = list_at + t % kLists * S;
+            const uint8_t *staged = smem_raw + kSharedBytes + t % kDepth * buf_bytes + tid * 16;
+#pragma unroll 4
+            for (int row = row0; row < count; row += row_step, staged += kThreads * 16) {
+                const long long to = at[row].y;
+                if (to >= 0) *reinterpret_cast<uint4 *>(mine + to) = *reinterpret_cast<const uint4 *>(staged);
+            }
+            if (rank == 0 && tid < count) {
+                const int j = done + dest + tid, page = page_of(j);
+                if (page >= 0) p.weights[weight_at(page, j)] = list_w[t % kLists * S + tid];
+            }
+        }
+        done += rows;
+        // the bits are read no more (nor does anybody leave while they may be written)
+        if (ctas > 1 && end < n)
+            cluster_sync();
+        else
+            __syncthreads();
     }
-    if (ctas > 1) cluster_sync();  // nobody leaves while its shared memory may be read or written
 }
 
 }  // namespace evict
