@@ -12,18 +12,21 @@
 // tensor memory, so that the sum over rows is a sum over one thread's registers, and a tile of
 // keys, the M operand, is read once for all rows of its sequence and K/V head. A unit is one tile
 // of 128 keys of one K/V head with all tiles of R rows that see it; CTA c takes every gridDim-th
-// unit from c on. That shares them evenly (units of one sequence grow lighter along the keys under
-// a causal mask, and neighbours go to different CTAs), needs no counters, and gives every
+// unit from c on (every other time from the end of the run: units of one sequence grow lighter along
+// the keys under a causal mask). That shares them evenly, needs no counters, and gives every
 // key to one thread: one addition per key and call, so the result is the same every time (keys
 // of pages that several sequences share get one addition each, in any order).
 //
-// What bounds it: single steps read K once, by HBM. Chunks take one exponential per key and
-// row: 128 x 128 of them occupy the SM's exponential unit for 1,024 cycles, where the
-// products (d = 128) take 512.
+// What bounds it: single steps read K once, by HBM (8 sequences of 32768 keys of 8 heads of 128: 89
+// us, 6.2 TB/s). Chunks: a tile of 128 x 128 scores takes about 1,150 cycles, of which the products
+// take 528 and the exponentials as long; computing some of those by multiply-adds made it slower
+// (10 of 32: 115 -> 130 us), as the sums wait for tensor memory and for each other more than for a pipe.
 //
-// Warps (384 threads): 0-3 and 4-7 sum alternate tiles of rows (of units with one: alternate
-// units), 8 finds units, 9 issues the products, 10 loads queries and their LSE, 11 loads keys;
-// the loaders ask for the next page numbers and LSEs before they wait for the present ones.
+// Warps (640 threads): 0-15 are four teams of four that sum every fourth tile of rows (of units with
+// one: every fourth unit), as one team's loads from tensor memory and exponentials wait for each
+// other; 16 finds units, 32 at a time, 17 issues the products, 18 loads queries and their LSE, 19 loads
+// keys; the loaders ask for page numbers one tile ahead, and for LSEs one or, where units have many tiles,
+// three (2048 tokens on 6000 keys: 128 us with one, 116 with three).
 // Every wait is bounded; on expiry the CTA records the failure, drains its copies and
 // products, frees its tensor memory and returns.
 #pragma once
@@ -40,13 +43,14 @@ namespace fa {
 namespace weights {
 
 constexpr int kBK = 128;  // keys per tile
-constexpr int kThreads = 384;
-constexpr int kPlanWarp = 8, kIssueWarp = 9, kQWarp = 10, kKWarp = 11;
-constexpr int kUnitSlots = 8;
-constexpr int kUnitConsumers = 11;  // warps that take the units: all but the one that finds them
+constexpr int kTeams = 4;
+constexpr int kThreads = (4 * kTeams + 4) * 32;
+constexpr int kPlanWarp = 4 * kTeams, kIssueWarp = kPlanWarp + 1, kQWarp = kPlanWarp + 2, kKWarp = kPlanWarp + 3;
+constexpr int kUnitSlots = 16;  // more than a loader's look-ups and tiles together
+constexpr int kUnitConsumers = 4 * kTeams + 3;  // warps that take the units: all but the one that finds them
 constexpr int kMaxStages = 8;
-constexpr int kBufs = 4;  // of scores and of their rows' LSE
-constexpr int kByHand = 12;
+constexpr int kBufs = 4;  // of scores
+constexpr int kLses = 8;  // of their rows' LSE: more, as queries are loaded after the LSE before them
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmem = 0;  // all columns are allocated: they start at 0
 constexpr unsigned kStatusTimeout = 4;
@@ -75,10 +79,11 @@ struct Smem {
     static constexpr int kTile = kBK / 8 * P::kGroup;
     static constexpr int kQRegion = R * P::kRowBytes;
     static constexpr int kQBytes = P::kRegions * kQRegion;
-    static constexpr int kSmall = 4608;
+    static constexpr int kSmall = 9728;
     static constexpr int kMost = 227 * 1024 - kSmall;
-    // as many tiles of queries as leave four of keys (two where a tile of keys is 64 KB)
-    static constexpr int kQFit = (kMost - (D == 256 ? 2 : 4) * kTile) / kQBytes;
+    // up to four tiles of queries that leave four of keys; two of keys where one is 64 KB, or where
+    // units have many tiles of rows, which then come faster than keys
+    static constexpr int kQFit = (kMost - (D == 256 || R == 128 ? 2 : 4) * kTile) / kQBytes;
     static constexpr int kQStages = kQFit < 4 ? kQFit : 4;
     static constexpr int kKFit = (kMost - kQStages * kQBytes) / kTile;
     static constexpr int kKStages = kKFit < kMaxStages ? kKFit : kMaxStages;
@@ -86,11 +91,11 @@ struct Smem {
     static constexpr int kK = 0;
     static constexpr int kQ = kK + kKStages * kTile;
     static constexpr int kBar = kQ + kQStages * kQBytes;
-    static constexpr int kMisc = kBar + 72 * 8;              // TMEM address, abort flag
+    static constexpr int kMisc = kBar + 96 * 8;              // TMEM address, abort flag
     static constexpr int kRing = kMisc + 16;                 // kUnitSlots units
-    static constexpr int kLse = kRing + kUnitSlots * 64;     // kBufs x R, times log2 e
-    static constexpr int kSums = kLse + kBufs * R * 4;       // two units' sums of the second four warps
-    static constexpr int kBytes = kSums + 2 * kBK * 4;
+    static constexpr int kLse = kRing + kUnitSlots * 64;     // kLses x R, times -log2 e
+    static constexpr int kSums = kLse + kLses * R * 4;       // two units' sums of three teams
+    static constexpr int kBytes = kSums + 2 * (kTeams - 1) * kBK * 4;
     static_assert(kLse % 16 == 0 && kBytes - kBar <= kSmall, "layout");
     static constexpr int kAlloc = kBytes > 120 * 1024 ? kBytes : 120 * 1024;  // one CTA per SM
 };
@@ -101,16 +106,17 @@ enum : int {
     kBarQFull = kBarKEmpty + kMaxStages,   // + stage (4)
     kBarQEmpty = kBarQFull + 4,            // + stage (4)
     kBarSFull = kBarQEmpty + 4,            // + buffer
-    kBarSEmpty = kBarSFull + kBufs,        // + buffer: scores and LSE read
-    kBarLFull = kBarSEmpty + kBufs,        // + buffer
-    kBarSumFull = kBarLFull + kBufs,       // + slot (2)
+    kBarSEmpty = kBarSFull + kBufs,        // + buffer
+    kBarLFull = kBarSEmpty + kBufs,        // + LSE slot
+    kBarLEmpty = kBarLFull + kLses,        // + LSE slot
+    kBarSumFull = kBarLEmpty + kLses,      // + slot (2)
     kBarSumEmpty = kBarSumFull + 2,        // + slot (2)
     kBarUnitFull = kBarSumEmpty + 2,            // + slot
     kBarUnitEmpty = kBarUnitFull + kUnitSlots,  // + slot
     kBarDrain = kBarUnitEmpty + kUnitSlots,
     kNumBars = kBarDrain + 1,
 };
-static_assert(kNumBars <= 72, "barrier slots");
+static_assert(kNumBars <= 96, "barrier slots");
 
 // A tile of keys of K/V head h of sequence b, and its n tiles of rows from the first-th on
 // (tile r: tokens from r / subs * tpt on, heads from r mod subs * pf on).
@@ -155,49 +161,24 @@ __device__ __forceinline__ void record_timeout(const Params &p, volatile int *ab
     }
 }
 
-// (a, b) <- (2^a, 2^b) by multiply-adds: 2^x = 2^i 2^f with i the nearest integer and 2^f on
-// [-1/2, 1/2] by the polynomial of degree 5 of least relative error (7.5e-8, found by exchange). x
-// is cut to [-126, 128]: below, 2^-126 adds nothing to a sum that is not as small; above, the
-// result is infinite as it should be. NaN stays NaN.
-__device__ __forceinline__ void exp2_pair(float &a, float &b) {
-    constexpr float kShift = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-126.f));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-126.f));
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(128.f));
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(128.f));
-    float ta = a, tb = b;
-    fadd2(ta, tb, kShift, kShift);
-    float fa = ta, fb = tb;
-    fadd2(fa, fb, -kShift, -kShift);
-    ffma2(fa, fb, -1.f, -1.f, a, b);  // x - i
-    float ya = 0.00132764725f, yb = 0.00132764725f;
-    ffma2(ya, yb, fa, fb, 0.00967554096f, 0.00967554096f);
-    ffma2(ya, yb, fa, fb, 0.0555071309f, 0.0555071309f);
-    ffma2(ya, yb, fa, fb, 0.240221202f, 0.240221202f);
-    ffma2(ya, yb, fa, fb, 0.693146944f, 0.693146944f);
-    ffma2(ya, yb, fa, fb, 1.00000012f, 1.00000012f);
-    // the integer's low bits, as an exponent
-    const float sa = __int_as_float((__float_as_int(ta) << 23) + 0x3f800000);
-    const float sb = __int_as_float((__float_as_int(tb) << 23) + 0x3f800000);
-    fmul2(ya, yb, sa, sb);
-    a = ya;
-    b = yb;
-}
-
+// 16 or 32 columns of this warp's lanes; and the wait for them.
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+        : "r"(taddr));
 }
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
-    tmem_ld32(taddr, r);
-    tmem_ld_wait(r);
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void ld_cols_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
+__device__ __forceinline__ void ld_cols_wait(uint32_t (&r)[32]) { tmem_ld_wait(r); }
 
 template <int D, int R, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -241,10 +222,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kBufs; ++s) {
             mbar_init(bar(kBarSFull + s), 1);
             mbar_init(bar(kBarSEmpty + s), 128);
+        }
+        for (int s = 0; s < kLses; ++s) {
             mbar_init(bar(kBarLFull + s), 32);
+            mbar_init(bar(kBarLEmpty + s), 4);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(kBarSumFull + s), 128);
+            mbar_init(bar(kBarSumFull + s), 128 * (kTeams - 1));
             mbar_init(bar(kBarSumEmpty + s), 128);
         }
         for (int k = 0; k < kUnitSlots; ++k) {
@@ -291,63 +275,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================================================================ units
         // Units are numbered sequence by sequence, tile by tile, head by head (the heads of a tile lie
         // beside each other, and CTAs side by side read them at the same time). Each lane holds one
-        // sequence of the 32 from b0 on: its units, and those before them from `base` on.
-        long long base = 0, unit = blockIdx.x;
-        int b0 = 0;
-        Seq s = load_seq(lane, p);
-        int tiles = key_tiles(s, p);
-        long long incl = static_cast<long long>(tiles) * p.H_kv;
-        auto scan = [&] {
+        // sequence of the 32 from b0 on, with its units and those before it from `base` on, and
+        // looks up one of this CTA's next 32 units among them.
+        // The i-th is in the i-th run of gridDim units, from its front or, for odd i, from its end: where
+        // units grow lighter, who has a heavy one has a light one next.
+        auto unit_of = [&](long long i) {
+            return i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        };
+        long long base = 0, next = lane;
+        bool ok = true;
+        int k = 0;
+        for (int b0 = 0; ok && b0 < p.B; b0 += 32) {
+            const Seq s = load_seq(b0 + lane, p);
+            const int tiles = key_tiles(s, p);
+            long long incl = static_cast<long long>(tiles) * p.H_kv;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long x = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += x;
             }
-        };
-        scan();
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            Unit u{};
-            u.b = -1;
-            while (true) {
-                const unsigned hit = __ballot_sync(0xffffffffu, unit - base < incl);
-                if (hit != 0) {
-                    const int at = __ffs(hit) - 1;
-                    u.b = b0 + at;
-                    u.q0 = __shfl_sync(0xffffffffu, s.q0, at);
-                    u.nq = __shfl_sync(0xffffffffu, s.nq, at);
-                    u.nk = __shfl_sync(0xffffffffu, s.nk, at);
-                    const int n = __shfl_sync(0xffffffffu, tiles, at);
-                    const int x = static_cast<int>(unit - base - (__shfl_sync(0xffffffffu, incl, at) -
-                                                                  static_cast<long long>(n) * p.H_kv));
-                    const int y = p.by_heads.of(x);
-                    u.h = x - y * p.H_kv;
-                    u.q_off = u.nk - u.nq;
-                    u.j = y + first_tile(Seq{0, u.nq, u.nk}, p);
-                    int lo, hi;
-                    tokens_of(u, u.j * kBK, min(u.j * kBK + kBK, u.nk) - 1, p, lo, hi);
-                    u.first = p.by_tpt.of(lo) * p.subs;
-                    u.n = hi < lo ? 0 : (p.by_tpt.of(hi) + 1) * p.subs - u.first;
-                    break;
+            const long long before = incl - static_cast<long long>(tiles) * p.H_kv;
+            const long long all = __shfl_sync(0xffffffffu, incl, 31);
+            while (ok) {
+                const long long rel = unit_of(next) - base;
+                // the last sequence with no more than rel units before it
+                int at = 0;
+#pragma unroll
+                for (int step = 16; step > 0; step >>= 1)
+                    if (__shfl_sync(0xffffffffu, before, at + step) <= rel) at += step;
+                Unit u{};
+                u.b = b0 + at;
+                u.q0 = __shfl_sync(0xffffffffu, s.q0, at);
+                u.nq = __shfl_sync(0xffffffffu, s.nq, at);
+                u.nk = __shfl_sync(0xffffffffu, s.nk, at);
+                const int x = static_cast<int>(rel - __shfl_sync(0xffffffffu, before, at));
+                const int found = __popc(__ballot_sync(0xffffffffu, rel < all));  // of the 32 units
+                const int y = p.by_heads.of(max(x, 0));
+                u.h = x - y * p.H_kv;
+                u.q_off = u.nk - u.nq;
+                u.j = y + first_tile(Seq{0, u.nq, u.nk}, p);
+                int lo, hi;
+                tokens_of(u, u.j * kBK, min(u.j * kBK + kBK, u.nk) - 1, p, lo, hi);
+                u.first = p.by_tpt.of(lo) * p.subs;
+                u.n = hi < lo ? 0 : (p.by_tpt.of(hi) + 1) * p.subs - u.first;
+                for (int i = 0; ok && i < found; ++i, ++k) {
+                    const int slot = k % kUnitSlots;
+                    ok = wait(kBarUnitEmpty + slot, ((k / kUnitSlots) & 1) ^ 1);
+                    if (ok && lane == i) {
+                        *slot_of(k) = u;
+                        mbar_arrive(bar(kBarUnitFull + slot));
+                    }
+                    __syncwarp();
                 }
-                base += __shfl_sync(0xffffffffu, incl, 31);
-                b0 += 32;
-                if (b0 >= p.B) break;
-                s = load_seq(b0 + lane, p);
-                tiles = key_tiles(s, p);
-                incl = static_cast<long long>(tiles) * p.H_kv;
-                scan();
+                next += found;
+                if (found < 32) break;
             }
-            unit += gridDim.x;
+            base += all;
+        }
+        if (ok) {
             const int slot = k % kUnitSlots;
             ok = wait(kBarUnitEmpty + slot, ((k / kUnitSlots) & 1) ^ 1);
-            if (!ok) break;
-            if (lane == 0) {
+            if (ok && lane == 0) {
+                Unit u{};
+                u.b = -1;
                 *slot_of(k) = u;
                 mbar_arrive(bar(kBarUnitFull + slot));
             }
             __syncwarp();
-            if (u.b < 0) break;
         }
         if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleTma, -3);
     } else if (warp == kKWarp) {
@@ -419,55 +413,90 @@ __global__ void __launch_bounds__(kThreads, 1)
             head[y] = lane + 32 * y - tok[y] * p.pf;
         }
         Unit u{};
-        int x = 0, t0 = -1, h0 = 0, row0 = 0;  // the next tile of rows: t0 < 0: none
-        float v[kOwn];                         // its LSEs
-        auto next = [&] {
-            t0 = -1;
+        int x = 0;
+        bool end = false;
+        // A tile of rows: its first token of all (< 0: no more) and head, and its LSEs.
+        struct Tile {
+            int row0, h0;
+            float v[kOwn];
+        };
+        auto next = [&](Tile &n) {
+            n.row0 = -1;
+            if (end) return;
             while (x >= u.n) {
                 u = take(k, ok);
                 ++k;
                 x = 0;
-                if (!ok || u.b < 0) return;
+                if (!ok || u.b < 0) {
+                    end = true;
+                    return;
+                }
             }
             const int r = u.first + x++;
-            const int ts = p.by_subs.of(r);
-            t0 = ts * p.tpt;
-            h0 = (u.h * p.subs + r - ts * p.subs) * p.pf;
-            row0 = u.q0 + t0;
+            const int ts = p.by_subs.of(r), t0 = ts * p.tpt;
+            n.h0 = (u.h * p.subs + r - ts * p.subs) * p.pf;
+            n.row0 = u.q0 + t0;
 #pragma unroll
             for (int y = 0; y < kOwn; ++y) {
-                v[y] = INFINITY;
+                n.v[y] = -INFINITY;
                 if (tok[y] < p.tpt && t0 + tok[y] < u.nq)
-                    v[y] = p.LSE[(static_cast<size_t>(row0) + tok[y]) * p.H + h0 + head[y]];
+                    n.v[y] = p.LSE[(static_cast<size_t>(n.row0) + tok[y]) * p.H + n.h0 + head[y]];
             }
         };
-        next();
-        while (ok && t0 >= 0) {
-            const int st = i % L::kQStages, buf = i % kBufs;
-            ok = wait(kBarQEmpty + st, ((i / L::kQStages) & 1) ^ 1);
-            if (!ok) break;
+        auto load = [&](const Tile &n) {
+            const int st = i % L::kQStages;
+            ok = ok && wait(kBarQEmpty + st, ((i / L::kQStages) & 1) ^ 1);
+            if (!ok) return;
             if (lane == 0)
                 mbar_arrive_expect_tx(bar(kBarQFull + st),
                                       static_cast<uint32_t>(p.pf * p.tpt) * P::kRowBytes * P::kRegions);
             __syncwarp();
             if (lane < P::kRegions)
-                tma_load_3d(sQ(i) + lane * L::kQRegion, &tmQ, bar(kBarQFull + st), P::kCols * lane, h0, row0);
+                tma_load_3d(sQ(i) + lane * L::kQRegion, &tmQ, bar(kBarQFull + st), P::kCols * lane, n.h0, n.row0);
             __syncwarp();
             ++i;
-            float w[kOwn];
-#pragma unroll
-            for (int y = 0; y < kOwn; ++y) w[y] = v[y];
-            next();
-            if (!ok) break;
-            ok = wait(kBarSEmpty + buf, (((i - 1) / kBufs) & 1) ^ 1);
-            if (!ok) break;
-            // row c: token c / pf, head c mod pf; tokens that saw nothing get +infinity, which
-            // makes every weight 0
+        };
+        // row c: token c / pf, head c mod pf. Minus the LSE, so that tokens that saw nothing get
+        // -infinity, which makes every weight 0
+        auto store = [&](const Tile &n) {
+            const int slot = (i - 1) % kLses;
+            ok = ok && wait(kBarLEmpty + slot, (((i - 1) / kLses) & 1) ^ 1);
+            if (!ok) return;
 #pragma unroll
             for (int y = 0; y < kOwn; ++y)
                 if (lane + 32 * y < R)
-                    lse_ring[buf * R + lane + 32 * y] = w[y] == -INFINITY ? INFINITY : w[y] * 1.4426950408889634f;
-            mbar_arrive(bar(kBarLFull + buf));
+                    lse_ring[slot * R + lane + 32 * y] =
+                        n.v[y] == -INFINITY ? -INFINITY : n.v[y] * -1.4426950408889634f;
+            mbar_arrive(bar(kBarLFull + slot));
+        };
+        if constexpr (R >= 64) {
+            // LSEs three tiles ahead, in variables of their own, as a copy would wait for them
+            Tile n0, n1, n2;
+            next(n0);
+            next(n1);
+            next(n2);
+            bool more = true;
+            auto step = [&](Tile &n) {
+                more = more && ok && n.row0 >= 0;
+                if (!more) return;
+                load(n);
+                store(n);
+                if (ok) next(n);
+            };
+            while (more) {
+                step(n0);
+                step(n1);
+                step(n2);
+            }
+        } else {
+            Tile n;
+            next(n);
+            while (ok && n.row0 >= 0) {
+                load(n);
+                const Tile now = n;
+                next(n);
+                store(now);
+            }
         }
         if (lane == 0) {
             if (!ok) record_timeout(p, abort_flag, kRoleTma, -2);
@@ -519,25 +548,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ================================================================ sums over rows
-        const int half = warp >> 2;  // which four warps
+        const int team = warp >> 2;
         const int own = threadIdx.x & 127;
         const uint32_t tl = kTmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const float sl2 = p.scale_log2;
         float *const sums = reinterpret_cast<float *>(smem + L::kSums);
-        int i = 0, k = 0, joined = 0;  // tiles of rows; units; those that both halves shared
+        int i = 0, k = 0, joined = 0;  // tiles of rows; units; those that the teams share
         bool ok = true;
         for (; ok; ++k) {
             const Unit u = take(k, ok);
             if (!ok || u.b < 0) break;
             if (u.n == 0) continue;
-            if (u.n == 1 && (k & 1) != half) {  // the others' unit
+            const int me = (team + k) % kTeams;  // tiles me, me + kTeams, ... of the unit are this team's
+            if (u.n == 1 && me != 0) {
                 ++i;
                 continue;
             }
             const int key = u.j * kBK + own;
             const bool there = key < u.nk;
             int page = -1;
-            if (there && (u.n == 1 || half == 0))
+            if (there && me == 0)
                 page = p.table[static_cast<size_t>(u.b) * p.max_pages + (key >> p.page_log2)];
             // tokens that see this key, and those that see every key of the tile
             int lo, hi, all_lo, all_hi, x1, x2;
@@ -545,10 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tokens_of(u, u.j * kBK + kBK - 1, u.j * kBK + kBK - 1, p, all_lo, x1);
             tokens_of(u, u.j * kBK, u.j * kBK, p, x2, all_hi);
             float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-            const int start = u.n == 1 ? 0 : half, step = u.n == 1 ? 1 : 2;
-            for (int x = start; ok && x < u.n; x += step) {
+            for (int x = me; ok && x < u.n; x += kTeams) {
                 const int at = i + x, buf = at % kBufs, t0 = p.by_subs.of(u.first + x) * p.tpt;
-                ok = wait(kBarLFull + buf, (at / kBufs) & 1);
+                ok = wait(kBarLFull + at % kLses, (at / kLses) & 1);
                 if (ok) ok = wait(kBarSFull + buf, (at / kBufs) & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -556,63 +585,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // behind the sequence's last token may hold anything: they are not looked at)
                 const int c_lo = (lo - t0) * p.pf, c_hi = min(hi - t0 + 1, p.tpt) * p.pf;
                 const bool whole = t0 >= all_lo && t0 + p.tpt - 1 <= all_hi && p.tpt * p.pf == R;
-                const float *lse = lse_ring + buf * R;
+                const float *lse = lse_ring + at % kLses * R;
                 constexpr int kCols = R < 32 ? R : 32;
+                uint32_t r[2][kCols];  // the next columns come while these are summed
+                ld_cols(tl + buf * R, r[0]);
 #pragma unroll
                 for (int h = 0; h < R; h += kCols) {
-                    uint32_t r[kCols];
-                    ld_cols(tl + buf * R + h, r);
+                    uint32_t(&now)[kCols] = r[h / kCols & 1];
+                    ld_cols_wait(now);
+                    if (h + kCols < R) ld_cols(tl + buf * R + h + kCols, r[(h / kCols + 1) & 1]);
                     float y[kCols];
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
                         const float4 v = *reinterpret_cast<const float4 *>(lse + h + c);
-                        y[c] = __uint_as_float(r[c]), y[c + 1] = __uint_as_float(r[c + 1]);
-                        y[c + 2] = __uint_as_float(r[c + 2]), y[c + 3] = __uint_as_float(r[c + 3]);
-                        ffma2(y[c], y[c + 1], sl2, sl2, -v.x, -v.y);
-                        ffma2(y[c + 2], y[c + 3], sl2, sl2, -v.z, -v.w);
+                        y[c] = __uint_as_float(now[c]), y[c + 1] = __uint_as_float(now[c + 1]);
+                        y[c + 2] = __uint_as_float(now[c + 2]), y[c + 3] = __uint_as_float(now[c + 3]);
+                        ffma2(y[c], y[c + 1], sl2, sl2, v.x, v.y);
+                        ffma2(y[c + 2], y[c + 3], sl2, sl2, v.z, v.w);
+                    }
+                    if (h + kCols == R) {  // scores and LSE are read: the next ones may come
+                        tc_fence_before();
+                        mbar_arrive(bar(kBarSEmpty + buf));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kBarLEmpty + at % kLses));
                     }
                     if (!whole) {
 #pragma unroll
                         for (int c = 0; c < kCols; ++c)
                             if (h + c < c_lo || h + c >= c_hi) y[c] = -INFINITY;
                     }
-                    // of 32 exponentials kByHand are computed by multiply-adds, beside the others
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 2) {
-                        if (R >= 64 && c % 32 < kByHand) {
-                            exp2_pair(y[c], y[c + 1]);
-                        } else {
-                            y[c] = ex2_approx(y[c]);
-                            y[c + 1] = ex2_approx(y[c + 1]);
-                        }
-                    }
+                    for (int c = 0; c < kCols; ++c) y[c] = ex2_approx(y[c]);
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
                         fadd2(a0, a1, y[c], y[c + 1]);
                         fadd2(a2, a3, y[c + 2], y[c + 3]);
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(bar(kBarSEmpty + buf));
             }
             i += u.n;
             if (!ok) break;
             float sum = (a0 + a1) + (a2 + a3);
             if (u.n > 1) {
-                // the second four warps hand their sums to the first
+                // the other teams hand their sums to the first
                 const int slot = joined % 2;
-                if (half == 1) {
+                float *const sum_of = sums + slot * (kTeams - 1) * kBK + own;
+                if (me != 0) {
                     ok = wait(kBarSumEmpty + slot, ((joined / 2) & 1) ^ 1);
                     if (!ok) break;
-                    sums[slot * kBK + own] = sum;
+                    sum_of[(me - 1) * kBK] = sum;
                     mbar_arrive(bar(kBarSumFull + slot));
                 } else {
                     ok = wait(kBarSumFull + slot, (joined / 2) & 1);
                     if (!ok) break;
-                    sum += sums[slot * kBK + own];
+#pragma unroll
+                    for (int o = 0; o < kTeams - 1; ++o) sum += sum_of[o * kBK];
                     mbar_arrive(bar(kBarSumEmpty + slot));
                 }
                 ++joined;
+                if (me != 0) continue;
             }
             if (there && page >= 0 && page < p.num_pages) {
                 float *w = p.weights + ((static_cast<size_t>(page) * p.H_kv + u.h) << p.page_log2) +
