@@ -62,7 +62,7 @@ cudaError_t launch(const Plan &x, int dev, cudaStream_t st) {
                           : x.rows == 32 ? launch_rows<DL, 32, BF16>(x, dev, st)
                                          : launch_rows<DL, 64, BF16>(x, dev, st);
     if (e != cudaSuccess) return e;
-    return fa::launch_after(fa::latent::fa_latent_merge_kernel<DL, BF16>, dim3(2 * x.sms), fa::latent::kMergeThreads,
+    return fa::launch_after(fa::latent::fa_latent_merge_kernel<DL, BF16>, dim3(fa::latent::kMergeBlocks * x.sms), fa::latent::kMergeThreads,
                             0, st, x.merge);
 }
 

@@ -260,6 +260,21 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) 
         : "r"(taddr)
         : "memory");
 }
+// 32 lanes x 16 consecutive columns, at both of two places, and the wait for them.
+__device__ __forceinline__ void tmem_ld16_two(uint32_t ta, uint32_t tb, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(ta), "r"(tb)
+        : "memory");
+}
 // 32 lanes x 16 consecutive columns, and the wait for them.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -942,51 +957,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             // lanes 4 i .. 4 i + 3 trade four rows' columns, so that each has four columns of a row
             const size_t row0 = P.slot < 0 ? static_cast<size_t>(P.row0) : static_cast<size_t>(P.slot) * R;
             const size_t at0 = (row0 + (lane & 3)) * DL + warp * 32 + (lane & ~3);
+            const bool b0 = lane & 1, b1 = lane & 2;
+            constexpr int kParts = L::kParts;
+            // 16 rows of two slices of O^T at a time (of one where there is one)
+            constexpr int kAtOnce = kParts > 1 ? 2 : 1;
 #pragma unroll 1
-            for (int c = 0; c < DL / 128 * R; c += 16) {
-                const int r0 = c % R, col = c / R * 128;
-                if (r0 >= P.rows) continue;
-                uint32_t o[16];
-                float y[16];
-                tmem_ld16(tl + L::kTmemO + c, o);
+            for (int r0 = 0; r0 < P.rows; r0 += 16) {
+                float f[16];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(factor + r0 + e);
+                    f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+                }
+#pragma unroll 1
+                for (int part = 0; part < kParts; part += kAtOnce) {
+                    uint32_t o[16 * kAtOnce];
+                    const uint32_t from = tl + L::kTmemO + part * R + r0;
+                    if constexpr (kAtOnce == 2)
+                        tmem_ld16_two(from, from + R, o);
+                    else
+                        tmem_ld16(from, o);
+                    float y[16 * kAtOnce];
                     // a row without keys: 0, whatever its column holds
-                    const float4 f = *reinterpret_cast<const float4 *>(factor + r0 + e);
-                    y[e] = f.x == 0.f ? 0.f : __uint_as_float(o[e]) * f.x;
-                    y[e + 1] = f.y == 0.f ? 0.f : __uint_as_float(o[e + 1]) * f.y;
-                    y[e + 2] = f.z == 0.f ? 0.f : __uint_as_float(o[e + 2]) * f.z;
-                    y[e + 3] = f.w == 0.f ? 0.f : __uint_as_float(o[e + 3]) * f.w;
-                }
-                const bool b0 = lane & 1, b1 = lane & 2;
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float z = __shfl_xor_sync(0xffffffffu, b0 ? y[e] : y[e + 1], 1);
-                    y[e] = b0 ? z : y[e];
-                    y[e + 1] = b0 ? y[e + 1] : z;
-                }
+                    for (int e = 0; e < 16 * kAtOnce; ++e)
+                        y[e] = f[e % 16] == 0.f ? 0.f : __uint_as_float(o[e]) * f[e % 16];
 #pragma unroll
-                for (int e = 0; e < 16; e += 4)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float z = __shfl_xor_sync(0xffffffffu, b1 ? y[e + i] : y[e + i + 2], 2);
-                        y[e + i] = b1 ? z : y[e + i];
-                        y[e + i + 2] = b1 ? y[e + i + 2] : z;
+                    for (int e = 0; e < 16 * kAtOnce; e += 2) {
+                        const float z = __shfl_xor_sync(0xffffffffu, b0 ? y[e] : y[e + 1], 1);
+                        y[e] = b0 ? z : y[e];
+                        y[e + 1] = b0 ? y[e + 1] : z;
                     }
-                const size_t at = at0 + static_cast<size_t>(r0) * DL + col;
-                if (P.slot < 0) {
-                    uint16_t *out = static_cast<uint16_t *>(p.O) + at;
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        if (r0 + e + (lane & 3) < P.rows)
-                            *reinterpret_cast<uint2 *>(out + e * DL) =
-                                make_uint2(pack2<BF16>(y[e], y[e + 1]), pack2<BF16>(y[e + 2], y[e + 3]));
-                } else {
-                    float *out = p.part_O + at;
+                    for (int e = 0; e < 16 * kAtOnce; e += 4)
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        if (r0 + e + (lane & 3) < P.rows)
-                            *reinterpret_cast<float4 *>(out + e * DL) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        for (int i = 0; i < 2; ++i) {
+                            const float z = __shfl_xor_sync(0xffffffffu, b1 ? y[e + i] : y[e + i + 2], 2);
+                            y[e + i] = b1 ? z : y[e + i];
+                            y[e + i + 2] = b1 ? y[e + i + 2] : z;
+                        }
+                    const size_t at = at0 + static_cast<size_t>(r0) * DL + part * 128;
+#pragma unroll
+                    for (int e = 0; e < 16 * kAtOnce; e += 4) {
+                        const bool row_there = r0 + e % 16 + (lane & 3) < P.rows;
+                        const size_t to = at + e % 16 * DL + e / 16 * 128;
+                        if (P.slot < 0) {
+                            if (row_there)
+                                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.O) + to) =
+                                    make_uint2(pack2<BF16>(y[e], y[e + 1]), pack2<BF16>(y[e + 2], y[e + 3]));
+                        } else if (row_there) {
+                            *reinterpret_cast<float4 *>(p.part_O + to) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        }
+                    }
                 }
             }
             tc_fence_before();
@@ -1006,11 +1028,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the cut blocks. With O_s, LSE_s of piece s
 //     LSE = ln sum_s exp(LSE_s)          O = sum_s exp(LSE_s - LSE) O_s
-// around the largest LSE_s, in a fixed order. Every thread block finds the cut blocks' rows among
-// the CTAs' infos (in shared memory, with the rows before each) and takes every gridDim-th
-// batch of them: a block per row instead, most of which found nothing to do, took 14 us where
-// this takes 5. A thread holds four columns of a row; with fewer rows than there are places for
-// them, several groups of DL / 4 threads share a row's pieces and are summed at the end.
+// around the largest LSE_s, in a fixed order. Every thread block lists the cut blocks in shared memory,
+// with the rows before each, and takes every gridDim-th batch of the rows. A thread holds four
+// columns of a row; with fewer rows than there are places for them, several groups of DL / 4
+// threads share a row's pieces and are summed at the end. Bound by latency: statistics and the first
+// pieces are asked for together. (A block per row, most of which found nothing to do, took 14 us for 32 rows
+// of 8 sequences in 20 pieces.)
 struct MergeParams {
     const paged::MergeInfo *info;
     const float *part_O, *part_LSE;
@@ -1020,19 +1043,25 @@ struct MergeParams {
 };
 constexpr int kMergeThreads = 512;
 constexpr int kMergeMost = 512;  // CTAs at most
+constexpr int kMergeBlocks = 2;  // per SM
 
 template <int DL, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) fa_latent_merge_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks) fa_latent_merge_kernel(const MergeParams p) {
     constexpr int kAcross = DL / 4, kPlaces = kMergeThreads / kAcross;
     __shared__ float4 sums[kMergeThreads];
     __shared__ int before[kMergeMost], warp_rows[kMergeThreads / 32];
+    __shared__ int4 units[kMergeMost];  // pieces, first slot, rows of a slot, first row of all
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     after_previous();
     let_next_start();
     // rows of the cut blocks up to this one's
     static_assert(kMergeMost == kMergeThreads, "a CTA per thread");
     int rows = 0;
-    if (tid < p.ctas) rows = p.info[tid].last_cta >= 0 ? p.info[tid].rows : 0;
+    if (tid < p.ctas) {
+        const paged::MergeInfo u = p.info[tid];
+        rows = u.last_cta >= 0 ? u.rows : 0;
+        units[tid] = make_int4(u.last_cta - tid + 1, u.slot, u.slot_rows, u.head0);
+    }
     int incl = rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1054,40 +1083,46 @@ __global__ void __launch_bounds__(kMergeThreads) fa_latent_merge_kernel(const Me
     const int per_block = kPlaces / groups;
     const int place = tid / kAcross, col = tid % kAcross, group = place % groups;
     for (int x0 = blockIdx.x * per_block; x0 < total_rows; x0 += gridDim.x * per_block) {
-        const int x = x0 + place / groups;
-        const bool there = x < total_rows;
-        // the last CTA with no more than x rows before it that has rows: its block
+        const bool there = x0 + place / groups < total_rows;
+        const int x = min(x0 + place / groups, total_rows - 1);
+        // the last CTA with no more than x rows before it: its block
         int c = 0;
+#pragma unroll
         for (int step = kMergeMost / 2; step > 0; step >>= 1)
-            if (before[c + step] <= min(x, total_rows - 1)) c += step;
-        paged::MergeInfo u = p.info[c];
-        const int row = min(x, total_rows - 1) - before[c], n = u.last_cta - c + 1;
-        auto at = [&](int s) { return static_cast<size_t>(s == 0 ? u.slot : 2 * (c + s)) * u.slot_rows + row; };
-        float m = -INFINITY, total = 0.f;
-        for (int s = lane; s < n; s += 32) m = fmaxf(m, p.part_LSE[at(s)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // the weight of a piece; one that saw nothing weighs 0, one with NaN NaN
-        auto weight = [&](float x) { return x == -INFINITY ? 0.f : expf(x - m); };
-        for (int s = lane; s < n; s += 32) total += weight(p.part_LSE[at(s)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kBatch = 8;  // pieces in flight
-        for (int s0 = group; s0 < n; s0 += kBatch * groups) {
-            float4 o[kBatch];
-            float w[kBatch];
+            if (before[c + step] <= x) c += step;
+        const int4 u = units[c];
+        const int row = x - before[c], n = u.x;
+        auto at = [&](int s) { return static_cast<size_t>(s == 0 ? u.y : 2 * (c + s)) * u.z + row; };
+        constexpr int kBatch = 4;  // pieces in flight
+        float4 o[kBatch];
+        float w[kBatch];
+        auto fetch = [&](int s0) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int s = s0 + i * groups;
-                if (s >= n) break;
+                const int s = min(s0 + i * groups, n - 1);
                 o[i] = *reinterpret_cast<const float4 *>(p.part_O + at(s) * DL + 4 * col);
                 w[i] = p.part_LSE[at(s)];
             }
+        };
+        const float first = lane < n ? p.part_LSE[at(lane)] : -INFINITY;
+        fetch(group);
+        float m = first, total = 0.f;
+        for (int s = lane + 32; s < n; s += 32) m = fmaxf(m, p.part_LSE[at(s)]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        // the weight of a piece; one that saw nothing weighs 0, one with NaN NaN
+        auto weight = [&](float x) { return x == -INFINITY ? 0.f : expf(x - m); };
+        total = weight(first);
+        for (int s = lane + 32; s < n; s += 32) total += weight(p.part_LSE[at(s)]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = group; s0 < n; s0 += kBatch * groups) {
+            if (s0 != group) fetch(s0);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (s0 + i * groups >= n) break;
-                const float f = weight(w[i]);
+                const float f = s0 + i * groups < n ? weight(w[i]) : 0.f;
+                if (f == 0.f) continue;  // (a piece that saw nothing, or none)
                 acc.x = fmaf(f, o[i].x, acc.x);
                 acc.y = fmaf(f, o[i].y, acc.y);
                 acc.z = fmaf(f, o[i].z, acc.z);
@@ -1107,7 +1142,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_latent_merge_kernel(const Me
         if (!there || group != 0) continue;
         const bool none = total == 0.f;
         const float inv = none ? 0.f : 1.f / total;
-        const size_t g = static_cast<size_t>(u.head0) + row;
+        const size_t g = static_cast<size_t>(u.w) + row;
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.O) + g * DL + 4 * col) =
             make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
         if (col == 0) p.LSE[g] = none ? -INFINITY : m + logf(total);
