@@ -2,11 +2,16 @@
 // latent normalised, the rotary part of the key and those of the queries rotated.
 //
 // An item is one token's row of the cache, or up to kHeads of its queries' rotary parts; a warp
-// takes one item at a time. With r = 1 / sqrt(mean(c^2) + eps) over the DL latent elements the
-// row is (c r w, rotated k_rope); rotations are those of fa_rope_kernel.cuh (exact phases, a
-// row of 64 elements to 8 lanes, partners read from a copy in shared memory). The loads of
-// an item start before its place in the cache is searched for and its angles are computed.
-// Bound by memory for prompts, and by the latency of those two for single tokens.
+// takes an equal share of the line of items, so that a token's place in the cache and its angles
+// are found once for its items of the warp. With r = 1 / sqrt(mean(c^2) + eps) over the DL
+// latent elements the row is (c r w, rotated k_rope); rotations are those of fa_rope_kernel.cuh
+// (exact phases, a row of 64 elements to 8 lanes, partners read from a copy in shared memory).
+// The loads of an item start before its place is searched for and its angles are computed.
+//
+// What bounds it: instructions for prompts (24 prompts of 1-2000 tokens, 12 heads, DL = 256, in
+// 15.5 us, 3.5 TB/s; 20.4 with items dealt in turn, each finding its own place and angles; 15.9
+// with the next item's loads ahead, which cost registers and with them warps), and for single
+// tokens the latency of place, page and angles (3.3 us).
 #pragma once
 
 #include <cstdint>
@@ -21,6 +26,8 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kSteps = 4;           // rows of queries per lane and item
 constexpr int kHeads = 4 * kSteps;  // heads per item
+// blocks an SM holds at once, by their registers (80 and 110)
+constexpr int blocks_per_sm(int64_t dl) { return dl == 512 ? 2 : 3; }
 
 struct AppendParams {
     rope::Params r;  // rotation, batch and pages; q and q_out
@@ -46,11 +53,14 @@ __global__ void __launch_bounds__(kAppendThreads) fa_latent_append_kernel(const 
     const int partner_l = MODE == kLane ? partner<MODE>(8 * l, half_r) / 8 : l;
     after_previous();
     let_next_start();
-    const long long step = static_cast<long long>(gridDim.x) * kAppendWarps;
-    for (long long i = static_cast<long long>(blockIdx.x) * kAppendWarps + warp; i < p.items; i += step) {
-        const int m = static_cast<int>(i / p.parts), part = static_cast<int>(i - static_cast<long long>(m) * p.parts);
-        const int h0 = (part - 1) * kHeads + g;
-        uint4 in[kSteps], k_in = make_uint4(0, 0, 0, 0);
+    // this warp's items: the w-th of equal shares of their line
+    const long long w = static_cast<long long>(blockIdx.x) * kAppendWarps + warp;
+    const long long warps = static_cast<long long>(gridDim.x) * kAppendWarps;
+    const long long begin = p.items * w / warps, end = p.items * (w + 1) / warps;
+    if (begin >= end) return;
+    int m = static_cast<int>(begin / p.parts), part = static_cast<int>(begin - static_cast<long long>(m) * p.parts);
+    uint4 in[kSteps], k_in = make_uint4(0, 0, 0, 0);
+    auto load = [&](int m, int part, uint4(&in)[kSteps], uint4 &k_in) {
         if (part == 0) {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.c + m * p.c_token);
 #pragma unroll
@@ -58,16 +68,26 @@ __global__ void __launch_bounds__(kAppendThreads) fa_latent_append_kernel(const 
                 in[x] = lane + 32 * x < kPer ? src[lane + 32 * x] : make_uint4(0, 0, 0, 0);
             if (g == 0) k_in = reinterpret_cast<const uint4 *>(p.k + m * p.k_token)[l];
         } else {
+            const int h0 = (part - 1) * kHeads + g;
             const uint16_t *src = p.r.q.p + m * p.r.q.token + h0 * p.r.q.head + 8 * l;
 #pragma unroll
             for (int x = 0; x < kSteps; ++x)
                 if (h0 + 4 * x < p.r.H) in[x] = *reinterpret_cast<const uint4 *>(src + 4 * x * p.r.q.head);
         }
-        const Place where = place<true>(p.r, m, 0);
-        f2 C[4], S[4];
-        if (half_r > 0) {
-            angles(cs, p.r, where.pos);
-            coefficients<MODE, false>(cs, half_r, l, C, S);
+    };
+    int placed = -1;
+    Place where{0, false, -1};
+    f2 C[4], S[4];
+    for (long long i = begin; i < end; ++i, part = part + 1 < p.parts ? part + 1 : 0, m += part == 0) {
+        load(m, part, in, k_in);
+        const int h0 = (part - 1) * kHeads + g;
+        if (m != placed) {
+            placed = m;
+            where = place<true>(p.r, m, 0);
+            if (half_r > 0) {
+                angles(cs, p.r, where.pos);
+                coefficients<MODE, false>(cs, half_r, l, C, S);
+            }
         }
         // a row's 8 elements of this lane from its staged copy, rotated
         auto rotated = [&](const uint4 *at) -> uint4 {

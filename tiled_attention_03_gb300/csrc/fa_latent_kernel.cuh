@@ -57,7 +57,9 @@ constexpr int kBK = 64;     // keys per tile
 constexpr int kDR = 64;     // rotary elements of a row
 constexpr int kThreads = 256;
 constexpr int kLoadWarp = 4, kScoreWarp = 5, kOutWarp = 6, kPlanWarp = 7;
-constexpr int kTicks = 3;   // a block's start and end, in tiles
+// A block's start and end, in tiles (of 3, 6, 8 and 11: 40 sequences of 0-16000 rows with 128 heads 69,
+// 59, 59 and 61 us, 96 of 0-12000 with 12 heads at DL 256 32, 29, 30 and 29).
+constexpr int kTicks = 6;
 constexpr int kUnitSlots = 4;
 constexpr int kUnitConsumers = 7;  // warps that take the pieces: all but the scheduler
 constexpr int kMaxStages = 4;

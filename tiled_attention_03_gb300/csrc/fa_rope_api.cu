@@ -583,7 +583,7 @@ fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_row
     a.items = total_q * a.parts;
     // a warp per item up to what the SMs hold at once
     const long long each = (a.items + fa::latent::kAppendWarps - 1) / fa::latent::kAppendWarps;
-    const long long most = static_cast<long long>(di.sm_count) * 4;
+    const long long most = static_cast<long long>(di.sm_count) * fa::latent::blocks_per_sm(dl);
     const unsigned blocks = static_cast<unsigned>(each < most ? each : most);
     const int mode = mode_of(r);
     const bool bf16 = cache->dtype == FA_DTYPE_BF16;
