@@ -568,8 +568,10 @@ size_t fa_forward_latent_workspace_bytes(int64_t d_latent);
  * H_kv x page_size float32, contiguous: entry (page, head, token). Entries of keys that no new
  * token sees, and of slots past a sequence's end, are left as they are. A page that several
  * sequences of the batch share gets each one's a_j, added in any order; otherwise the
- * results are the same every time. weights overlaps no other buffer. One kernel launch, no
- * workspace. Everything else as fa_forward_paged.
+ * results are the same every time. weights overlaps no other buffer. total_q * H, and H_kv
+ * times the tiles of 128 keys that max_pages pages hold, are at most 2^30. A token that offsets in
+ * no order give to several sequences counts for the first. One kernel launch, no workspace.
+ * Everything else as fa_forward_paged.
  */
 fa_status fa_paged_weights(const void *Q, const float *LSE, float *weights, const fa_paged_cache *cache,
                            const int32_t *block_table, int64_t max_pages, const int32_t *cu_seqlens_q,
@@ -634,8 +636,9 @@ int64_t fa_launch_count(void);
  * fa_backward or fa_backward_varlen, the position counts units instead: every
  * CTA of its dK/dV kernel skips the K/V load of its unit number
  * `kv_position`, with the same outcome. fa_forward_paged takes the hook in the kernel
- * that runs chunks of new tokens; calls and kernels without such waits (single steps
- * over the paged cache, the append, norm and rotation) spend it without effect.
+ * that runs chunks of new tokens, fa_forward_latent and fa_paged_weights in theirs (the position
+ * counts a CTA's key tiles); calls and kernels without such waits (single steps over the paged
+ * cache, the appends, norm and rotation, the eviction) spend it without effect.
  */
 void fa_test_arm_fault(int32_t kv_position);
 

@@ -150,6 +150,15 @@ def test_many_sequences(B):
     check_gather(paged(lens, 4, 2, 64, torch.bfloat16, 16, seed=2), 0.125, "causal")
 
 
+@pytest.mark.parametrize("H,Hk,d", [(64, 2, 64), (48, 1, 128), (32, 1, 256), (5, 1, 32)])
+@pytest.mark.parametrize("most", [2, 3, 7])
+def test_units_of_different_numbers_of_rows(H, Hk, d, most):
+    """Tiles of keys that one, two, three and more tiles of rows see, in all orders: the warps that share a
+    unit's rows and those that have one to themselves stay in step."""
+    lens = [(1 + i * i % most, 700 + 61 * i) for i in range(24)]
+    check_gather(paged(lens, H, Hk, d, torch.bfloat16, 64, seed=most), d ** -0.5, "causal")
+
+
 def test_rows_without_keys_add_nothing():
     """A position before 0 under a mask leaves LSE = -infinity; its scores may be anything."""
     b = paged([(7, 3), (2, 40)], 4, 2, 64, torch.bfloat16, 16, seed=2)
@@ -189,6 +198,19 @@ def test_page_numbers_outside_the_cache_are_not_written():
     gather(q, lse, got[2:-2], cache, table, cu, lens, 0.125, "causal")
     want[2:-2][lost] = 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("B,T", [(2, 1), (40, 30), (70, 3)])
+def test_offsets_in_no_order_give_a_token_to_the_first_sequence(B, T):
+    """Every second sequence claims all tokens: the others of them add nothing."""
+    q, cache, table, cu, lens, seqs = paged([(T, 300)] + [(0, 300)] * (B - 1), 8, 2, 64, torch.bfloat16, 16, seed=4)
+    lse = lse_of(seqs, 2, 0.125, "causal", (0, 0), T)
+    want = torch.ones(cache.num_pages, 2, 16, device=DEV)
+    got = want.clone()
+    gather(q, lse, want, cache, table, cu, lens, 0.125, "causal")
+    gather(q, lse, got, cache, table, i32(([0, T] * B)[:B + 1]), lens, 0.125, "causal")
+    assert torch.equal(got, want) and not bool((want == 1).all())
+    gather(q, lse, got, cache, table, i32([-5, 0] + [T + 9, -1] * B)[:B + 1].contiguous(), lens, 0.125, "causal")
 
 
 @pytest.mark.parametrize("new", [1, 40])

@@ -94,7 +94,9 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
     p.first = static_cast<int>(first < most ? first : most);
     p.recent = static_cast<int>(recent < most ? recent : most);
     // CTAs per sequence and head: one for every 128 bytes of a row (a key and its value), twice as many
-    // where that leaves SMs without one; but at least 16 KB to move for each.
+    // where that leaves SMs without one (24 units of 500 rows of 256 bytes: 12.7 us, 14.5 with no
+    // more); but at least 16 KB to move for each (small budgets 9.1 us, 12.8 with at least 4 KB; those
+    // 24 units 14.7 with at least 64).
     const int row_bytes = p.d * 4;
     const int64_t units = B * cache->H_kv;
     int ctas = row_bytes / 128 < kMaxCluster ? row_bytes / 128 : kMaxCluster;
@@ -102,7 +104,8 @@ extern "C" fa_status fa_paged_evict(const fa_paged_cache *cache, float *weights,
     while (ctas > 1 && static_cast<int64_t>(p.budget) * row_bytes < ctas * 16384) ctas /= 2;
     const int columns = row_bytes / ctas;
     while ((16 << p.piece_log2) < columns) ++p.piece_log2;
-    // shared memory: two CTAs to an SM; all of it where there are no two
+    // shared memory: two CTAs to an SM; all of it where there are no two (always all: 58 -> 79 us
+    // for many sequences)
     const int shared = units * ctas <= di.sm_count ? kMostShared : kMostShared / 2 / 1024 * 1024;
     const int room = (shared - kSharedBytes) / 128 * 128;
     const int rows = room / (kDepth * columns + kLists * 20);

@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_evict_kernel(const Params p) {
             }
             shift -= 8;
         }
+    } else if (ctas > 1) {
+        cluster_sync();  // all have started: their shared memory is written below
     }
 
     // ---- move. A thread copies the same 16-byte piece of every kThreads / 2^piece_log2-th row.

@@ -87,6 +87,7 @@ struct Params {
     int chunk;         // tokens per TMA box: min(page size, kBK)
     int page_step, page_none;  // the map's last coordinate: page * page_step; past its end
     int wl, wr;        // key j visible to the query at position i iff i - wl <= j <= i + wr
+    unsigned line_most;  // the longest line of work that ascending offsets can make
     float scale_log2;
     unsigned long long wait_budget_ns;
     unsigned int *status;
@@ -409,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         scanned(seq_work(load_seq(b0 + static_cast<int>(threadIdx.x), p), p), more);
         W = paged::add_work(W, more);
     }
-    if (W == paged::kNoLine) W = 0;
+    // more than an ordered batch of these sizes can have: offsets in no order, the batch is left alone
+    if (W > p.line_most) W = 0;
     const unsigned T = (W + workers - 1) / workers;
     const unsigned w0 = min(worker * T, W), w1 = min(w0 + T, W);
     auto start_at = [&](int b, const Seq &s, unsigned incl, unsigned w) {

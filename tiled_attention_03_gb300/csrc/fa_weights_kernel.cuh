@@ -51,6 +51,9 @@ constexpr int kUnitConsumers = 4 * kTeams + 3;  // warps that take the units: al
 constexpr int kMaxStages = 8;
 constexpr int kBufs = 4;  // of scores
 constexpr int kLses = 8;  // of their rows' LSE: more, as queries are loaded after the LSE before them
+// A team's tiles follow each other by kTeams, so it meets every use of its buffer and slots: a wait
+// tells two uses of a barrier apart only when they follow each other.
+static_assert(kBufs == kTeams && (kTeams & (kTeams - 1)) == 0 && kLses % kTeams == 0, "buffers of a team");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmem = 0;  // all columns are allocated: they start at 0
 constexpr unsigned kStatusTimeout = 4;
@@ -282,11 +285,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto unit_of = [&](long long i) {
             return i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         };
+        // A token belongs to the first sequence that claims it, so that offsets in no order make no
+        // more work than ordered ones.
         long long base = 0, next = lane;
         bool ok = true;
-        int k = 0;
+        int k = 0, claimed = 0;
         for (int b0 = 0; ok && b0 < p.B; b0 += 32) {
-            const Seq s = load_seq(b0 + lane, p);
+            Seq s = load_seq(b0 + lane, p);
+            int ends = s.q0 + s.nq;  // the most of the sequences' ends up to this one
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, ends, o);
+                if (lane >= o) ends = max(ends, x);
+            }
+            int before_me = __shfl_up_sync(0xffffffffu, ends, 1);
+            before_me = max(lane > 0 ? before_me : 0, claimed);
+            if (s.q0 < before_me) s.nq = 0;
+            claimed = max(claimed, __shfl_sync(0xffffffffu, ends, 31));
             const int tiles = key_tiles(s, p);
             long long incl = static_cast<long long>(tiles) * p.H_kv;
 #pragma unroll
@@ -559,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit u = take(k, ok);
             if (!ok || u.b < 0) break;
             if (u.n == 0) continue;
-            const int me = (team + k) % kTeams;  // tiles me, me + kTeams, ... of the unit are this team's
+            const int me = (team - i) & (kTeams - 1);  // tiles me, me + kTeams, ... of the unit are this team's
             if (u.n == 1 && me != 0) {
                 ++i;
                 continue;
@@ -630,9 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the other teams hand their sums to the first
                 const int slot = joined % 2;
                 float *const sum_of = sums + slot * (kTeams - 1) * kBK + own;
+                // (the first as well, as the others may not have handed it those of two units ago)
+                ok = wait(kBarSumEmpty + slot, ((joined / 2) & 1) ^ 1);
+                if (!ok) break;
                 if (me != 0) {
-                    ok = wait(kBarSumEmpty + slot, ((joined / 2) & 1) ^ 1);
-                    if (!ok) break;
                     sum_of[(me - 1) * kBK] = sum;
                     mbar_arrive(bar(kBarSumFull + slot));
                 } else {
