@@ -57,9 +57,9 @@ constexpr int kBK = 64;     // keys per tile
 constexpr int kDR = 64;     // rotary elements of a row
 constexpr int kThreads = 256;
 constexpr int kLoadWarp = 4, kScoreWarp = 5, kOutWarp = 6, kPlanWarp = 7;
-// A block's start and end, in tiles (of 3, 6, 8 and 11: 40 sequences of 0-16000 rows with 128 heads 69,
-// 59, 59 and 61 us, 96 of 0-12000 with 12 heads at DL 256 32, 29, 30 and 29).
-constexpr int kTicks = 6;
+// A block's start and end, in tiles (at 3, 4, 6 and 8: 40 sequences of 0-16000 rows with 128 heads 54.6,
+// 54.0, 55.8 and 55.6 us, 96 of 0-12000 with 12 heads at DL 256 24.4, 24.8, 26.4 and 27.1).
+constexpr int kTicks = 3;
 constexpr int kUnitSlots = 4;
 constexpr int kUnitConsumers = 7;  // warps that take the pieces: all but the scheduler
 constexpr int kMaxStages = 4;
@@ -656,24 +656,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait = [&](int b, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, abort_flag, budget));
         };
-        // Rows of key tile t (keys kv0 ..) outside keys lo .. hi: 0 times whatever the page
-        // holds there must be 0.
-        auto zero_rows = [&](int t, int kv0, int lo, int hi) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
+        // Latent columns of rows r0 .. r1 - 1 of key tile t: 0 times whatever the page holds there
+        // must be 0.
+        auto zero_rows = [&](int t, int r0, int r1) {
             uint8_t *base = smem + L::kK + (t % L::kStages) * L::kTile;
-            constexpr int kPer = L::kRegions * 8;  // 16-byte pieces of a row
-            auto zero = [&](int r0, int r1) {
-                for (int c = r0 * kPer + lane; c < r1 * kPer; c += 32) {
-                    const int r = c / kPer, x = c % kPer, g = x >> 3;  // region
-                    const int at = g == L::kRegions - 1 ? L::kParts * L::kPart + (r >> 3) * L::kAtom
-                                                        : (g >> 1) * L::kPart + (r >> 3) * L::kGroup + (g & 1) * L::kAtom;
-                    *reinterpret_cast<uint4 *>(base + at + (r & 7) * 128 + (x & 7) * 16) = z;
-                }
-            };
-            zero(0, min(max(lo - kv0, 0), kBK));
-            zero(min(max(hi + 1 - kv0, 0), kBK), kBK);
-            fence_proxy_async_smem();
-            __syncwarp();
+            constexpr int kPer = DL / 8;  // 16-byte pieces of a row
+            for (int c = r0 * kPer + lane; c < r1 * kPer; c += 32) {
+                const int r = c / kPer, x = c % kPer;
+                *reinterpret_cast<uint4 *>(base + (x >> 4) * L::kPart + (r >> 3) * L::kGroup + ((x >> 3) & 1) * L::kAtom +
+                                           (r & 7) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
         };
         int t = 0, live = 0;  // key tiles, and pieces with tiles, so far
         bool ok = true;
@@ -687,14 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(kBarQFull + live % L::kQStages, (live / L::kQStages) & 1);
                 const uint64_t db = paged::tile_desc<128>(sQ(live), 16, 1024);
                 for (int x = 0; ok && x < n; ++x, ++t) {
-                    const int kv0 = (j0 + x) * kBK;
                     const uint32_t phase = (t / L::kStages) & 1;
                     const int st = t % L::kStages * L::kParts;
-                    if (kv0 < lo || kv0 + kBK - 1 > hi) {
-                        for (int part = 0; ok && part < L::kParts; ++part) ok = wait(kBarKFull + st + part, phase);
-                        if (!ok) break;
-                        zero_rows(t, kv0, lo, hi);
-                    }
                     // the scores before in this buffer have been read
                     if (t >= 2) ok = wait(kBarPFull + t % 2, (t / 2 - 1) & 1);
                     if (!ok) break;
@@ -729,21 +715,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 for (int x = 0; ok && x < n; ++x, ++t) {
+                    // the tile's rows a .. b hold keys lo .. hi: the product takes the steps of 16 that
+                    // have one of them, whose other rows become 0 (hidden keys' scores, which may be read
+                    // meanwhile, are not looked at)
+                    const int kv0 = (j0 + x) * kBK, a = max(lo - kv0, 0), b = min(hi - kv0, kBK - 1);
+                    const int c0 = a / 16, c1 = b / 16, st = t % L::kStages * L::kParts;
+                    if ((a & 15) != 0 || (b & 15) != 15) {
+                        for (int part = 0; ok && part < L::kParts; ++part)
+                            ok = wait(kBarKFull + st + part, (t / L::kStages) & 1);
+                        if (!ok) break;
+                        zero_rows(t, c0 * 16, a);
+                        zero_rows(t, b + 1, c1 * 16 + 16);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                     ok = wait(kBarPFull + t % 2, (t / 2) & 1);
                     if (ok && x == 0 && live > 0) ok = wait(kBarOFree, (live - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = paged::tile_desc<128>(sK(t), L::kAtom, L::kGroup);
                     const uint64_t db = paged::tile_desc<128>(sP(t), 16, 1024);
-                    const int st = t % L::kStages * L::kParts;
                     if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < L::kParts; ++s) {
 #pragma unroll
                             for (int c = 0; c < kBK / 16; ++c)
-                                umma_f16_ss(kTmem + L::kTmemO + s * R,
-                                            da + s * (L::kPart >> 4) + c * ((2 * L::kGroup) >> 4), db + c * 2, idesc_o,
-                                            x > 0 || c > 0 ? 1u : 0u);
+                                if (c >= c0 && c <= c1)
+                                    umma_f16_ss(kTmem + L::kTmemO + s * R,
+                                                da + s * (L::kPart >> 4) + c * ((2 * L::kGroup) >> 4), db + c * 2,
+                                                idesc_o, x > 0 || c > c0 ? 1u : 0u);
                             umma_commit(bar(kBarKEmpty + st + s));
                         }
                         umma_commit(bar(kBarPVDone + t % 2));
@@ -958,10 +958,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             // lane = a column of O, register = a row
-            // lanes 4 i .. 4 i + 3 trade four rows' columns, so that each has four columns of a row
             const size_t row0 = P.slot < 0 ? static_cast<size_t>(P.row0) : static_cast<size_t>(P.slot) * R;
-            const size_t at0 = (row0 + (lane & 3)) * DL + warp * 32 + (lane & ~3);
-            const bool b0 = lane & 1, b1 = lane & 2;
+            const size_t at0 = row0 * DL + warp * 32 + lane;
             constexpr int kParts = L::kParts;
             // 16 rows of two slices of O^T at a time (of one where there is one)
             constexpr int kAtOnce = kParts > 1 ? 2 : 1;
@@ -986,32 +984,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16 * kAtOnce; ++e)
                         y[e] = f[e % 16] == 0.f ? 0.f : __uint_as_float(o[e]) * f[e % 16];
-#pragma unroll
-                    for (int e = 0; e < 16 * kAtOnce; e += 2) {
-                        const float z = __shfl_xor_sync(0xffffffffu, b0 ? y[e] : y[e + 1], 1);
-                        y[e] = b0 ? z : y[e];
-                        y[e + 1] = b0 ? y[e + 1] : z;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16 * kAtOnce; e += 4)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float z = __shfl_xor_sync(0xffffffffu, b1 ? y[e + i] : y[e + i + 2], 2);
-                            y[e + i] = b1 ? z : y[e + i];
-                            y[e + i + 2] = b1 ? y[e + i + 2] : z;
-                        }
                     const size_t at = at0 + static_cast<size_t>(r0) * DL + part * 128;
+                    const int left = P.rows - r0;
+                    if (P.slot < 0) {
+                        uint16_t *to = static_cast<uint16_t *>(p.O) + at;
 #pragma unroll
-                    for (int e = 0; e < 16 * kAtOnce; e += 4) {
-                        const bool row_there = r0 + e % 16 + (lane & 3) < P.rows;
-                        const size_t to = at + e % 16 * DL + e / 16 * 128;
-                        if (P.slot < 0) {
-                            if (row_there)
-                                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.O) + to) =
-                                    make_uint2(pack2<BF16>(y[e], y[e + 1]), pack2<BF16>(y[e + 2], y[e + 3]));
-                        } else if (row_there) {
-                            *reinterpret_cast<float4 *>(p.part_O + to) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-                        }
+                        for (int e = 0; e < 16 * kAtOnce; ++e)
+                            if (e % 16 < left)
+                                to[e % 16 * DL + e / 16 * 128] = static_cast<uint16_t>(pack2<BF16>(y[e], 0.f));
+                    } else {
+                        float *to = p.part_O + at;
+#pragma unroll
+                        for (int e = 0; e < 16 * kAtOnce; ++e)
+                            if (e % 16 < left) to[e % 16 * DL + e / 16 * 128] = y[e];
                     }
                 }
             }
