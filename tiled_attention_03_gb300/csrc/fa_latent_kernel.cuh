@@ -263,21 +263,25 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) 
         : "r"(taddr)
         : "memory");
 }
-// 32 lanes x 16 consecutive columns, at both of two places, and the wait for them.
-__device__ __forceinline__ void tmem_ld16_two(uint32_t ta, uint32_t tb, uint32_t (&r)[32]) {
+// 16 or 32 columns of this warp's lanes; and the wait for them.
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(ta), "r"(tb)
-        : "memory");
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void ld_cols_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void ld_cols_wait(uint32_t (&r)[32]) { tmem_ld_wait(r); }
+
 // 32 lanes x 16 consecutive columns, and the wait for them.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -961,44 +965,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t row0 = P.slot < 0 ? static_cast<size_t>(P.row0) : static_cast<size_t>(P.slot) * R;
             const size_t at0 = row0 * DL + warp * 32 + lane;
             constexpr int kParts = L::kParts;
-            // 16 rows of two slices of O^T at a time (of one where there is one)
-            constexpr int kAtOnce = kParts > 1 ? 2 : 1;
-#pragma unroll 1
-            for (int r0 = 0; r0 < P.rows; r0 += 16) {
-                float f[16];
+            // 32 rows (or R) of a slice of O^T at a time; the next ones come while these are stored
+            constexpr int kAtOnce = R < 32 ? R : 32, kSteps = R / kAtOnce * kParts;
+            uint32_t o[2][kAtOnce];
+            auto fetch = [&](int x, uint32_t(&to)[kAtOnce]) {
+                if (x < kSteps) ld_cols(tl + L::kTmemO + x * kAtOnce, to);
+            };
+            auto store = [&](int x, uint32_t(&from)[kAtOnce]) {
+                const int part = x * kAtOnce / R, r0 = x * kAtOnce % R, left = P.rows - r0;
+                float y[kAtOnce];
+                // a row without keys: 0, whatever its column holds
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(factor + r0 + e);
-                    f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+                for (int e = 0; e < kAtOnce; e += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(factor + r0 + e);
+                    y[e] = f.x == 0.f ? 0.f : __uint_as_float(from[e]) * f.x;
+                    y[e + 1] = f.y == 0.f ? 0.f : __uint_as_float(from[e + 1]) * f.y;
+                    y[e + 2] = f.z == 0.f ? 0.f : __uint_as_float(from[e + 2]) * f.z;
+                    y[e + 3] = f.w == 0.f ? 0.f : __uint_as_float(from[e + 3]) * f.w;
                 }
-#pragma unroll 1
-                for (int part = 0; part < kParts; part += kAtOnce) {
-                    uint32_t o[16 * kAtOnce];
-                    const uint32_t from = tl + L::kTmemO + part * R + r0;
-                    if constexpr (kAtOnce == 2)
-                        tmem_ld16_two(from, from + R, o);
-                    else
-                        tmem_ld16(from, o);
-                    float y[16 * kAtOnce];
-                    // a row without keys: 0, whatever its column holds
+                const size_t at = at0 + static_cast<size_t>(r0) * DL + part * 128;
+                if (P.slot < 0) {
+                    uint16_t *to = static_cast<uint16_t *>(p.O) + at;
 #pragma unroll
-                    for (int e = 0; e < 16 * kAtOnce; ++e)
-                        y[e] = f[e % 16] == 0.f ? 0.f : __uint_as_float(o[e]) * f[e % 16];
-                    const size_t at = at0 + static_cast<size_t>(r0) * DL + part * 128;
-                    const int left = P.rows - r0;
-                    if (P.slot < 0) {
-                        uint16_t *to = static_cast<uint16_t *>(p.O) + at;
-#pragma unroll
-                        for (int e = 0; e < 16 * kAtOnce; ++e)
-                            if (e % 16 < left)
-                                to[e % 16 * DL + e / 16 * 128] = static_cast<uint16_t>(pack2<BF16>(y[e], 0.f));
-                    } else {
-                        float *to = p.part_O + at;
-#pragma unroll
-                        for (int e = 0; e < 16 * kAtOnce; ++e)
-                            if (e % 16 < left) to[e % 16 * DL + e / 16 * 128] = y[e];
+                    for (int e = 0; e < kAtOnce; e += 2) {
+                        const uint32_t two = pack2<BF16>(y[e], y[e + 1]);
+                        if (e < left) to[e * DL] = static_cast<uint16_t>(two);
+                        if (e + 1 < left) to[(e + 1) * DL] = static_cast<uint16_t>(two >> 16);
                     }
+                } else {
+                    float *to = p.part_O + at;
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e)
+                        if (e < left) to[e * DL] = y[e];
                 }
+            };
+#pragma unroll 1
+            for (int x = 0; x < kSteps; ++x) {
+                fetch(x, o[0]);
+                ld_cols_wait(o[0]);
+                store(x, o[0]);
             }
             tc_fence_before();
             mbar_arrive(bar(kBarOFree));

@@ -76,7 +76,7 @@ extern "C" fa_status fa_paged_weights(const void *Q, const float *LSE, float *we
     const int64_t max_keys = max_pages * cache->page_size;
     const int64_t kLimit = int64_t{1} << 29;
     if (total_q > kLimit || max_pages > kLimit || max_keys > kLimit || B > kLimit || H > kLimit ||
-        total_q * H > (int64_t{1} << 30) || (max_keys / fa::weights::kBK + 1) * H_kv > (int64_t{1} << 30))
+        total_q * H > (int64_t{1} << 30) || (max_keys / 128 + 1) * H_kv > (int64_t{1} << 30))
         return FA_ERR_UNSUPPORTED;
     // Rows of a tile: a sequence's on average (new tokens x query heads of a K/V head), 16, 64 or
     // 128; of them the heads of a group, or a divisor of them, for as many tokens as fit. (With 16,
@@ -130,7 +130,8 @@ extern "C" fa_status fa_paged_weights(const void *Q, const float *LSE, float *we
     x.rows = rows;
     x.sms = static_cast<unsigned>(di.sm_count);
     fa_host::PageSteps steps;
-    const int64_t box = cache->page_size < fa::weights::kBK ? cache->page_size : fa::weights::kBK;
+    const int64_t keys = fa::weights::tile_keys(static_cast<int>(d), rows);
+    const int64_t box = cache->page_size < keys ? cache->page_size : keys;
     if (!fa_host::page_steps(*cache, &steps) ||
         !fa_host::make_map_rows(&x.q, Q, bf16, total_q, H, d, static_cast<uint32_t>(pf), static_cast<uint32_t>(tpt)) ||
         !fa_host::make_map_pages(&x.k, cache->k, *cache, steps, static_cast<uint32_t>(box)))

@@ -42,7 +42,9 @@
 namespace fa {
 namespace weights {
 
-constexpr int kBK = 128;  // keys per tile
+// Keys of a tile: 128, or 256 (two products, one behind the other) for narrow tiles of rows, where what
+// a unit costs besides its products is most of it.
+constexpr int tile_keys(int d, int rows) { return rows == 16 && d <= 128 ? 256 : 128; }
 constexpr int kTeams = 4;
 constexpr int kThreads = (4 * kTeams + 4) * 32;
 constexpr int kPlanWarp = 4 * kTeams, kIssueWarp = kPlanWarp + 1, kQWarp = kPlanWarp + 2, kKWarp = kPlanWarp + 3;
@@ -79,6 +81,8 @@ struct Params {
 template <int D, int R>
 struct Smem {
     using P = paged::Smem<D>;  // the layout of key tiles: groups of 8 rows, their regions side by side
+    static constexpr int kBK = tile_keys(D, R);
+    static constexpr int kHalves = kBK / 128;
     static constexpr int kTile = kBK / 8 * P::kGroup;
     static constexpr int kQRegion = R * P::kRowBytes;
     static constexpr int kQBytes = P::kRegions * kQRegion;
@@ -86,7 +90,7 @@ struct Smem {
     static constexpr int kMost = 227 * 1024 - kSmall;
     // up to four tiles of queries that leave four of keys; two of keys where one is 64 KB, or where
     // units have many tiles of rows, which then come faster than keys
-    static constexpr int kQFit = (kMost - (D == 256 || R == 128 ? 2 : 4) * kTile) / kQBytes;
+    static constexpr int kQFit = (kMost - (D == 256 || R == 128 ? 2 : 4) * kTile / kHalves) / kQBytes;
     static constexpr int kQStages = kQFit < 4 ? kQFit : 4;
     static constexpr int kKFit = (kMost - kQStages * kQBytes) / kTile;
     static constexpr int kKStages = kKFit < kMaxStages ? kKFit : kMaxStages;
@@ -99,6 +103,7 @@ struct Smem {
     static constexpr int kLse = kRing + kUnitSlots * 64;     // kLses x R, times -log2 e
     static constexpr int kSums = kLse + kLses * R * 4;       // two units' sums of three teams
     static constexpr int kBytes = kSums + 2 * (kTeams - 1) * kBK * 4;
+    static_assert(kBufs * kHalves * R <= kTmemCols, "TMEM columns");
     static_assert(kLse % 16 == 0 && kBytes - kBar <= kSmall, "layout");
     static constexpr int kAlloc = kBytes > 120 * 1024 ? kBytes : 120 * 1024;  // one CTA per SM
 };
@@ -142,11 +147,13 @@ __device__ __forceinline__ Seq load_seq(int b, const Params &p) {
     return s;
 }
 // The first tile of keys that a token of the sequence sees, and how many follow.
+template <int kBK>
 __device__ __forceinline__ int first_tile(const Seq &s, const Params &p) {
     return max(0, s.nk - s.nq - p.wl) / kBK;
 }
+template <int kBK>
 __device__ __forceinline__ int key_tiles(const Seq &s, const Params &p) {
-    return s.nq == 0 || s.nk == 0 ? 0 : max(0, (s.nk - 1) / kBK - first_tile(s, p) + 1);
+    return s.nq == 0 || s.nk == 0 ? 0 : max(0, (s.nk - 1) / kBK - first_tile<kBK>(s, p) + 1);
 }
 // Tokens lo .. hi (hi < lo: none) see a key of keys k0 .. k1.
 __device__ __forceinline__ void tokens_of(const Unit &u, int k0, int k1, const Params &p, int &lo, int &hi) {
@@ -189,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ Params p) {
     using L = Smem<D, R>;
     using P = typename L::P;
+    constexpr int kBK = L::kBK, kHalves = L::kHalves;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *const smem = smem_raw;
     const uint32_t sbase = smem_u32(smem);
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             before_me = max(lane > 0 ? before_me : 0, claimed);
             if (s.q0 < before_me) s.nq = 0;
             claimed = max(claimed, __shfl_sync(0xffffffffu, ends, 31));
-            const int tiles = key_tiles(s, p);
+            const int tiles = key_tiles<kBK>(s, p);
             long long incl = static_cast<long long>(tiles) * p.H_kv;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int y = p.by_heads.of(max(x, 0));
                 u.h = x - y * p.H_kv;
                 u.q_off = u.nk - u.nq;
-                u.j = y + first_tile(Seq{0, u.nq, u.nk}, p);
+                u.j = y + first_tile<kBK>(Seq{0, u.nq, u.nk}, p);
                 int lo, hi;
                 tokens_of(u, u.j * kBK, min(u.j * kBK + kBK, u.nk) - 1, p, lo, hi);
                 u.first = p.by_tpt.of(lo) * p.subs;
@@ -523,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kIssueWarp) {
         // ================================================================ S^T = K Q^T
-        constexpr uint32_t idesc = idesc_f16_ab(BF16, kBK, R, false, false);
+        constexpr uint32_t idesc = idesc_f16_ab(BF16, 128, R, false, false);
         constexpr int kSteps = P::kCols / 16;  // K-steps of 16 columns per region
         int t = 0, i = 0, k = 0;
         bool ok = true;
@@ -539,12 +547,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dq = paged::tile_desc<P::kRowBytes>(sQ(i), 16, P::kAtom);
-                const uint32_t d = kTmem + (i % kBufs) * R;
+                const uint32_t d = kTmem + (i % kBufs) * kHalves * R;
                 if (elect_one()) {
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c)
-                        umma_f16_ss(d, dk + (c / kSteps) * (P::kAtom >> 4) + (c % kSteps) * 2,
-                                    dq + (c / kSteps) * (L::kQRegion >> 4) + (c % kSteps) * 2, idesc, c > 0 ? 1u : 0u);
+                    for (int c = 0; c < kHalves * D / 16; ++c) {
+                        constexpr int kOf = D / 16;
+                        umma_f16_ss(d + c / kOf * R,
+                                    dk + c / kOf * (16 * P::kGroup >> 4) + (c % kOf / kSteps) * (P::kAtom >> 4) +
+                                        (c % kSteps) * 2,
+                                    dq + (c % kOf / kSteps) * (L::kQRegion >> 4) + (c % kSteps) * 2, idesc,
+                                    c % kOf > 0 ? 1u : 0u);
+                    }
                     umma_commit(bar(kBarSFull + i % kBufs));
                     umma_commit(bar(kBarQEmpty + i % L::kQStages));
                 }
@@ -579,17 +592,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++i;
                 continue;
             }
-            const int key = u.j * kBK + own;
-            const bool there = key < u.nk;
-            int page = -1;
-            if (there && me == 0)
-                page = p.table[static_cast<size_t>(u.b) * p.max_pages + (key >> p.page_log2)];
-            // tokens that see this key, and those that see every key of the tile
-            int lo, hi, all_lo, all_hi, x1, x2;
-            tokens_of(u, key, key, p, lo, hi);
+            // this thread's keys; their pages; the tokens that see them, and those that see every key of the tile
+            int key[kHalves], page[kHalves], lo[kHalves], hi[kHalves], all_lo, all_hi, x1, x2;
+#pragma unroll
+            for (int y = 0; y < kHalves; ++y) {
+                key[y] = u.j * kBK + 128 * y + own;
+                page[y] = -1;
+                if (key[y] < u.nk && me == 0)
+                    page[y] = p.table[static_cast<size_t>(u.b) * p.max_pages + (key[y] >> p.page_log2)];
+                tokens_of(u, key[y], key[y], p, lo[y], hi[y]);
+            }
             tokens_of(u, u.j * kBK + kBK - 1, u.j * kBK + kBK - 1, p, all_lo, x1);
             tokens_of(u, u.j * kBK, u.j * kBK, p, x2, all_hi);
-            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+            float a[kHalves][4];
+#pragma unroll
+            for (int y = 0; y < kHalves; ++y) a[y][0] = a[y][1] = a[y][2] = a[y][3] = 0.f;
             for (int x = me; ok && x < u.n; x += kTeams) {
                 const int at = i + x, buf = at % kBufs, t0 = p.by_subs.of(u.first + x) * p.tpt;
                 ok = wait(kBarLFull + at % kLses, (at / kLses) & 1);
@@ -598,17 +615,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // rows that see this key, and whether that is every row of the tile for all keys (rows
                 // behind the sequence's last token may hold anything: they are not looked at)
-                const int c_lo = (lo - t0) * p.pf, c_hi = min(hi - t0 + 1, p.tpt) * p.pf;
                 const bool whole = t0 >= all_lo && t0 + p.tpt - 1 <= all_hi && p.tpt * p.pf == R;
                 const float *lse = lse_ring + at % kLses * R;
-                constexpr int kCols = R < 32 ? R : 32;
+                constexpr int kCols = R < 32 ? R : 32, kLoads = kHalves * R / kCols;
                 uint32_t r[2][kCols];  // the next columns come while these are summed
-                ld_cols(tl + buf * R, r[0]);
+                ld_cols(tl + buf * kHalves * R, r[0]);
 #pragma unroll
-                for (int h = 0; h < R; h += kCols) {
-                    uint32_t(&now)[kCols] = r[h / kCols & 1];
+                for (int z = 0; z < kLoads; ++z) {
+                    const int h = z * kCols % R, half = z * kCols / R;
+                    uint32_t(&now)[kCols] = r[z & 1];
                     ld_cols_wait(now);
-                    if (h + kCols < R) ld_cols(tl + buf * R + h + kCols, r[(h / kCols + 1) & 1]);
+                    if (z + 1 < kLoads) ld_cols(tl + buf * kHalves * R + (z + 1) * kCols, r[(z + 1) & 1]);
                     float y[kCols];
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
@@ -618,13 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ffma2(y[c], y[c + 1], sl2, sl2, v.x, v.y);
                         ffma2(y[c + 2], y[c + 3], sl2, sl2, v.z, v.w);
                     }
-                    if (h + kCols == R) {  // scores and LSE are read: the next ones may come
+                    if (z + 1 == kLoads) {  // scores and LSE are read: the next ones may come
                         tc_fence_before();
                         mbar_arrive(bar(kBarSEmpty + buf));
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kBarLEmpty + at % kLses));
                     }
                     if (!whole) {
+                        const int c_lo = (lo[half] - t0) * p.pf, c_hi = min(hi[half] - t0 + 1, p.tpt) * p.pf;
 #pragma unroll
                         for (int c = 0; c < kCols; ++c)
                             if (h + c < c_lo || h + c >= c_hi) y[c] = -INFINITY;
@@ -633,14 +651,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kCols; ++c) y[c] = ex2_approx(y[c]);
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
-                        fadd2(a0, a1, y[c], y[c + 1]);
-                        fadd2(a2, a3, y[c + 2], y[c + 3]);
+                        fadd2(a[half][0], a[half][1], y[c], y[c + 1]);
+                        fadd2(a[half][2], a[half][3], y[c + 2], y[c + 3]);
                     }
                 }
             }
             i += u.n;
             if (!ok) break;
-            float sum = (a0 + a1) + (a2 + a3);
+            float sum[kHalves];
+#pragma unroll
+            for (int y = 0; y < kHalves; ++y) sum[y] = (a[y][0] + a[y][1]) + (a[y][2] + a[y][3]);
             if (u.n > 1) {
                 // the other teams hand their sums to the first
                 const int slot = joined % 2;
@@ -649,26 +669,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(kBarSumEmpty + slot, ((joined / 2) & 1) ^ 1);
                 if (!ok) break;
                 if (me != 0) {
-                    sum_of[(me - 1) * kBK] = sum;
+#pragma unroll
+                    for (int y = 0; y < kHalves; ++y) sum_of[(me - 1) * kBK + 128 * y] = sum[y];
                     mbar_arrive(bar(kBarSumFull + slot));
                 } else {
                     ok = wait(kBarSumFull + slot, (joined / 2) & 1);
                     if (!ok) break;
 #pragma unroll
-                    for (int o = 0; o < kTeams - 1; ++o) sum += sum_of[o * kBK];
+                    for (int o = 0; o < kTeams - 1; ++o)
+#pragma unroll
+                        for (int y = 0; y < kHalves; ++y) sum[y] += sum_of[o * kBK + 128 * y];
                     mbar_arrive(bar(kBarSumEmpty + slot));
                 }
                 ++joined;
                 if (me != 0) continue;
             }
-            if (there && page >= 0 && page < p.num_pages) {
-                float *w = p.weights + ((static_cast<size_t>(page) * p.H_kv + u.h) << p.page_log2) +
-                           (key & ((1 << p.page_log2) - 1));
-                if (key >= u.q_off)
-                    *w = sum;
-                else
-                    atomicAdd(w, sum);
-            }
+#pragma unroll
+            for (int y = 0; y < kHalves; ++y)
+                if (key[y] < u.nk && page[y] >= 0 && page[y] < p.num_pages) {
+                    float *w = p.weights + ((static_cast<size_t>(page[y]) * p.H_kv + u.h) << p.page_log2) +
+                               (key[y] & ((1 << p.page_log2) - 1));
+                    if (key[y] >= u.q_off)
+                        *w = sum[y];
+                    else
+                        atomicAdd(w, sum[y]);
+                }
         }
         if (!ok && lane == 0) record_timeout(p, abort_flag, kRoleSum, k);
     }
