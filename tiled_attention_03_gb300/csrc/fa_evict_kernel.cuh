@@ -16,7 +16,7 @@
 // they lie behind everything that this round writes. One block barrier a round orders all of that. (With
 // whole rows per CTA and slots shared among the cluster a round was small and took a cluster barrier
 // and 1.5 to 2 us: 16 sequences of 5000 to 20000 keys cut to 8192 took 295 us; rounds of
-// consecutive slots instead of rows, fewer bytes in flight where few are kept, 174.)
+// consecutive slots instead of rows, fewer bytes in flight where few are kept, 174; this 127, 4.8 TB/s.)
 //
 // Bound by memory: rows and weights are read and written once.
 #pragma once

@@ -30,13 +30,16 @@
 // CTAs that take the same tiles for R rows each, side by side, so that with more rows than R the
 // second reads them from L2.
 //
-// What bounds it: at 64 rows a tile of 64 keys at DL = 512 is 74 KB, which this SM's share
-// of HBM delivers in about 3,100 cycles.
+// What bounds it: a tile of 64 keys at DL = 512 is 74 KB, which this SM's share of HBM delivers in
+// about 3,100 cycles: with one block per sequence, memory (8 sequences of 32768 rows, 32 heads: 61
+// us, 5.0 TB/s, of which 10 are the start, the last output and the merge). With more blocks the
+// products, 36 of M = 64 and 16 of M = 128 at 33 and 49 cycles at least, 1,970 of a tile's 2,300
+// cycles (1000 tokens of 16 heads on 14000 rows: 456 us, 1,110 TFLOP/s; 447 without any key loads).
 //
 // Warps (256 threads): 0-3 softmax and outputs, 4 key tiles, 5 issuer of S^T, 6 issuer of
 // O^T, 7 scheduler and Q tiles. What the issuers' branches and descriptors come from is taken
 // from one lane by a shuffle, so that the compiler knows it to be the warp's and the products
-// are issued from uniform registers (1000 x 16 rows on 14000 keys: 480 us, 583 without).
+// are issued from uniform registers (1000 x 16 rows on 14000 keys: 480 us at that point, 583 without).
 // Every wait is bounded; on expiry the CTA records the failure, drains
 // its copies and products, frees its tensor memory and returns. Waits of the softmax warps
 // end in a vote before the next barrier, so that all four leave together.
@@ -263,25 +266,6 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) 
         : "r"(taddr)
         : "memory");
 }
-// 16 or 32 columns of this warp's lanes; and the wait for them.
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-__device__ __forceinline__ void ld_cols_wait(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-__device__ __forceinline__ void ld_cols_wait(uint32_t (&r)[32]) { tmem_ld_wait(r); }
-
 // 32 lanes x 16 consecutive columns, and the wait for them.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -965,23 +949,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t row0 = P.slot < 0 ? static_cast<size_t>(P.row0) : static_cast<size_t>(P.slot) * R;
             const size_t at0 = row0 * DL + warp * 32 + lane;
             constexpr int kParts = L::kParts;
-            // 32 rows (or R) of a slice of O^T at a time; the next ones come while these are stored
+            // 32 rows (or R) of a slice of O^T at a time (with the next ones asked for ahead the code is
+            // twice as long: 54 -> 58 us at 128 heads)
             constexpr int kAtOnce = R < 32 ? R : 32, kSteps = R / kAtOnce * kParts;
-            uint32_t o[2][kAtOnce];
-            auto fetch = [&](int x, uint32_t(&to)[kAtOnce]) {
-                if (x < kSteps) ld_cols(tl + L::kTmemO + x * kAtOnce, to);
-            };
-            auto store = [&](int x, uint32_t(&from)[kAtOnce]) {
+#pragma unroll 1
+            for (int x = 0; x < kSteps; ++x) {
                 const int part = x * kAtOnce / R, r0 = x * kAtOnce % R, left = P.rows - r0;
+                if (left <= 0) continue;
+                uint32_t o[kAtOnce];
+                if constexpr (kAtOnce == 32) {
+                    tmem_ld32(tl + L::kTmemO + x * kAtOnce, o);
+                    tmem_ld_wait(o);
+                } else {
+                    tmem_ld16(tl + L::kTmemO + x * kAtOnce, o);
+                }
                 float y[kAtOnce];
                 // a row without keys: 0, whatever its column holds
 #pragma unroll
                 for (int e = 0; e < kAtOnce; e += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(factor + r0 + e);
-                    y[e] = f.x == 0.f ? 0.f : __uint_as_float(from[e]) * f.x;
-                    y[e + 1] = f.y == 0.f ? 0.f : __uint_as_float(from[e + 1]) * f.y;
-                    y[e + 2] = f.z == 0.f ? 0.f : __uint_as_float(from[e + 2]) * f.z;
-                    y[e + 3] = f.w == 0.f ? 0.f : __uint_as_float(from[e + 3]) * f.w;
+                    y[e] = f.x == 0.f ? 0.f : __uint_as_float(o[e]) * f.x;
+                    y[e + 1] = f.y == 0.f ? 0.f : __uint_as_float(o[e + 1]) * f.y;
+                    y[e + 2] = f.z == 0.f ? 0.f : __uint_as_float(o[e + 2]) * f.z;
+                    y[e + 3] = f.w == 0.f ? 0.f : __uint_as_float(o[e + 3]) * f.w;
                 }
                 const size_t at = at0 + static_cast<size_t>(r0) * DL + part * 128;
                 if (P.slot < 0) {
@@ -998,12 +988,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < kAtOnce; ++e)
                         if (e < left) to[e * DL] = y[e];
                 }
-            };
-#pragma unroll 1
-            for (int x = 0; x < kSteps; ++x) {
-                fetch(x, o[0]);
-                ld_cols_wait(o[0]);
-                store(x, o[0]);
             }
             tc_fence_before();
             mbar_arrive(bar(kBarOFree));

@@ -11,16 +11,18 @@
 // The scores are taken transposed, S^T = K Q^T (128 keys x R rows): keys stand in the lanes of
 // tensor memory, so that the sum over rows is a sum over one thread's registers, and a tile of
 // keys, the M operand, is read once for all rows of its sequence and K/V head. A unit is one tile
-// of 128 keys of one K/V head with all tiles of R rows that see it; CTA c takes every gridDim-th
+// of 128 or 256 keys of one K/V head with all tiles of R rows that see it; CTA c takes every gridDim-th
 // unit from c on (every other time from the end of the run: units of one sequence grow lighter along
 // the keys under a causal mask). That shares them evenly, needs no counters, and gives every
 // key to one thread: one addition per key and call, so the result is the same every time (keys
 // of pages that several sequences share get one addition each, in any order).
 //
-// What bounds it: single steps read K once, by HBM (8 sequences of 32768 keys of 8 heads of 128: 89
-// us, 6.2 TB/s). Chunks: a tile of 128 x 128 scores takes about 1,150 cycles, of which the products
-// take 528 and the exponentials as long; computing some of those by multiply-adds made it slower
-// (10 of 32: 115 -> 130 us), as the sums wait for tensor memory and for each other more than for a pipe.
+// What bounds it: single steps read K once, by HBM (8 sequences of 32768 keys of 8 heads of 128: 88
+// us, 6.1 TB/s); short or narrow ones by the 1,400 cycles that a unit costs its issuer, in waits and in
+// instructions that are fetched anew (waiting for several barriers at once, and finding units for all warps 32
+// at a time, changed nothing). Chunks: a tile of 128 x 128 scores takes about 1,150 cycles, of which
+// the products take 528 and the exponentials as long; computing some of those by multiply-adds made it
+// slower (10 of 32: 115 -> 130 us), as the sums wait for tensor memory and for each other more than for a pipe.
 //
 // Warps (640 threads): 0-15 are four teams of four that sum every fourth tile of rows (of units with
 // one: every fourth unit), as one team's loads from tensor memory and exponentials wait for each
@@ -43,7 +45,9 @@ namespace fa {
 namespace weights {
 
 // Keys of a tile: 128, or 256 (two products, one behind the other) for narrow tiles of rows, where what
-// a unit costs besides its products is most of it.
+// a unit costs besides its products is most of it (8 sequences of 32768 keys 87.7 us, with 128 89.3;
+// 100 of 0-12000 at d = 64 20.7 and 25.4; with tiles of 64 rows 128 are better, 16 sequences of
+// 6000-9000 keys and 40 rows 28 and 32).
 constexpr int tile_keys(int d, int rows) { return rows == 16 && d <= 128 ? 256 : 128; }
 constexpr int kTeams = 4;
 constexpr int kThreads = (4 * kTeams + 4) * 32;
