@@ -19,8 +19,8 @@
 //
 // What bounds it: single steps read K once, by HBM (8 sequences of 32768 keys of 8 heads of 128: 88
 // us, 6.1 TB/s); short or narrow ones by the 1,400 cycles that a unit costs its issuer, in waits and in
-// instructions that are fetched anew (waiting for several barriers at once, and finding units for all warps 32
-// at a time, changed nothing). Chunks: a tile of 128 x 128 scores takes about 1,150 cycles, of which
+// instructions that are fetched anew (lanes that wait for a barrier each, and units handed out 32 at a
+// time, made both slower, by 2 and 8 %). Chunks: a tile of 128 x 128 scores takes about 1,150 cycles, of which
 // the products take 528 and the exponentials as long; computing some of those by multiply-adds made it
 // slower (10 of 32: 115 -> 130 us), as the sums wait for tensor memory and for each other more than for a pipe.
 //
