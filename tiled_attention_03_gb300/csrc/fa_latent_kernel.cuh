@@ -112,7 +112,7 @@ struct Smem {
     static constexpr int kQRegion = R * 128;
     static constexpr int kQBytes = kRegions * kQRegion;
     static constexpr int kPBytes = R * 128;
-    static constexpr int kSmall = 3072;
+    static constexpr int kSmall = 3 * 1024;
     static constexpr int kMost = 227 * 1024 - kSmall;
     // two Q tiles (the next block's scores start while this one ends) and two of the weights
     // where two key tiles leave room for them; the rest is for key tiles

@@ -72,7 +72,7 @@ struct Params {
     const int *cu_q, *seq_k, *table;
     int B, H, H_kv, pf, subs, tpt;  // heads and tokens of a tile of rows; tiles of heads per group
     int total_q, max_pages, page_log2, num_pages, max_keys;
-    int chunk;         // tokens per TMA box: min(page size, kBK)
+    int chunk;         // tokens per TMA box: min(page size, keys of a tile)
     int page_step, head_step, page_none;  // the map's last coordinate; past its end
     Divisor by_heads, by_tpt, by_subs;  // by H_kv, tpt and subs
     int wl, wr;        // key j visible to the query at position i iff i - wl <= j <= i + wr
