@@ -278,6 +278,25 @@ def test_weights_are_the_same_every_time_and_captured():
         assert torch.equal(x, outs[0])
 
 
+def test_weights_on_two_streams_at_once():
+    bs = [paged(lens, 8, 2, 128, torch.bfloat16, 64, seed=9 + i)
+          for i, lens in enumerate([[(1, 9000)] * 6, [(700, 3000), (1, 50)]])]
+    lses = [lse_of(b[5], 2, 0.1, "causal", (0, 0), b[0].shape[0]) for b in bs]
+    blank = [torch.zeros(b[1].num_pages, 2, 64, device=DEV) for b in bs]
+    want = [w.clone() for w in blank]
+    for b, lse, w in zip(bs, lses, want):
+        gather(b[0], lse, w, *b[1:5], 0.1, "causal")
+    streams = [torch.cuda.Stream() for _ in bs]
+    got = [[w.clone() for w in blank] for _ in range(20)]
+    torch.cuda.synchronize()
+    for one in got:
+        for b, lse, w, s in zip(bs, lses, one, streams):
+            fa.fa_paged_weights(b[0], lse, w, *b[1:5], 0.1, stream=s)
+    torch.cuda.synchronize()
+    assert fa.fa_sync_status() == fa.FA_OK
+    assert all(torch.equal(g, w) for one in got for g, w in zip(one, want))
+
+
 def test_the_fault_hook_ends_in_a_timeout():
     b = paged([(40, 600)], 2, 1, 128, torch.bfloat16, 16, seed=3)
     want = check_gather(b, 0.1, "causal")
