@@ -26,7 +26,8 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kSteps = 4;           // rows of queries per lane and item
 constexpr int kHeads = 4 * kSteps;  // heads per item
-// blocks an SM holds at once, by their registers (80 and 110)
+// blocks an SM holds at once, by their registers (80 and 110): 24 prompts of 1-2000 tokens 15.4 us at
+// DL = 256, with four 20.4; 22.0 at DL = 512, with three 26.4
 constexpr int blocks_per_sm(int64_t dl) { return dl == 512 ? 2 : 3; }
 
 struct AppendParams {
