@@ -537,8 +537,9 @@ fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_row
  * of the heads as the model defines them. Positions, masks, tokens without keys or sequences,
  * what is not looked at, and NaN in rows that are: as for fa_forward_paged.
  *
- * Scores, softmax statistics and sums are float32; the weights exp(score - reference) are
- * rounded to the cache's dtype for their product with the rows.
+ * Scores, softmax statistics and sums are float32. The weights exp(score - reference) are rounded
+ * to the cache's dtype for their product with the rows; where a batch has at most 32 rows (tokens x
+ * heads) per sequence on average, they keep twice as many bits.
  *
  * workspace: caller-owned device memory of at least
  * fa_forward_latent_workspace_bytes(d_latent) bytes, 32-byte aligned, scratch: its contents on

@@ -149,6 +149,46 @@ def test_peaky_scores(H, dl):
     check(o, lse, seqs, 0.3, "causal", (0, 0), torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dl", [128, 256, 512])
+@pytest.mark.parametrize("H", [4, 12, 20, 25])
+def test_steps_round_their_outputs_alone(H, dl, dtype):
+    """Batches of up to 32 rows a sequence: the weights of the keys go into their product with the
+    rows in two 16-bit parts. What the second leaves is half a step of half a step of each (or 2^-25
+    where fp16 goes below its normal range).
+
+    The scores are exact: queries are 0 on the latent columns, and what both hold on the rotary
+    ones are multiples of 1/4 up to 4, so that sums of 64 products, multiples of 1/16 below
+    1024, are floats. Exponents (base 2) below 32 then have two roundings of 2^-24 of themselves, so
+    a weight is off by 2^-18 of itself, and 2^-21 for the exponential; so is the sum that divides it.
+    The products add 16 keys at a time, each with a step of 2^-23 of the sum at most."""
+    scale = 0.0625
+    q, cache, table, cu, lens, seqs = paged([(1, 700), (2, 300), (1, 90), (1, 1)], H, dl, dtype, 16, seed=dl + H)
+    quarter = lambda x: (x.float().clamp(-4, 4) * 4).round() / 4  # noqa: E731
+    t, half = 0, torch.finfo(dtype).eps / 2
+    for b, (qq, rows) in enumerate(seqs):
+        qq[..., :dl], qq[..., dl:] = 0, quarter(qq[..., dl:])
+        rows[:, dl:] = quarter(rows[:, dl:])
+        q[t:t + qq.shape[0]] = qq
+        j = torch.arange(rows.shape[0], device=DEV)
+        cache.data[table[b, j // 16].long(), j % 16] = rows
+        t += qq.shape[0]
+    o, _ = run(q, cache, table, cu, lens, scale)
+    t = 0
+    for b, (qq, rows) in enumerate(seqs):
+        n, L = qq.shape[0], rows.shape[0]
+        x = torch.einsum("ihd,jd->ihj", qq.double(), rows.double()) * scale
+        assert float(x.abs().max()) * math.log2(math.e) < 16  # and less twice that from the reference
+        x.masked_fill_(~(torch.arange(L, device=DEV) <= torch.arange(L - n, L, device=DEV)[:, None])[:, None], -math.inf)
+        p, v = x.softmax(-1), rows[:, :dl].double()
+        want, size = p @ v, p @ v.abs()
+        bound = half * want.abs() * (1 + 2.0 ** -7) + (half ** 2 + 2 * (2.0 ** -18 + 2.0 ** -21) + (L / 16 + 1) * 2.0 ** -23) * size
+        if dtype == torch.float16:
+            bound += 2.0 ** -25 * (1 + v.abs().sum(0))
+        assert_within(o[t:t + n], want, bound, f"sequence {b}: O")
+        t += n
+
+
 @pytest.mark.parametrize("mask,window", [("window", (100, 0)), ("causal", (0, 0))])
 def test_what_is_not_seen_is_not_looked_at(mask, window):
     """Rows before every window, and all behind a sequence's end, hold NaN."""

@@ -20,7 +20,8 @@
 // S^T arrives with keys in lanes, 16 lanes of each warp's 32 (the layout of M = 64), and is
 // read as 16 x 256 bit fragments: a thread holds 2 keys of each of R / 4 rows. The weights
 // p = exp2(s scale log2 e - ref) go to shared memory through transposing 8 x 8 stores, as the
-// K-major B operand of the second product. The reference of a row is lazy: it moves only
+// K-major B operand of the second product; blocks of up to 32 rows hand them over as two 16-bit parts,
+// each multiplied by itself into the same O^T. The reference of a row is lazy: it moves only
 // when a score passes it by 2^8, so a tile costs the four warps one barrier with a vote and
 // no row maximum; when it does move, the row's l and its column of O^T are rescaled.
 //
@@ -111,12 +112,22 @@ struct Smem {
     static constexpr int kTile = kParts * kPart + kBK / 8 * kAtom;
     static constexpr int kQRegion = R * 128;
     static constexpr int kQBytes = kRegions * kQRegion;
-    static constexpr int kPBytes = R * 128;
+    // 16-bit parts of a weight in its product with the values, and the bytes of one part and of a buffer
+    // of all. One alone puts O's error at 0.0021 where its own rounding is 0.0017 (bf16, relative,
+    // root mean square). With up to 32 rows, where tiles wait for memory, the second part costs little (8
+    // sequences of 32768 rows 61 -> 63 us, 96 ragged ones 24.2 -> 24.9). With 64 the products are the bound (at DL
+    // = 256 1000 tokens of 16 heads on 14000 rows 336 -> 400 us, 40 sequences with 128 heads 39.6 ->
+    // 44.0), and at DL = 512 shared memory has no place for it: there weights are rounded, as in the
+    // forward passes over whole sequences.
+    static constexpr int kPParts = R <= 32 ? 2 : 1;
+    static constexpr int kPPart = R * 128;
+    static constexpr int kPBytes = kPParts * kPPart;
     static constexpr int kSmall = 3 * 1024;
     static constexpr int kMost = 227 * 1024 - kSmall;
-    // two Q tiles (the next block's scores start while this one ends) and two of the weights
-    // where two key tiles leave room for them; the rest is for key tiles
-    static constexpr int kQStages = 2 * kQBytes + 2 * kTile + kPBytes <= kMost ? 2 : 1;
+    // two Q tiles (the next block's scores start while this one ends) and two buffers of weights
+    // where two key tiles leave room for them, else two of weights where they do (16 sequences of 0-16000
+    // rows, 20 heads, DL 512: 24.0 us, with two Q tiles in their place 25.4); the rest is for key tiles
+    static constexpr int kQStages = 2 * kQBytes + 2 * kTile + 2 * kPBytes <= kMost ? 2 : 1;
     static constexpr int kPBufs = kQStages * kQBytes + 2 * kTile + 2 * kPBytes <= kMost ? 2 : 1;
     static constexpr int kFit = (kMost - kQStages * kQBytes - kPBufs * kPBytes) / kTile;
     // an even number, so that a slot of the ring has one buffer of scores and of weights
@@ -729,9 +740,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < kBK / 16; ++c)
                                 if (c >= c0 && c <= c1)
-                                    umma_f16_ss(kTmem + L::kTmemO + s * R,
-                                                da + s * (L::kPart >> 4) + c * ((2 * L::kGroup) >> 4), db + c * 2,
-                                                idesc_o, x > 0 || c > c0 ? 1u : 0u);
+#pragma unroll
+                                    for (int y = 0; y < L::kPParts; ++y)
+                                        umma_f16_ss(kTmem + L::kTmemO + s * R,
+                                                    da + s * (L::kPart >> 4) + c * ((2 * L::kGroup) >> 4),
+                                                    db + y * (L::kPPart >> 4) + c * 2, idesc_o,
+                                                    x > 0 || c > c0 || y > 0 ? 1u : 0u);
                             umma_commit(bar(kBarKEmpty + st + s));
                         }
                         umma_commit(bar(kBarPVDone + t % 2));
@@ -895,7 +909,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     load();
                 }
-                // ---- weights: l keeps the fp32 values, the product takes 16 bits
+                // ---- weights: l keeps the fp32 values, the product takes 16 bits, or the sum of two parts of
+                // 16 bits (see kPParts)
 #pragma unroll
                 for (int c = 0; c < R / 2; ++c) x[c] = ex2_approx(x[c]);
 #pragma unroll
@@ -911,9 +926,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < R / 8; b += 2) {
                     const int c = 4 * b;
                     const int r = 8 * (b + (lane >> 4)) + (lane & 7), octet = 2 * warp + ((lane >> 3) & 1);
-                    store_transposed(base + r * 128 + ((octet ^ (r & 7)) << 4), pack2<BF16>(x[c], x[c + 1]),
-                                     pack2<BF16>(x[c + 2], x[c + 3]), pack2<BF16>(x[c + 4], x[c + 5]),
-                                     pack2<BF16>(x[c + 6], x[c + 7]));
+                    const uint32_t at = base + r * 128 + ((octet ^ (r & 7)) << 4);
+                    if constexpr (L::kPParts == 2) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) two_parts<BF16>(x[c + 2 * e], x[c + 2 * e + 1], hi[e], lo[e]);
+                        store_transposed(at, hi[0], hi[1], hi[2], hi[3]);
+                        store_transposed(at + L::kPPart, lo[0], lo[1], lo[2], lo[3]);
+                    } else {
+                        store_transposed(at, pack2<BF16>(x[c], x[c + 1]), pack2<BF16>(x[c + 2], x[c + 3]),
+                                         pack2<BF16>(x[c + 4], x[c + 5]), pack2<BF16>(x[c + 6], x[c + 7]));
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();

@@ -371,4 +371,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
+// a and b (in the lower and upper 16 bits) as hi + lo: hi their rounding, lo the rounding of what
+// that leaves.
+template <bool BF16>
+__device__ __forceinline__ void two_parts(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack2<BF16>(a, b);
+    float ha, hb;
+    if constexpr (BF16) {
+        ha = __uint_as_float(hi << 16);
+        hb = __uint_as_float(hi & 0xffff0000u);
+    } else {
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+            : "=f"(ha), "=f"(hb)
+            : "r"(hi));
+    }
+    lo = pack2<BF16>(a - ha, b - hb);
+}
+
 }  // namespace fa
