@@ -168,6 +168,27 @@ def test_rows_without_keys_add_nothing():
     check_gather(b, 0.125, "causal", lse=lse)
 
 
+@pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("lens,H,Hk", [([(1, 300), (2, 140), (1, 40)], 8, 2), ([(20, 300), (20, 200)], 4, 2),
+                                       ([(70, 300), (40, 60)], 4, 2), ([(300, 900)], 8, 2)])
+def test_rows_of_lse_minus_infinity_add_nothing_whatever_they_hold(lens, H, Hk, d, bad):
+    """Queries of NaN and infinities whose LSE is -infinity, in tiles that every row sees and in others."""
+    b = paged(lens, H, Hk, d, torch.bfloat16, 16, seed=6)
+    q, seqs = b[0], b[5]
+    lse = lse_of(seqs, Hk, 0.1, "causal", (0, 0), q.shape[0])
+    g = torch.Generator(device=DEV).manual_seed(3)
+    hit = torch.rand(lse.shape, generator=g, device=DEV) < 0.2
+    hit[0, 0] = True
+    lse[hit] = -math.inf
+    q[hit] = bad
+    t = 0
+    for qq, _, _ in seqs:
+        qq.copy_(q[t:t + qq.shape[0]])
+        t += qq.shape[0]
+    check_gather(b, 0.1, "causal", lse=lse)
+
+
 def test_nan_of_another_sequence_and_of_a_key_stay_there():
     q, cache, table, cu, lens, seqs = paged([(1, 90), (1, 100), (3, 70)], 4, 2, 64, torch.bfloat16, 16, seed=2)
     scale = 0.125

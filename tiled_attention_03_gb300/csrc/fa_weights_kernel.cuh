@@ -106,7 +106,9 @@ struct Smem {
     static constexpr int kRing = kMisc + 16;                 // kUnitSlots units
     static constexpr int kLse = kRing + kUnitSlots * 64;     // kLses x R, times -log2 e
     static constexpr int kSums = kLse + kLses * R * 4;       // two units' sums of three teams
-    static constexpr int kBytes = kSums + 2 * (kTeams - 1) * kBK * 4;
+    static constexpr int kBlind = kSums + 2 * (kTeams - 1) * kBK * 4;  // a bit per row of an LSE slot
+    static constexpr int kBlindWords = (R + 31) / 32;
+    static constexpr int kBytes = kBlind + kLses * kBlindWords * 4;
     static_assert(kBufs * kHalves * R <= kTmemCols, "TMEM columns");
     static_assert(kLse % 16 == 0 && kBytes - kBar <= kSmall, "layout");
     static constexpr int kAlloc = kBytes > 120 * 1024 ? kBytes : 120 * 1024;  // one CTA per SM
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto sK = [sbase](int t) { return sbase + L::kK + (t % L::kKStages) * L::kTile; };
     auto sQ = [sbase](int t) { return sbase + L::kQ + (t % L::kQStages) * L::kQBytes; };
     float *const lse_ring = reinterpret_cast<float *>(smem + L::kLse);
+    uint32_t *const blind_ring = reinterpret_cast<uint32_t *>(smem + L::kBlind);  // 1: the row's LSE is -infinity
     // (from one lane: the compiler then knows that the roles' branches are the warp's)
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
@@ -483,17 +486,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++i;
         };
-        // row c: token c / pf, head c mod pf. Minus the LSE, so that tokens that saw nothing get
-        // -infinity, which makes every weight 0
+        // row c: token c / pf, head c mod pf. Minus the LSE; rows that saw nothing are marked, as no
+        // number added to any score, NaN and infinity among them, would make their weights 0
         auto store = [&](const Tile &n) {
             const int slot = (i - 1) % kLses;
             ok = ok && wait(kBarLEmpty + slot, (((i - 1) / kLses) & 1) ^ 1);
             if (!ok) return;
 #pragma unroll
-            for (int y = 0; y < kOwn; ++y)
-                if (lane + 32 * y < R)
-                    lse_ring[slot * R + lane + 32 * y] =
-                        n.v[y] == -INFINITY ? -INFINITY : n.v[y] * -1.4426950408889634f;
+            for (int y = 0; y < kOwn; ++y) {
+                const uint32_t none = __ballot_sync(0xffffffffu, n.v[y] == -INFINITY);
+                if (lane == 0) blind_ring[slot * L::kBlindWords + y] = none;
+                if (lane + 32 * y < R) lse_ring[slot * R + lane + 32 * y] = n.v[y] * -1.4426950408889634f;
+            }
             mbar_arrive(bar(kBarLFull + slot));
         };
         if constexpr (R >= 64) {
@@ -621,6 +625,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // behind the sequence's last token may hold anything: they are not looked at)
                 const bool whole = t0 >= all_lo && t0 + p.tpt - 1 <= all_hi && p.tpt * p.pf == R;
                 const float *lse = lse_ring + at % kLses * R;
+                // (a bit per row: comparing the LSEs themselves cost registers, 116 -> 139 us for 2048 tokens on
+                // 6000 keys, the bits 118)
+                uint32_t blinds[L::kBlindWords], any_blind = 0;
+#pragma unroll
+                for (int w = 0; w < L::kBlindWords; ++w) any_blind |= blinds[w] = blind_ring[at % kLses * L::kBlindWords + w];
                 constexpr int kCols = R < 32 ? R : 32, kLoads = kHalves * R / kCols;
                 uint32_t r[2][kCols];  // the next columns come while these are summed
                 ld_cols(tl + buf * kHalves * R, r[0]);
@@ -645,11 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kBarLEmpty + at % kLses));
                     }
-                    if (!whole) {
+                    if (!whole || any_blind != 0) {
                         const int c_lo = (lo[half] - t0) * p.pf, c_hi = min(hi[half] - t0 + 1, p.tpt) * p.pf;
+                        // ones from bit n on, for n of 0 to 32
+                        auto from = [](int n) { return __funnelshift_lc(0u, ~0u, min(max(n, 0), 32)); };
+                        const uint32_t sees = from(c_lo - h) & ~from(c_hi - h) & ~blinds[h / 32];
 #pragma unroll
                         for (int c = 0; c < kCols; ++c)
-                            if (h + c < c_lo || h + c >= c_hi) y[c] = -INFINITY;
+                            if ((sees >> c & 1) == 0) y[c] = -INFINITY;
                     }
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) y[c] = ex2_approx(y[c]);
