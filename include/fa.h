@@ -570,9 +570,10 @@ size_t fa_forward_latent_workspace_bytes(int64_t d_latent);
  * token sees, and of slots past a sequence's end, are left as they are. A page that several
  * sequences of the batch share gets each one's a_j, added in any order; otherwise the
  * results are the same every time. weights overlaps no other buffer. total_q * H, and H_kv
- * times the tiles of 128 keys that max_pages pages hold, are at most 2^30. A token that offsets in
- * no order give to several sequences counts for the first. One kernel launch, no workspace.
- * Everything else as fa_forward_paged.
+ * times the tiles of 128 keys that max_pages pages hold, are at most 2^30. Where offsets are in no
+ * order, the tokens of a sequence that lie before the furthest end of the sequences before it (of
+ * those that have tokens) add nothing. One kernel launch, no workspace. Everything else as
+ * fa_forward_paged.
  */
 fa_status fa_paged_weights(const void *Q, const float *LSE, float *weights, const fa_paged_cache *cache,
                            const int32_t *block_table, int64_t max_pages, const int32_t *cu_seqlens_q,

@@ -234,6 +234,52 @@ def test_offsets_in_no_order_give_a_token_to_the_first_sequence(B, T):
     gather(q, lse, got, cache, table, i32([-5, 0] + [T + 9, -1] * B)[:B + 1].contiguous(), lens, 0.125, "causal")
 
 
+@pytest.mark.parametrize("H,Hk,d", [(4, 2, 64), (64, 2, 64), (8, 1, 256)])
+@pytest.mark.parametrize("cu,lens", [
+    ([0, 5, 3, 8], [90, 40, 70]),               # the last sequence keeps its tokens 5 to 7
+    ([5, 0, 8], [30, 90]),                      # an empty first one, far along
+    ([8, 8, 0, 4, 8], [30, 30, 20, 90]),
+    ([5, 8, 0, 6], [90, 30, 70]),               # behind the first one's end: nothing left
+    ([0, 6, 2, 9, 4, 12], [50, 9, 300, 11, 77]),
+    ([-5, 3, -1, 7, 2, 40], [4, 60, 200, 8, 90]),  # clamped to the tokens
+    ([-5, 0, 21, -1, 21], [30, 90, 40, 60]),
+    ([0, 12, 0, 12, 0, 12], [200, 1, 300, 2, 10]),
+])
+def test_offsets_in_no_order_against_the_definition(cu, lens, H, Hk, d):
+    """Each sequence's tokens before the furthest end so far are left out; the others, its last
+    ones, stand where they stood. Nothing outside the array is written."""
+    T, page, scale, guard = 12, 16, 0.1, 3
+    q, cache, table, _, seq_k, seqs = paged([(0, n) for n in lens], H, Hk, d, torch.bfloat16, page, seed=len(cu))
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q = torch.randn(T, H, d, generator=g, device=DEV).to(torch.bfloat16)
+    lse = torch.rand(T, H, generator=g, device=DEV) + 1  # any will do
+    whole = torch.full((cache.num_pages + 2 * guard, Hk, page), -777.0, device=DEV)
+    weights = whole[guard:-guard]
+    weights.copy_(torch.rand(weights.shape, generator=g, device=DEV))
+    before, rest = weights.clone(), torch.ones(weights.shape, dtype=torch.bool, device=DEV)
+    gather(q, lse, weights, cache, table, i32(cu), seq_k, scale, "causal")
+    end = 0
+    for b, (_, k, _) in enumerate(seqs):
+        first = min(max(cu[b], 0), T)
+        stop = min(max(cu[b + 1], first), T)
+        skip = min(max(end - first, 0), stop - first)
+        if stop > first:
+            end = max(end, stop)
+        n, L = stop - first - skip, lens[b]
+        if n == 0:
+            continue
+        j = torch.arange(L, device=DEV)
+        pg, sl = table[b, j // page].long(), j % page
+        old = before[pg, :, sl].double()
+        old[max(0, L - (stop - first)):] = 0  # the call's own keys, those of tokens left out among them
+        # gather_ref clears the keys of the tokens it is given, which are the last of these
+        want, bound = gather_ref(q[first + skip:stop], k, lse[first + skip:stop], old, scale, "causal", (0, 0))
+        assert_within(weights[pg, :, sl], want, bound, f"sequence {b}")
+        rest[pg, :, sl] = False
+    assert torch.equal(weights[rest], before[rest]), "wrote another slot"
+    assert bool((whole[:guard] == -777.0).all()) and bool((whole[-guard:] == -777.0).all())
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_a_shared_page_gets_every_sequences_share(new):
     """Two sequences over the same pages but for their own tokens': both add to the shared ones."""

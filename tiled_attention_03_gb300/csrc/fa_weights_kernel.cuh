@@ -138,6 +138,7 @@ struct Unit {
     int b, h, j;
     int first, n;
     int q0, nq, nk, q_off;  // token i of the sequence stands at key position i + q_off
+    int fresh;              // keys from here on are the call's own
 };
 static_assert(sizeof(Unit) <= 64, "ring slot");
 
@@ -300,14 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto unit_of = [&](long long i) {
             return i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         };
-        // A token belongs to the first sequence that claims it, so that offsets in no order make no
-        // more work than ordered ones.
+        // A sequence's tokens begin where those of the sequences before it end, at the earliest, so that
+        // offsets in no order make no more work than ordered ones. What is left of them are its
+        // last ones: they keep their positions.
         long long base = 0, next = lane;
         bool ok = true;
         int k = 0, claimed = 0;
         for (int b0 = 0; ok && b0 < p.B; b0 += 32) {
             Seq s = load_seq(b0 + lane, p);
-            int ends = s.q0 + s.nq;  // the most of the sequences' ends up to this one
+            int ends = s.nq > 0 ? s.q0 + s.nq : 0;  // the most of the sequences' ends up to this one
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, ends, o);
@@ -315,7 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             int before_me = __shfl_up_sync(0xffffffffu, ends, 1);
             before_me = max(lane > 0 ? before_me : 0, claimed);
-            if (s.q0 < before_me) s.nq = 0;
+            const int fresh = s.nk - s.nq, lost = min(max(before_me - s.q0, 0), s.nq);
+            s.q0 += lost;
+            s.nq -= lost;
             claimed = max(claimed, __shfl_sync(0xffffffffu, ends, 31));
             const int tiles = key_tiles<kBK>(s, p);
             long long incl = static_cast<long long>(tiles) * p.H_kv;
@@ -343,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int y = p.by_heads.of(max(x, 0));
                 u.h = x - y * p.H_kv;
                 u.q_off = u.nk - u.nq;
+                u.fresh = __shfl_sync(0xffffffffu, fresh, at);
                 u.j = y + first_tile<kBK>(Seq{0, u.nq, u.nk}, p);
                 int lo, hi;
                 tokens_of(u, u.j * kBK, min(u.j * kBK + kBK, u.nk) - 1, p, lo, hi);
@@ -705,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (key[y] < u.nk && page[y] >= 0 && page[y] < p.num_pages) {
                     float *w = p.weights + ((static_cast<size_t>(page[y]) * p.H_kv + u.h) << p.page_log2) +
                                (key[y] & ((1 << p.page_log2) - 1));
-                    if (key[y] >= u.q_off)
+                    if (key[y] >= u.fresh)
                         *w = sum[y];
                     else
                         atomicAdd(w, sum[y]);
