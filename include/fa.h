@@ -514,7 +514,8 @@ typedef struct {
  * strides are used: the two halves of one projection are fine); q_rope, q_out:
  * total_q x H x d_rope by `head` and `token`, or both with data = NULL (H is then
  * ignored): slices of wider buffers are fine, such as the last d_rope columns of the
- * absorbed queries that fa_forward_latent takes. q_out may be q_rope. rope->rotary_dim is
+ * absorbed queries that fa_forward_latent takes. q_out may be q_rope, and one buffer may
+ * hold a token's query heads, c and k_rope beside each other (equal token strides). rope->rotary_dim is
  * at most d_rope, rope->q_weight must be NULL. rope = NULL: rows are stored, and rotary parts of
  * queries copied, as they are. One kernel launch. Errors as fa_forward.
  */

@@ -129,6 +129,28 @@ def test_append_refusals(lib, kw):  # noqa: F811
     assert append(lib, **kw) == INVALID
 
 
+@pytest.mark.parametrize("first", ["queries", "latent"])
+@pytest.mark.parametrize("d_latent,H", [(512, 4), (128, 1), (256, 16)])
+def test_one_projection_of_queries_latent_and_rotary_part(lib, d_latent, H, first):  # noqa: F811
+    """A token's query heads (192 wide, their rotary parts last), c and k_rope beside each other, the
+    queries rotated in place: no element of one is another's, whichever comes first."""
+    heads, both = 192 * H, d_latent + 64
+    width, at_q, at_c = heads + both, (both if first == "latent" else 0), (heads if first == "queries" else 0)
+    where = lambda i: AT + 2 * i  # noqa: E731
+    q = FaRows(where(at_q + 128), 0, 192, width)
+    x, k = FaRows(where(at_c), 0, 0, width), FaRows(where(at_c + d_latent), 0, 0, width)
+    c = latent(d_latent=d_latent, token_stride=both, page_stride=16 * both)
+    assert past_checks(append(lib, H=H, q=q, y=q, x=x, k=k, c=c))
+    assert past_checks(append(lib, H=H, q=q, y=q, x=x, k=k, c=c, total=1))
+    # into the queries' place from another buffer
+    assert past_checks(append(lib, H=H, q=FaRows(AT + 8 * FAR, 0, 64, 64 * H), y=q, x=x, k=k, c=c))
+    # but not over the latent's first or last elements, nor where the strides differ
+    for off in (8 - d_latent, 56):
+        over = FaRows(where(at_q + 128 + 192 * (H - 1) + off), 0, 0, width)
+        assert append(lib, H=H, q=q, y=q, x=over, k=FaRows(AT + 4 * FAR, 0, 0, width), c=c) == INVALID
+    assert append(lib, H=H, q=q, y=q, x=FaRows(where(at_c), 0, 0, width + 8), k=k, c=c) == INVALID
+
+
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(lse=None), dict(w=None), dict(table=None), dict(cu=None), dict(lens=None),
     dict(B=0), dict(H=0), dict(H=5), dict(total=-1), dict(pages=-1), dict(scale=-1.0), dict(scale=math.nan),

@@ -355,6 +355,29 @@ def test_append_in_place_and_without_queries():
     assert torch.equal(data[0], data[1]) and torch.equal(data[0], data[2])
 
 
+@pytest.mark.parametrize("first", ["queries", "latent"])
+@pytest.mark.parametrize("dl,H", [(512, 5), (128, 20)])
+def test_append_from_one_projection_in_place(dl, H, first):
+    """[query heads | c | k_rope] of a token in one buffer, the queries rotated where they are: as with a
+    buffer for each, and the other columns stay."""
+    rope, _, _ = rope_handle(dl, 64, "half", torch.bfloat16, True)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    one = torch.randn(23, 192 * H + dl + DR, generator=g, device=DEV).to(torch.bfloat16)
+    cut = [192 * H, dl, DR] if first == "queries" else [dl, DR, 192 * H]
+    parts = one.split(cut, 1)
+    q, c, k = parts if first == "queries" else (parts[2], parts[0], parts[1])
+    q = q.unflatten(1, (H, 192))
+    want, out = one.clone(), torch.empty(23, H, DR, dtype=one.dtype, device=DEV)
+    data = [torch.zeros(4, 8, dl + DR, dtype=one.dtype, device=DEV) for _ in range(2)]
+    args = i32([[3, 1, 0, 2]]), i32([0, 23]), i32([30]), rope
+    fa.fa_latent_append(q[..., 128:].contiguous(), c.contiguous(), k.contiguous(), out, fa.LatentCache(data[0], dl), *args)
+    wq = want.split(cut, 1)[0 if first == "queries" else 2].unflatten(1, (H, 192))
+    wq[..., 128:] = out
+    fa.fa_latent_append(q[..., 128:], c, k, q[..., 128:], fa.LatentCache(data[1], dl), *args)
+    assert fa.fa_sync_status() == fa.FA_OK
+    assert torch.equal(one, want) and torch.equal(data[0], data[1]) and not torch.equal(out, q.new_zeros(out.shape))
+
+
 def test_append_skips_pages_outside_the_cache():
     data = torch.zeros(3, 8, 192, dtype=torch.bfloat16, device=DEV)
     down = torch.ones(40, 192, dtype=torch.bfloat16, device=DEV)

@@ -20,11 +20,11 @@ using fa::rope::Rows;
 
 constexpr int64_t kLimit = int64_t{1} << 29;  // tokens, and heads of a call
 
-// One tensor of a call: its sizes, whether it is written, and the tensor it may be in
-// place of (an index into the list; -1: none).
+// One tensor of a call: its sizes (rows of d elements), whether it is written, and the tensor it
+// may be in place of (an index into the list; -1: none).
 struct Tensor {
     const fa_rows *r;
-    int64_t B, heads, N;
+    int64_t B, heads, N, d;
     bool written;
     int twin;
 };
@@ -32,34 +32,34 @@ struct Tensor {
 bool there(const fa_rows *r) { return r != nullptr && r->data != nullptr; }
 
 // Elements from the first to the last of a tensor, or 0 when that does not fit 2^60.
-int64_t extent(const Tensor &t, int64_t d) {
+int64_t extent(const Tensor &t) {
     const int64_t st[3] = {t.r->batch, t.r->head, t.r->token}, n[3] = {t.B, t.heads, t.N};
     double e = 0;
     for (int i = 0; i < 3; ++i)
         if (n[i] > 1) e += static_cast<double>(n[i] - 1) * static_cast<double>(st[i]);
     if (e > 1e18) return 0;
-    int64_t sum = d;
+    int64_t sum = t.d;
     for (int i = 0; i < 3; ++i)
         if (n[i] > 1) sum += (n[i] - 1) * st[i];
     return sum;
 }
 
 // Whether no two elements of a written tensor share a place.
-bool injective(const Tensor &t, int64_t d) {
+bool injective(const Tensor &t) {
     const int64_t n[3] = {t.B, t.heads, t.N}, st[3] = {t.r->batch, t.r->head, t.r->token};
-    return fa_host::span_apart(n, st, d) > 0;
+    return fa_host::span_apart(n, st, t.d) > 0;
 }
 
 // Slices of one fused buffer: equal strides of tokens and batch entries (those there are
 // more than one of), the larger a multiple of the smaller, s; each tensor's part of a
 // token is shorter than s, and the two parts lie at different places modulo s.
-bool interleaved(const Tensor &a, const Tensor &b, int64_t d) {
+bool interleaved(const Tensor &a, const Tensor &b) {
     if ((a.N > 1 && a.r->token != b.r->token) || (a.B > 1 && a.r->batch != b.r->batch)) return false;
     const int64_t token = a.N > 1 ? a.r->token : 0, batch = a.B > 1 ? a.r->batch : 0;
     const int64_t s = token > 0 && (batch == 0 || token < batch) ? token : batch;
     if (s < 1 || token % s != 0 || batch % s != 0) return false;
-    const int64_t span_a = a.heads > 1 ? (a.heads - 1) * a.r->head + d : d;
-    const int64_t span_b = b.heads > 1 ? (b.heads - 1) * b.r->head + d : d;
+    const int64_t span_a = a.heads > 1 ? (a.heads - 1) * a.r->head + a.d : a.d;
+    const int64_t span_b = b.heads > 1 ? (b.heads - 1) * b.r->head + b.d : b.d;
     const intptr_t bytes = reinterpret_cast<intptr_t>(b.r->data) - reinterpret_cast<intptr_t>(a.r->data);
     int64_t off = (bytes / 2) % s;
     if (off < 0) off += s;
@@ -68,7 +68,7 @@ bool interleaved(const Tensor &a, const Tensor &b, int64_t d) {
 
 // The descriptors of a call: alignment, strides, and what is written overlaps nothing
 // else (but the tensor it replaces, or its neighbours in a fused buffer).
-fa_status check_tensors(const Tensor *t, int count, int64_t d) {
+fa_status check_tensors(const Tensor *t, int count) {
     for (int i = 0; i < count; ++i) {
         if (!there(t[i].r)) continue;
         const fa_rows &r = *t[i].r;
@@ -77,32 +77,32 @@ fa_status check_tensors(const Tensor *t, int count, int64_t d) {
         for (int x = 0; x < 3; ++x)  // the stride of a single entry does not matter
             if (n[x] > 1 && (st[x] < 0 || st[x] % 8 != 0 || st[x] >= (int64_t{1} << 40)))
                 return FA_ERR_INVALID_ARG;
-        if (extent(t[i], d) == 0) return FA_ERR_UNSUPPORTED;
-        if (t[i].written && !injective(t[i], d)) return FA_ERR_INVALID_ARG;
+        if (extent(t[i]) == 0) return FA_ERR_UNSUPPORTED;
+        if (t[i].written && !injective(t[i])) return FA_ERR_INVALID_ARG;
     }
     for (int i = 0; i < count; ++i) {
         if (!there(t[i].r) || !t[i].written) continue;
         for (int j = 0; j < count; ++j) {
             if (j == i || !there(t[j].r) || (t[j].written && j < i)) continue;
             const fa_rows &a = *t[i].r, &b = *t[j].r;
-            if (!fa_host::overlaps(a.data, static_cast<size_t>(extent(t[i], d)) * 2, b.data,
-                                   static_cast<size_t>(extent(t[j], d)) * 2))
+            if (!fa_host::overlaps(a.data, static_cast<size_t>(extent(t[i])) * 2, b.data,
+                                   static_cast<size_t>(extent(t[j])) * 2))
                 continue;
             if (j == t[i].twin && a.data == b.data && (t[i].B == 1 || a.batch == b.batch) &&
                 (t[i].heads == 1 || a.head == b.head) && (t[i].N == 1 || a.token == b.token))
                 continue;
-            if (!interleaved(t[i], t[j], d)) return FA_ERR_INVALID_ARG;
+            if (!interleaved(t[i], t[j])) return FA_ERR_INVALID_ARG;
         }
     }
     return FA_OK;
 }
 
 // Buffers that are only read (small arrays) against every written tensor.
-bool hits_written(const void *p, size_t n, const Tensor *t, int count, int64_t d) {
+bool hits_written(const void *p, size_t n, const Tensor *t, int count) {
     if (p == nullptr || n == 0) return false;
     for (int i = 0; i < count; ++i)
         if (there(t[i].r) && t[i].written &&
-            fa_host::overlaps(p, n, t[i].r->data, static_cast<size_t>(extent(t[i], d)) * 2))
+            fa_host::overlaps(p, n, t[i].r->data, static_cast<size_t>(extent(t[i])) * 2))
             return true;
     return false;
 }
@@ -270,16 +270,16 @@ fa_status fa_qk_norm_rope(const fa_rows *q, const fa_rows *k, const fa_rows *q_o
     fa_status s = check_sizes(B, &H, &H_kv, N, d, dtype, q, k);
     if (s == FA_OK) s = check_rope(*rope, d);
     if (s != FA_OK) return s;
-    const Tensor t[] = {{q, B, H, N, false, -1}, {k, B, H_kv, N, false, -1},
-                        {q_out, B, H, N, true, 0}, {k_out, B, H_kv, N, true, 1}};
-    s = check_tensors(t, 4, d);
+    const Tensor t[] = {{q, B, H, N, d, false, -1}, {k, B, H_kv, N, d, false, -1},
+                        {q_out, B, H, N, d, true, 0}, {k_out, B, H_kv, N, d, true, 1}};
+    s = check_tensors(t, 4);
     if (s != FA_OK) return s;
     if (!fa_host::aligned4(positions)) return FA_ERR_INVALID_ARG;
     const size_t wbytes = static_cast<size_t>(d) * 2;
-    if (hits_written(positions, static_cast<size_t>(B * N) * 4, t, 4, d) ||
+    if (hits_written(positions, static_cast<size_t>(B * N) * 4, t, 4) ||
         hits_written(rope->rotary_dim > 0 ? rope->steps : nullptr,
-                     static_cast<size_t>(rope->rotary_dim) * 4, t, 4, d) ||
-        hits_written(rope->q_weight, wbytes, t, 4, d) || hits_written(rope->k_weight, wbytes, t, 4, d))
+                     static_cast<size_t>(rope->rotary_dim) * 4, t, 4) ||
+        hits_written(rope->q_weight, wbytes, t, 4) || hits_written(rope->k_weight, wbytes, t, 4))
         return FA_ERR_INVALID_ARG;
     int dev = 0;
     fa_host::DeviceInfo di;
@@ -331,10 +331,10 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
     if (wq != (dq_weight != nullptr) || wk != (dk_weight != nullptr)) return FA_ERR_INVALID_ARG;
     if ((wq && !there(q)) || (wk && !there(k))) return FA_ERR_INVALID_ARG;
     const fa_rows *xq = wq ? q : nullptr, *xk = wk ? k : nullptr;
-    const Tensor t[] = {{xq, B, H, N, false, -1}, {xk, B, H_kv, N, false, -1},
-                        {dq_out, B, H, N, false, -1}, {dk_out, B, H_kv, N, false, -1},
-                        {dq, B, H, N, true, 2}, {dk, B, H_kv, N, true, 3}};
-    s = check_tensors(t, 6, d);
+    const Tensor t[] = {{xq, B, H, N, d, false, -1}, {xk, B, H_kv, N, d, false, -1},
+                        {dq_out, B, H, N, d, false, -1}, {dk_out, B, H_kv, N, d, false, -1},
+                        {dq, B, H, N, d, true, 2}, {dk, B, H_kv, N, d, true, 3}};
+    s = check_tensors(t, 6);
     if (s != FA_OK) return s;
     if (!fa_host::aligned4(positions) || !fa_host::aligned4(dq_weight) || !fa_host::aligned4(dk_weight))
         return FA_ERR_INVALID_ARG;
@@ -354,7 +354,7 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
                  {dk_weight, gbytes, true},
                  {wq || wk ? workspace : nullptr, need, true}};
     for (int i = 0; i < 7; ++i) {
-        if (hits_written(small[i].p, small[i].n, t, 6, d)) return FA_ERR_INVALID_ARG;
+        if (hits_written(small[i].p, small[i].n, t, 6)) return FA_ERR_INVALID_ARG;
         if (!small[i].written || small[i].p == nullptr) continue;
         for (int j = 0; j < 7; ++j)
             if (j != i && small[j].p != nullptr &&
@@ -362,7 +362,7 @@ fa_status fa_qk_norm_rope_backward(const fa_rows *q, const fa_rows *k, const fa_
                 return FA_ERR_INVALID_ARG;
         for (const Tensor &x : t)
             if (there(x.r) && fa_host::overlaps(small[i].p, small[i].n, x.r->data,
-                                                static_cast<size_t>(extent(x, d)) * 2))
+                                                static_cast<size_t>(extent(x)) * 2))
                 return FA_ERR_INVALID_ARG;
     }
     int dev = 0;
@@ -429,9 +429,9 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
     if (total_q > kLimit || B > kLimit || H > (1 << 20) || max_pages > kLimit ||
         max_pages * cache->page_size > (int64_t{1} << 31))
         return FA_ERR_UNSUPPORTED;
-    const Tensor t[] = {{q, 1, H, total_q, false, -1}, {k, 1, H_kv, total_q, false, -1},
-                        {v, 1, H_kv, total_q, false, -1}, {q_out, 1, H, total_q, true, 0}};
-    s = check_tensors(t, 4, d);
+    const Tensor t[] = {{q, 1, H, total_q, d, false, -1}, {k, 1, H_kv, total_q, d, false, -1},
+                        {v, 1, H_kv, total_q, d, false, -1}, {q_out, 1, H, total_q, d, true, 0}};
+    s = check_tensors(t, 4);
     if (s != FA_OK) return s;
     // k and v of the cache may be interleaved with each other (as the caller lays them
     // out), but neither touches anything else
@@ -446,13 +446,13 @@ fa_status fa_paged_append(const fa_rows *q, const fa_rows *k, const fa_rows *v, 
                  {cu_seqlens_q, static_cast<size_t>(B + 1) * 4},
                  {seqlens_k, static_cast<size_t>(B) * 4}};
     for (const auto &x : small)
-        if (hits_written(x.p, x.n, t, 4, d)) return FA_ERR_INVALID_ARG;
+        if (hits_written(x.p, x.n, t, 4)) return FA_ERR_INVALID_ARG;
     for (const void *c : {cache->k, cache->v}) {
         for (const auto &x : small)
             if (x.p != nullptr && fa_host::overlaps(c, cache_bytes, x.p, x.n)) return FA_ERR_INVALID_ARG;
         for (const Tensor &x : t)
             if (there(x.r) && fa_host::overlaps(c, cache_bytes, x.r->data,
-                                                static_cast<size_t>(extent(x, d)) * 2))
+                                                static_cast<size_t>(extent(x)) * 2))
                 return FA_ERR_INVALID_ARG;
     }
     int dev = 0;
@@ -523,12 +523,9 @@ fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_row
     if (total_q > kLimit || B > kLimit || H > (1 << 20) || max_pages > kLimit ||
         max_pages * cache->page_size > (int64_t{1} << 31))
         return FA_ERR_UNSUPPORTED;
-    const Tensor t[] = {{q_rope, 1, H, total_q, false, -1}, {k_rope, 1, 1, total_q, false, -1},
-                        {q_out, 1, H, total_q, true, 0}};
-    s = check_tensors(t, 3, dr);
-    if (s != FA_OK) return s;
-    const Tensor latents[] = {{c, 1, 1, total_q, false, -1}};
-    s = check_tensors(latents, 1, dl);
+    const Tensor t[] = {{q_rope, 1, H, total_q, dr, false, -1}, {k_rope, 1, 1, total_q, dr, false, -1},
+                        {c, 1, 1, total_q, dl, false, -1}, {q_out, 1, H, total_q, dr, true, 0}};
+    s = check_tensors(t, 4);
     if (s != FA_OK) return s;
     const struct {
         const void *p;
@@ -537,15 +534,14 @@ fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_row
                  {r.k_weight, static_cast<size_t>(dl) * 2},
                  {max_pages > 0 ? block_table : nullptr, static_cast<size_t>(B * max_pages) * 4},
                  {cu_seqlens_q, static_cast<size_t>(B + 1) * 4},
-                 {seqlens_k, static_cast<size_t>(B) * 4},
-                 {c->data, static_cast<size_t>(extent(latents[0], dl)) * 2}};
+                 {seqlens_k, static_cast<size_t>(B) * 4}};
     for (const auto &x : small) {
-        if (hits_written(x.p, x.n, t, 3, dr)) return FA_ERR_INVALID_ARG;
+        if (hits_written(x.p, x.n, t, 4)) return FA_ERR_INVALID_ARG;
         if (x.p != nullptr && fa_host::overlaps(cache->data, cache_bytes, x.p, x.n)) return FA_ERR_INVALID_ARG;
     }
     for (const Tensor &x : t)
         if (there(x.r) &&
-            fa_host::overlaps(cache->data, cache_bytes, x.r->data, static_cast<size_t>(extent(x, dr)) * 2))
+            fa_host::overlaps(cache->data, cache_bytes, x.r->data, static_cast<size_t>(extent(x)) * 2))
             return FA_ERR_INVALID_ARG;
     int dev = 0;
     fa_host::DeviceInfo di;
