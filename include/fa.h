@@ -536,7 +536,8 @@ fa_status fa_latent_append(const fa_rows *q_rope, const fa_rows *c, const fa_row
  * and values W_v c per head. Q: total_q x H x (d_latent + d_rope), O: total_q x H x d_latent,
  * both contiguous and of the cache's dtype; LSE: total_q x H float32; any H >= 1. scale is that
  * of the heads as the model defines them. Positions, masks, tokens without keys or sequences,
- * what is not looked at, and NaN in rows that are: as for fa_forward_paged.
+ * what is not looked at, and NaN in rows that are: as for fa_forward_paged. Rows whose scores are all
+ * -infinity end as those without keys; a score of +infinity ends in NaN.
  *
  * Scores, softmax statistics and sums are float32. The weights exp(score - reference) are rounded
  * to the cache's dtype for their product with the rows; where a batch has at most 32 rows (tokens x

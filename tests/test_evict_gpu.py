@@ -189,6 +189,34 @@ def test_rows_of_lse_minus_infinity_add_nothing_whatever_they_hold(lens, H, Hk, 
     check_gather(b, 0.1, "causal", lse=lse)
 
 
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 40)], [(300, 900)]])
+def test_infinite_scores(lens):
+    """A key of +infinity in one column: for a finite LSE its weight is infinite if a query of its group
+    has the same sign there, else it adds 0; for an LSE of +infinity it is NaN, and other keys get 0."""
+    H, Hk, d = 8, 2, 64
+    b = paged(lens, H, Hk, d, torch.bfloat16, 16, seed=8)
+    q, cache, table, cu, seq_k, seqs = b
+    lse = lse_of(seqs, Hk, 0.1, "causal", (0, 0), q.shape[0])
+    q[..., 3] = -0.5
+    q[0, :4, 3] = 0.5  # the first K/V head's: a score of +infinity for the first token
+    L, at = lens[0][1], 100
+    cache.k[table[0, at // 16], at % 16, :, 3] = math.inf
+    weights = torch.zeros(cache.num_pages, Hk, 16, device=DEV)
+    gather(q, lse, weights, cache, table, cu, seq_k, 0.1, "causal")
+    got = weights[table[0, torch.arange(L, device=DEV) // 16].long(), :, torch.arange(L, device=DEV) % 16]
+    assert float(got[at, 0]) == math.inf and float(got[at, 1]) == 0
+    got[at] = 1
+    assert bool(torch.isfinite(got).all()) and bool((got > 0).all())
+    n = lens[0][0]
+    lse[:n, :4] = math.inf
+    weights.zero_()
+    gather(q, lse, weights, cache, table, cu, seq_k, 0.1, "causal")
+    got = weights[table[0, torch.arange(L, device=DEV) // 16].long(), :, torch.arange(L, device=DEV) % 16]
+    assert bool(got[at, 0].isnan()) and float(got[at, 1]) == 0
+    got[at, 0] = 0
+    assert bool((got[:, 0] == 0).all())
+
+
 def test_nan_of_another_sequence_and_of_a_key_stay_there():
     q, cache, table, cu, lens, seqs = paged([(1, 90), (1, 100), (3, 70)], 4, 2, 64, torch.bfloat16, 16, seed=2)
     scale = 0.125

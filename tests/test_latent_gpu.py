@@ -211,6 +211,68 @@ def test_nan_in_a_visible_row_is_seen():
     assert bool(torch.isfinite(o[1]).all()) and bool(torch.isfinite(lse[1]).all())
 
 
+def with_infinity(b, at):
+    """Key `at` (all keys: None) of the first sequence gets +infinity in a rotary column; which of its
+    (token, head) rows have a query of the same sign there: a score of +infinity, the others -infinity."""
+    q, cache, table, _, _, seqs = b
+    qq, rows = seqs[0]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    up = torch.rand(qq.shape[:2], generator=g, device=DEV) < 0.5
+    col = cache.d_latent + 8
+    qq[..., col] = torch.where(up, 0.5, -0.5).to(q.dtype)
+    q[:qq.shape[0]] = qq
+    rows[slice(None) if at is None else at, col] = math.inf
+    j = torch.arange(rows.shape[0], device=DEV)
+    cache.data[table[0, j // 16].long(), j % 16] = rows
+    return up
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lens,H", [([(1, 300), (1, 90)], 16), ([(1, 20000), (1, 90)], 16), ([(1, 300), (1, 90)], 32),
+                                    ([(1, 700), (1, 70)], 128)])
+@pytest.mark.parametrize("at", [0, 70, -1])
+def test_infinite_scores(at, lens, H, dtype):
+    """A score of +infinity ends in NaN, as exp(inf - inf) does; one of -infinity is a weight of 0."""
+    b = paged(lens, H, 512, dtype, 16, seed=H)
+    qq, rows = b[5][0]
+    up = with_infinity(b, at % lens[0][1])
+    o, lse = run(*b[:5], 0.06)
+    assert bool(o[0][up[0]].isnan().all()) and bool(lse[0][up[0]].isnan().all())
+    at %= lens[0][1]
+    others = torch.cat([rows[:at], rows[at + 1:]])[:, None]
+    want, bound, wl, lb = attention_ref(qq, others, others, 0.06, "none", (0, 0), dtype)
+    assert_within(o[0][~up[0]], want[0][~up[0]][:, :512], bound[0][~up[0]][:, :512], "O")
+    assert_within(lse[0][~up[0]], wl[0][~up[0]], lb[0][~up[0]], "LSE")
+    check(o[1:], lse[1:], b[5][1:], 0.06, "causal", (0, 0), dtype)
+
+
+@pytest.mark.parametrize("H", [1, 8])
+@pytest.mark.parametrize("at", [240, 299])
+def test_tokens_that_do_not_see_an_infinite_key_are_as_without_it(at, H):
+    """In a chunk: the tokens before it. (An infinity in the rotary part: no value.)"""
+    b = paged([(70, 300), (3, 40)], H, 256, torch.bfloat16, 16, seed=3)
+    qq, rows = b[5][0]
+    up = with_infinity(b, at)
+    o, lse = run(*b[:5], 0.06)
+    m = at - 230  # tokens at 230 .. at - 1
+    check(o[:m], lse[:m], [(qq[:m], rows[:at])], 0.06, "causal", (0, 0), torch.bfloat16)
+    assert torch.equal(lse[m:70].isnan(), up[m:])
+    check(o[70:], lse[70:], b[5][1:], 0.06, "causal", (0, 0), torch.bfloat16)
+
+
+@pytest.mark.parametrize("lens,H", [([(1, 300), (1, 90)], 16), ([(1, 20000), (1, 90)], 16), ([(1, 700), (1, 70)], 128),
+                                    ([(70, 300), (3, 40)], 4)])
+def test_rows_whose_scores_are_all_minus_infinity(lens, H):
+    """They end as rows that see no key do: 0 and -infinity."""
+    b = paged(lens, H, 512, torch.bfloat16, 16, seed=H)
+    up = with_infinity(b, None)
+    n = lens[0][0]
+    o, lse = run(*b[:5], 0.06)
+    assert bool((lse[:n][~up] == -math.inf).all()) and bool((o[:n][~up] == 0).all())
+    assert bool(lse[:n][up].isnan().all()) and bool(o[:n][up].isnan().all())
+    check(o[n:], lse[n:], b[5][1:], 0.06, "causal", (0, 0), torch.bfloat16)
+
+
 @pytest.mark.parametrize("H", [8, 128])
 def test_page_numbers_outside_the_cache_read_as_zeros(H):
     q, cache, table, cu, lens, seqs = paged([(1, 300), (1, 200)], H, 512, torch.bfloat16, 16, seed=4)
