@@ -20,8 +20,8 @@
 // S^T arrives with keys in lanes, 16 lanes of each warp's 32 (the layout of M = 64), and is
 // read as 16 x 256 bit fragments: a thread holds 2 keys of each of R / 4 rows. The weights
 // p = exp2(s scale log2 e - ref) go to shared memory through transposing 8 x 8 stores, as the
-// K-major B operand of the second product; blocks of up to 32 rows hand them over as two 16-bit parts,
-// each multiplied by itself into the same O^T. The reference of a row is lazy: it moves only
+// K-major B operand of the second product; blocks of up to 32 rows hand them over as two 16-bit parts
+// side by side, with columns of O^T for each that are added at the end. The reference of a row is lazy: it moves only
 // when a score passes it by 2^8, so a tile costs the four warps one barrier with a vote and
 // no row maximum; when it does move, the row's l and its column of O^T are rescaled.
 //
@@ -114,11 +114,12 @@ struct Smem {
     static constexpr int kQBytes = kRegions * kQRegion;
     // 16-bit parts of a weight in its product with the values, and the bytes of one part and of a buffer
     // of all. One alone puts O's error at 0.0021 where its own rounding is 0.0017 (bf16, relative,
-    // root mean square). With up to 32 rows, where tiles wait for memory, the second part costs little (8
-    // sequences of 32768 rows 61 -> 63 us, 96 ragged ones 24.2 -> 24.9). With 64 the products are the bound (at DL
-    // = 256 1000 tokens of 16 heads on 14000 rows 336 -> 400 us, 40 sequences with 128 heads 39.6 ->
-    // 44.0), and at DL = 512 shared memory has no place for it: there weights are rounded, as in the
-    // forward passes over whole sequences.
+    // root mean square). With up to 32 rows a second part costs little as R further columns of the same
+    // products (8 sequences of 32768 rows 60.4 -> 61.1 us, 96 ragged ones 24.1 -> 24.5; as products of
+    // its own 62.9 and 24.9). With 64 the products are the bound (at DL = 256 1000 tokens of 16 heads on
+    // 14000 rows 335 -> 374 us, 40 sequences with 128 heads 39.9 -> 42.6), and at DL = 512 neither
+    // shared nor tensor memory has a place for it: there weights are rounded, as in the forward passes over
+    // whole sequences.
     static constexpr int kPParts = R <= 32 ? 2 : 1;
     static constexpr int kPPart = R * 128;
     static constexpr int kPBytes = kPParts * kPPart;
@@ -126,7 +127,7 @@ struct Smem {
     static constexpr int kMost = 227 * 1024 - kSmall;
     // two Q tiles (the next block's scores start while this one ends) and two buffers of weights
     // where two key tiles leave room for them, else two of weights where they do (16 sequences of 0-16000
-    // rows, 20 heads, DL 512: 24.0 us, with two Q tiles in their place 25.4); the rest is for key tiles
+    // rows, 20 heads, DL 512: 23.7 us, with two Q tiles in their place 25.0); the rest is for key tiles
     static constexpr int kQStages = 2 * kQBytes + 2 * kTile + 2 * kPBytes <= kMost ? 2 : 1;
     static constexpr int kPBufs = kQStages * kQBytes + 2 * kTile + 2 * kPBytes <= kMost ? 2 : 1;
     static constexpr int kFit = (kMost - kQStages * kQBytes - kPBufs * kPBytes) / kTile;
@@ -150,7 +151,8 @@ struct Smem {
     // TMEM columns) per SM
     static constexpr int kAlloc = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static constexpr uint32_t kTmemO = 0;
-    static constexpr uint32_t kTmemS = DL / 128 * R;
+    static constexpr int kOCols = kPParts * R;  // of a slice of O^T: for each part of the weights the rows
+    static constexpr uint32_t kTmemS = DL / 128 * kOCols;
     static_assert(kTmemS + 2 * R <= kTmemCols, "TMEM columns");
 };
 
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================================================================ issuers of the products
         const bool scores = warp == kScoreWarp;
         constexpr uint32_t idesc_s = idesc_f16_ab(BF16, kBK, R, false, false);
-        constexpr uint32_t idesc_o = idesc_f16_ab(BF16, 128, R, true, false);
+        constexpr uint32_t idesc_o = idesc_f16_ab(BF16, 128, L::kOCols, true, false);
         // a value that all lanes have, from one of them: the compiler then keeps what follows from
         // it in uniform registers, which the products take their descriptors from
         auto one = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
@@ -740,12 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < kBK / 16; ++c)
                                 if (c >= c0 && c <= c1)
-#pragma unroll
-                                    for (int y = 0; y < L::kPParts; ++y)
-                                        umma_f16_ss(kTmem + L::kTmemO + s * R,
-                                                    da + s * (L::kPart >> 4) + c * ((2 * L::kGroup) >> 4),
-                                                    db + y * (L::kPPart >> 4) + c * 2, idesc_o,
-                                                    x > 0 || c > c0 || y > 0 ? 1u : 0u);
+                                    umma_f16_ss(kTmem + L::kTmemO + s * L::kOCols,
+                                                da + s * (L::kPart >> 4) + c * ((2 * L::kGroup) >> 4), db + c * 2,
+                                                idesc_o, x > 0 || c > c0 ? 1u : 0u);
                             umma_commit(bar(kBarKEmpty + st + s));
                         }
                         umma_commit(bar(kBarPVDone + t % 2));
@@ -897,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (x0 > 0) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < DL / 128 * R; c += 16) {
+                        for (int c = 0; c < DL / 128 * L::kOCols; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tl + L::kTmemO + c, o);
 #pragma unroll
@@ -980,11 +979,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int part = x * kAtOnce / R, r0 = x * kAtOnce % R, left = P.rows - r0;
                 if (left <= 0) continue;
                 uint32_t o[kAtOnce];
-                if constexpr (kAtOnce == 32) {
-                    tmem_ld32(tl + L::kTmemO + x * kAtOnce, o);
-                    tmem_ld_wait(o);
-                } else {
-                    tmem_ld16(tl + L::kTmemO + x * kAtOnce, o);
+                auto columns = [&](int at, uint32_t(&o)[kAtOnce]) {
+                    if constexpr (kAtOnce == 32) {
+                        tmem_ld32(tl + L::kTmemO + at, o);
+                        tmem_ld_wait(o);
+                    } else {
+                        tmem_ld16(tl + L::kTmemO + at, o);
+                    }
+                };
+                columns(part * L::kOCols + r0, o);
+                if constexpr (L::kPParts == 2) {
+                    uint32_t more[kAtOnce];
+                    columns(part * L::kOCols + R + r0, more);
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(more[e]));
                 }
                 float y[kAtOnce];
                 // a row without keys: 0, whatever its column holds
