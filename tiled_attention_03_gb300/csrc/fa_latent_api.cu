@@ -94,10 +94,10 @@ fa_status run(const void *Q, void *O, float *LSE, const fa_latent_cache *cache, 
         total_q * H > (int64_t{1} << 30))
         return FA_ERR_UNSUPPORTED;
     // Rows of a CTA's block: as many as a sequence has on average, 16, 32 or 64 (at each: 4 short
-    // sequences of 16 rows 16.5, 17.3 and 17.9 us; 8 of 32768 keys and 32 rows 100, 61 and 64; 40 with
-    // 128 rows 124, 77 and 59); with more than
-    // one and a half blocks of 64, two CTAs side by side (40 sequences with 128 rows 59.0 us, with
-    // single CTAs 60.0; one of 16000 rows 461 and 463).
+    // sequences of 16 rows 10.8, 10.8 and 12.2 us; 8 of 32768 keys and 32 rows 98, 61 and 63; 40 with
+    // 128 rows 116, 74 and 53); with more than one and a half blocks of 64, two CTAs side by side (40
+    // sequences with 128 rows 53.3 us, with single CTAs 55.3; one of 16000 rows 456 either way; 8 of
+    // 32768 keys and 32 rows, where the second CTA has none, 61 alone and 92 in pairs).
     const int64_t all_rows = total_q * H;
     const int r = all_rows <= 16 * B ? 16 : all_rows <= 32 * B ? 32 : 64;
     const int group = all_rows > 96 * B ? 2 : 1;

@@ -11,7 +11,7 @@
 // Both products are taken transposed, S^T = K Q^T (64 keys x R rows) and O^T += V^T P^T
 // (DL x R in slices of 128), because O of 128 rows and 512 columns would fill tensor memory
 // by itself and leave no columns for S: with R <= 64 rows as the N of both products O^T takes
-// DL / 128 * R columns. A tile of 64 keys comes into shared memory once, by TMA from the
+// DL / 128 * R columns (twice that for R <= 32, see below). A tile of 64 keys comes into shared memory once, by TMA from the
 // pages, and is the K-major A operand of the first product and, read with its latent columns as
 // M, the MN-major A operand of the second. It comes and goes in parts of 128 columns (the last
 // with the rotary ones), each with its own barriers: the scores start on the first part, and
@@ -31,11 +31,12 @@
 // CTAs that take the same tiles for R rows each, side by side, so that with more rows than R the
 // second reads them from L2.
 //
-// What bounds it: a tile of 64 keys at DL = 512 is 74 KB, which this SM's share of HBM delivers in
-// about 3,100 cycles: with one block per sequence, memory (8 sequences of 32768 rows, 32 heads: 61
-// us, 5.0 TB/s, of which 10 are the start, the last output and the merge). With more blocks the
-// products, 36 of M = 64 and 16 of M = 128 at 33 and 49 cycles at least, 1,970 of a tile's 2,300
-// cycles (1000 tokens of 16 heads on 14000 rows: 456 us, 1,110 TFLOP/s; 447 without any key loads).
+// What bounds it: with one block per sequence the chain of a tile, scores, softmax and product, as
+// two tiles of 74 KB are all that shared memory holds at DL = 512: 8 sequences of 32768 rows, 32 heads, take
+// 61 us, 5.0 TB/s, of which 13.5 are the start, the last output and the merge, and take 59 to 65
+// without any key loads. With more blocks the products, 36 of M = 64 and 16 of M = 128 at 33 and 49 cycles at
+// least, 1,970 of a tile's 2,300 cycles (1000 tokens of 16 heads on 14000 rows: 456 us, 1,110
+// TFLOP/s; 433 without any key loads).
 //
 // Warps (256 threads): 0-3 softmax and outputs, 4 key tiles, 5 issuer of S^T, 6 issuer of
 // O^T, 7 scheduler and Q tiles. What the issuers' branches and descriptors come from is taken
@@ -61,8 +62,8 @@ constexpr int kBK = 64;     // keys per tile
 constexpr int kDR = 64;     // rotary elements of a row
 constexpr int kThreads = 256;
 constexpr int kLoadWarp = 4, kScoreWarp = 5, kOutWarp = 6, kPlanWarp = 7;
-// A block's start and end, in tiles (at 3, 4, 6 and 8: 40 sequences of 0-16000 rows with 128 heads 54.6,
-// 54.0, 55.8 and 55.6 us, 96 of 0-12000 with 12 heads at DL 256 24.4, 24.8, 26.4 and 27.1).
+// A block's start and end, in tiles (at 3, 4 and 6: 40 sequences of 0-16000 rows with 128 heads 53.3,
+// 53.7 and 55.1 us, 96 of 0-12000 with 12 heads at DL 256 24.8, 25.2 and 26.9).
 constexpr int kTicks = 3;
 constexpr int kUnitSlots = 4;
 constexpr int kUnitConsumers = 7;  // warps that take the pieces: all but the scheduler
@@ -972,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t at0 = row0 * DL + warp * 32 + lane;
             constexpr int kParts = L::kParts;
             // 32 rows (or R) of a slice of O^T at a time (with the next ones asked for ahead the code is
-            // twice as long: 54 -> 58 us at 128 heads)
+            // twice as long, 8 % slower at 128 heads)
             constexpr int kAtOnce = R < 32 ? R : 32, kSteps = R / kAtOnce * kParts;
 #pragma unroll 1
             for (int x = 0; x < kSteps; ++x) {

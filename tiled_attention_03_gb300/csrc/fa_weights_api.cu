@@ -80,8 +80,8 @@ extern "C" fa_status fa_paged_weights(const void *Q, const float *LSE, float *we
         return FA_ERR_UNSUPPORTED;
     // Rows of a tile: a sequence's on average (new tokens x query heads of a K/V head), 16, 64 or
     // 128; of them the heads of a group, or a divisor of them, for as many tokens as fit. (With 16,
-    // 64 and 128: 8 sequences of 32768 keys and 4 rows 90, 103 and 171 us; 16 of 6000 to 9000 keys
-    // and 40 rows 45, 28 and 37 us; 4096 rows of one sequence 187 with 64, 115 with 128.)
+    // 64 and 128: 8 sequences of 32768 keys and 4 rows 88, 96 and 158 us; 16 of 6000 to 9000 keys
+    // and 40 rows 35, 27 and 33; 8192 rows of one sequence 187 with 64, 118 with 128.)
     const int64_t group = H / H_kv, all_rows = total_q * group;
     int rows = all_rows <= 16 * B ? 16 : all_rows <= 64 * B ? 64 : most_rows(d);
     int64_t pf = group < rows ? group : rows;

@@ -22,13 +22,13 @@
 // instructions that are fetched anew (lanes that wait for a barrier each, and units handed out 32 at a
 // time, made both slower, by 2 and 8 %). Chunks: a tile of 128 x 128 scores takes about 1,150 cycles, of which
 // the products take 528 and the exponentials as long; computing some of those by multiply-adds made it
-// slower (10 of 32: 115 -> 130 us), as the sums wait for tensor memory and for each other more than for a pipe.
+// slower (10 of 32: by 13 %), as the sums wait for tensor memory and for each other more than for a pipe.
 //
 // Warps (640 threads): 0-15 are four teams of four that sum every fourth tile of rows (of units with
 // one: every fourth unit), as one team's loads from tensor memory and exponentials wait for each
 // other; 16 finds units, 32 at a time, 17 issues the products, 18 loads queries and their LSE, 19 loads
 // keys; the loaders ask for page numbers one tile ahead, and for LSEs one or, where units have many tiles,
-// three (2048 tokens on 6000 keys: 128 us with one, 116 with three).
+// three (2048 tokens on 6000 keys: 126 us with one, 118 with three).
 // Every wait is bounded; on expiry the CTA records the failure, drains its copies and
 // products, frees its tensor memory and returns.
 #pragma once
@@ -45,9 +45,9 @@ namespace fa {
 namespace weights {
 
 // Keys of a tile: 128, or 256 (two products, one behind the other) for narrow tiles of rows, where what
-// a unit costs besides its products is most of it (8 sequences of 32768 keys 87.7 us, with 128 89.3;
-// 100 of 0-12000 at d = 64 20.7 and 25.4; with tiles of 64 rows 128 are better, 16 sequences of
-// 6000-9000 keys and 40 rows 28 and 32).
+// a unit costs besides its products is most of it (8 sequences of 32768 keys 88.4 us, with 128 88.7;
+// 100 of 0-12000 at d = 64 20.4 and 25.0; with tiles of 64 rows 128 are better, 16 sequences of
+// 6000-9000 keys and 40 rows 27.1 and 29.6).
 constexpr int tile_keys(int d, int rows) { return rows == 16 && d <= 128 ? 256 : 128; }
 constexpr int kTeams = 4;
 constexpr int kThreads = (4 * kTeams + 4) * 32;
