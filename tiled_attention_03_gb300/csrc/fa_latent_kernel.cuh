@@ -117,10 +117,11 @@ struct Smem {
     // of all. One alone puts O's error at 0.0021 where its own rounding is 0.0017 (bf16, relative,
     // root mean square). With up to 32 rows a second part costs little as R further columns of the same
     // products (8 sequences of 32768 rows 60.4 -> 61.1 us, 96 ragged ones 24.1 -> 24.5; as products of
-    // its own 62.9 and 24.9). With 64 the products are the bound (at DL = 256 1000 tokens of 16 heads on
-    // 14000 rows 335 -> 374 us, 40 sequences with 128 heads 39.9 -> 42.6), and at DL = 512 neither
-    // shared nor tensor memory has a place for it: there weights are rounded, as in the forward passes over
-    // whole sequences.
+    // its own 62.9 and 24.9). With 64 the products are the bound: at DL = 256 1000 tokens of 16 heads on
+    // 14000 rows 335 -> 374 us, 40 sequences with 128 heads 39.9 -> 42.6; at DL = 512, where tensor memory
+    // has no columns for it, a product of its own from the place of the tile's rotary part (which the
+    // scores have used by then) 456 -> 614 and 53 -> 60. There weights are rounded, as in the forward
+    // passes over whole sequences.
     static constexpr int kPParts = R <= 32 ? 2 : 1;
     static constexpr int kPPart = R * 128;
     static constexpr int kPBytes = kPParts * kPPart;
